@@ -413,6 +413,44 @@ MOE_API moe_status_t moe_set_gemm_tiles(int32_t mode, int32_t* previous);
 MOE_API moe_status_t moe_expert_utilization(const int32_t* stats, int32_t E, int64_t* counts, float* utilization,
                                             moe_stream_t stream);
 
+/* The router's auxiliary training losses and their gradient to the logits.
+ * The pages train without one ("Routing: top-2 without auxiliary loss") and
+ * watch the balance instead ("Training dynamics: expert specialization"); a
+ * feature list on "Let Grok spill the beans on Grok" names a balancing loss
+ * without a formula.  The formula here: token t is live when its mask byte is
+ * not 0 and it lies in a sequence s = [seq_offsets[s], seq_offsets[s + 1]);
+ * with n_s live tokens in s, N in all, p_t = softmax of logits[t, :] and
+ * lse_t = log sum_e exp(logits[t, e]):
+ *   counts[s, e] = assignments of the live tokens of s to expert e
+ *   f[s, e]      = counts[s, e] / (2 n_s)
+ *   balance      = E / N * sum over live t of sum_e f[s(t), e] p[t, e]
+ *   z            = 1 / N * sum over live t of lse_t^2
+ *   loss[0..2]   = balance_coef * balance + z_coef * z, balance, z
+ *   dlogits      = d loss[0] / d logits, the counts held fixed
+ * (one sequence of balanced tokens gives balance = 1).  Rows that are not live
+ * are not read and get dlogits 0; every row of dlogits is written.  With no
+ * live token loss and dlogits are 0.  A live row whose logits hold a NaN or
+ * +inf makes loss and its own dlogits row NaN; -inf logits are experts of
+ * probability 0.
+ * logits [T, E] fp32, topk_idx [T, 2] as moe_router_topk writes them;
+ * token_mask [T] bytes or NULL (all live); seq_offsets [n_seq + 1] int32,
+ * non-decreasing within [0, T] (empty sequences allowed, tokens before the
+ * first and behind the last are not live), or NULL with n_seq = 1: one
+ * sequence of T tokens; counts [n_seq, E] int32; loss [3] fp32; dlogits [T, E]
+ * fp32 or NULL.  All on the device.  1 <= n_seq <= MOE_BALANCE_MAX_SEQS and
+ * finite coefficients, else MOE_ERR_INVALID_ARG.  Offsets that decrease or
+ * leave [0, T] set MOE_DEVERR_OFFSETS (the outputs are then unspecified); an
+ * index outside [0, E) sets MOE_DEVERR_EXPERT_INDEX and is not counted.
+ * Sums have a fixed order: results do not depend on scheduling.  T == 0 writes
+ * zeros.  ws: moe_balance_loss_workspace_size bytes of scratch, used by one
+ * call at a time. */
+#define MOE_BALANCE_MAX_SEQS (1 << 24)
+MOE_API size_t moe_balance_loss_workspace_size(const moe_config_t* cfg, int32_t n_seq);
+MOE_API moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logits, const int32_t* topk_idx,
+                                      const uint8_t* token_mask, const int32_t* seq_offsets, int32_t n_seq,
+                                      float balance_coef, float z_coef, int32_t* counts, float* loss, float* dlogits,
+                                      void* ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Phase timing of the training pair, for measurement; the pages have no
  * counterpart.  While enabled (moe_profile_phases(1), a process-wide setting),
  * moe_layer_forward_train and moe_layer_backward record a pair of CUDA events

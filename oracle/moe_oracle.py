@@ -488,3 +488,46 @@ def expert_utilization(counts, num_experts: int = 8, top_k: int = 2) -> np.ndarr
     c = np.asarray(counts, dtype=np.float64)
     n_tokens = c.sum() / top_k
     return c / n_tokens * num_experts / top_k
+
+
+# ----------------------------------------------------------------------------
+# auxiliary losses of the router
+# ----------------------------------------------------------------------------
+def balance_loss(logits, idx, mask=None, seq_offsets=None, balance_coef=0.01, z_coef=0.0):
+    """Balance loss and z-loss over ragged sequences, one token after the other.
+
+    A token is live when its mask is set and it lies in a sequence [offsets[s],
+    offsets[s + 1]).  With n_s live tokens in s, N in all, p = softmax(logits_t):
+      counts[s, e] = live assignments to e,  f = counts / (2 n_s)
+      balance = E / N sum_t sum_e f[s(t), e] p[t, e],  z = 1 / N sum_t lse_t^2
+    and the gradient of balance_coef * balance + z_coef * z with f held fixed.
+    Returns (loss [3], counts [n_seq, E] int64, dlogits [T, E]), float64.
+    """
+    lg = np.asarray(logits, dtype=np.float64)
+    T, E = lg.shape
+    off = [0, T] if seq_offsets is None else [int(v) for v in seq_offsets]
+    n_seq = len(off) - 1
+    counts = np.zeros((n_seq, E), dtype=np.int64)
+    members = []
+    for s in range(n_seq):
+        live = [t for t in range(off[s], off[s + 1]) if mask is None or mask[t]]
+        members.append(live)
+        for t in live:
+            for e in idx[t]:
+                counts[s, e] += 1
+    n = sum(len(m) for m in members)
+    balance = z = 0.0
+    dl = np.zeros((T, E))
+    for s, live in enumerate(members):
+        if not live:
+            continue
+        f = counts[s] / (2.0 * len(live))
+        for t in live:
+            top = np.max(lg[t])
+            ex = np.exp(lg[t] - top)
+            p = ex / ex.sum()
+            lse = top + math.log(ex.sum())
+            balance += E * float(f @ p) / n
+            z += lse * lse / n
+            dl[t] = p * (balance_coef * E / n * (f - float(f @ p)) + 2.0 * z_coef / n * lse)
+    return np.array([balance_coef * balance + z_coef * z, balance, z]), counts, dl

@@ -27,6 +27,7 @@ __all__ = [
     "workspace_size_train", "layer_forward_train", "layer_backward", "route_counts", "dispatch_shard", "gather_rows",
     "EP_MAX_WORLD", "EpPeers", "ep_dispatch_peers", "ep_expert_ffn_peers", "ep_combine_peers", "peer_export",
     "peer_import", "peer_release",
+    "balance_loss_workspace_size", "balance_loss",
     "GEMM_TILES", "set_gemm_tiles", "gemm_tiles", "PHASES", "profile_phases", "profile_read",
 ]
 
@@ -112,6 +113,9 @@ def _load():
         "moe_expert_ffn_w8": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "moe_layer_forward_w8": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "moe_expert_utilization": ([P, ctypes.c_int32, P, P, P], ctypes.c_int),
+        "moe_balance_loss_workspace_size": ([cfgp, ctypes.c_int32], sz),
+        "moe_balance_loss": ([cfgp, P, P, P, P, ctypes.c_int32, ctypes.c_float, ctypes.c_float, P, P, P, P, sz, P],
+                             ctypes.c_int),
         "moe_profile_phases": ([ctypes.c_int32], ctypes.c_int),
         "moe_profile_read": ([P, P, ctypes.c_int32], ctypes.c_int),
         "moe_ep_dispatch_peers": ([cfgp, ctypes.POINTER(_CEpPeers), P, P, P, P, P, P, P], ctypes.c_int),
@@ -212,6 +216,13 @@ def _expect_layer(cfg, x=None, w_router=None, w_gate=None, w_up=None, w_down=Non
 
 def _empty(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _same_device(first, *others):
+    """Tensors of one call live on one CUDA device (None is allowed among the others)."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device} in one call")
 
 
 def abi_version() -> int:
@@ -572,6 +583,50 @@ def quantize_int8(cfg: Config, w, q=None, scale=None, stream=None):
     _check(lib.moe_quantize_int8(cfg.ref, _dev_ptr(w), K, N, _dev_ptr(q), _dev_ptr(scale), _stream(stream, w.device)),
            "moe_quantize_int8")
     return q, scale
+
+
+def balance_loss_workspace_size(cfg: Config, n_seq: int = 1) -> int:
+    return lib.moe_balance_loss_workspace_size(cfg.ref, int(n_seq))
+
+
+def balance_loss(cfg: Config, logits, topk_idx, token_mask=None, seq_offsets=None, balance_coef: float = 0.01,
+                 z_coef: float = 0.0, want_grad: bool = True, out=None, ws=None, stream=None):
+    """Balance loss and z-loss of the router, per-sequence expert counts and the gradient to the logits
+    (``moe_balance_loss``).  logits [T, E] fp32 and topk_idx [T, 2] as router_topk returns them; token_mask [T]
+    (bool or uint8, 0 = padding) and seq_offsets [n_seq + 1] (int32) may be None.  Returns a dict of loss [3]
+    (the weighted sum, the balance loss, the z-loss), counts [n_seq, E] and dlogits [T, E] (None without
+    want_grad); dlogits goes into layer_backward or layer_backward_c8."""
+    _expect("logits", logits, cfg.T * cfg.E, torch.float32)
+    _expect("topk_idx", topk_idx, cfg.T * cfg.top_k, torch.int32)
+    if token_mask is not None:
+        if token_mask.dtype == torch.bool:
+            token_mask = token_mask.view(torch.uint8)
+        _expect("token_mask", token_mask, cfg.T, torch.uint8)
+    n_seq = 1
+    if seq_offsets is not None:
+        n_seq = seq_offsets.numel() - 1
+        if seq_offsets.dtype != torch.int32 or n_seq < 1:
+            raise ValueError("seq_offsets must be int32 with at least two entries")
+    o = dict(out or {})
+    o.setdefault("loss", _empty((3,), torch.float32, logits))
+    o.setdefault("counts", _empty((n_seq, cfg.E), torch.int32, logits))
+    if want_grad:
+        o.setdefault("dlogits", _empty((cfg.T, cfg.E), torch.float32, logits))
+    else:
+        o["dlogits"] = None
+    _expect("loss", o["loss"], 3, torch.float32)
+    _expect("counts", o["counts"], n_seq * cfg.E, torch.int32)
+    _expect("dlogits", o["dlogits"], cfg.T * cfg.E, torch.float32)
+    if ws is None:
+        ws = _empty((max(balance_loss_workspace_size(cfg, n_seq), 1),), torch.uint8, logits)
+    _same_device(logits, topk_idx, token_mask, seq_offsets, ws, *o.values())
+    with torch.cuda.device(logits.device):
+        _check(lib.moe_balance_loss(cfg.ref, _dev_ptr(logits), _dev_ptr(topk_idx), _dev_ptr(token_mask),
+                                    _dev_ptr(seq_offsets), n_seq, float(balance_coef), float(z_coef),
+                                    _dev_ptr(o["counts"]), _dev_ptr(o["loss"]), _dev_ptr(o["dlogits"]), _dev_ptr(ws),
+                                    ws.numel() * ws.element_size(), _stream(stream, logits.device)),
+               "moe_balance_loss")
+    return o
 
 
 class QuantizedExperts:

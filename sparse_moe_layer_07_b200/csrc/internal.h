@@ -177,6 +177,13 @@ cudaError_t launch_wait_check(int64_t limit_ns, cudaStream_t s, const Ctx& ctx);
 // counts[e] += stats[e] and utilization[e] = counts[e] * E / sum(counts) (one block).
 cudaError_t launch_utilization(const int32_t* stats, int E, int64_t* counts, float* util, cudaStream_t s);
 
+// Balance loss, z-loss, per-sequence counts and the gradient to the logits
+// (ws: balance_slot_bytes bytes).
+int64_t balance_slot_bytes(int64_t T, int64_t n_seq);
+cudaError_t launch_balance(const moe_config_t& c, const float* logits, const int32_t* idx, const uint8_t* mask,
+                           const int32_t* seq, int32_t n_seq, float coef_a, float coef_b, int32_t* counts, float* loss,
+                           float* dlogits, void* ws, cudaStream_t s, const Ctx& ctx);
+
 // Argument check shared by the entry points (MOE_OK when the config is usable).
 moe_status_t validate_config(const moe_config_t* cfg);
 // Device facts of the current device (cached per device).

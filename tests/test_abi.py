@@ -313,3 +313,39 @@ def test_peer_entry_points_check_arguments_before_any_cuda_call():
         assert call(EpPeers(3, 0, good + [good[0]])) == 2  # 3 ranks do not divide E = 8
         assert call(EpPeers(2, 0, good), Config(512, 256, 384, dtype="f32")) == 2
         assert call(EpPeers(2, 0, good), Config(512, 128, 384)) == 2  # d not a multiple of 256
+
+
+def test_balance_loss_arguments_checked_before_launch(moe):
+    P = ctypes.c_void_p
+    c = _cfg(moe, T=64)
+    p, odd = P(256), P(260)  # never dereferenced
+    n = moe.balance_loss_workspace_size(c, 3)
+    assert n > 0 and moe.balance_loss_workspace_size(c, 0) == 0
+    assert moe.balance_loss_workspace_size(c, (1 << 24) + 1) == 0
+    assert moe.balance_loss_workspace_size(_cfg(moe, E=4), 1) == 0
+
+    def call(cfg=c, lg=p, idx=p, mask=None, seq=p, n_seq=3, a=0.1, b=0.1, counts=p, loss=p, dl=p, ws=p, size=n):
+        return moe.STATUS[moe.lib.moe_balance_loss(cfg.ref, lg, idx, mask, seq, n_seq, a, b, counts, loss, dl, ws, size,
+                                                   None)]
+
+    bad = "MOE_ERR_INVALID_ARG"
+    assert call(lg=None) == bad and call(idx=None) == bad and call(counts=None) == bad and call(loss=None) == bad
+    assert call(lg=odd) == bad and call(dl=odd) == bad and call(ws=odd) == bad and call(seq=P(258)) == bad
+    assert call(n_seq=0) == bad and call(seq=None) == bad and call(a=math.nan) == bad and call(b=math.inf) == bad
+    assert call(size=n - 1) == "MOE_ERR_WORKSPACE" and call(ws=None) == "MOE_ERR_WORKSPACE"
+    assert call(cfg=_cfg(moe, top_k=1)) == "MOE_ERR_UNSUPPORTED"
+
+
+def test_balance_loss_binding_checks(moe):
+    import torch
+
+    c = _cfg(moe, T=4)
+    lg, idx = torch.zeros((4, 8)), torch.zeros((4, 2), dtype=torch.int32)
+    with pytest.raises(ValueError, match="logits must"):
+        moe.balance_loss(c, lg.double(), idx)
+    with pytest.raises(ValueError, match="topk_idx must"):
+        moe.balance_loss(c, lg, idx.long())
+    with pytest.raises(ValueError, match="token_mask must"):
+        moe.balance_loss(c, lg, idx, token_mask=torch.ones(3, dtype=torch.bool))
+    with pytest.raises(ValueError, match="seq_offsets"):
+        moe.balance_loss(c, lg, idx, seq_offsets=torch.zeros(1, dtype=torch.int32))
