@@ -302,6 +302,56 @@ MOE_API moe_status_t moe_layer_backward(const moe_config_t* cfg, const void* x, 
                                 void* dx, float* dw_router, float* dbias, float* dw_gate, float* dw_up,
                                 float* dw_down, void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/* moe_layer_backward with one more gradient to the router logits: dlogits
+ * [T, E] fp32 (from moe_balance_loss on the same routing), added to the one
+ * that comes through the routing weights before dx, dw_router and dbias are
+ * formed.  NULL: moe_layer_backward, bit for bit. */
+MOE_API moe_status_t moe_layer_backward_aux(const moe_config_t* cfg, const void* x, const void* w_router,
+                                    const void* w_gate, const void* w_up, const void* w_down, const void* dout,
+                                    const float* dlogits, void* dx, float* dw_router, float* dbias, float* dw_gate,
+                                    float* dw_up, float* dw_down, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The training pair with 8-bit activation checkpoints.  Between forward and
+ * backward a layer keeps the routing and its pre-activations G = X W_gate and
+ * U = X W_up as 8-bit codes (the bf16 pair keeps X, G, U and H); everything
+ * else is scratch that all layers of a model can share, one call after the
+ * other.  Blocks of 32 columns of a row share a scale:
+ *   s = bf16(max |v| / 127) (0 when below 2^-126),  c = rint(v / s),  v^ = c s
+ * from the fp32 accumulators; a block that holds a NaN or an infinity gets
+ * s = NaN, codes 0, and decodes to NaN.  out is moe_layer_forward's bit for
+ * bit (it does not go through the codes).  The backward is the derivative of
+ * the layer at G^, U^: with H^ = silu(G^) U^, dHu = dout W_down^T, routing
+ * weight w:
+ *   dweight = <dHu, H^>, dG = w dHu U^ silu'(G^), dU = w dHu silu(G^),
+ *   dW_down = (w H^)^T dout, dW_gate = X^T dG, dW_up = X^T dU,
+ *   dlogits_total = softmax part + dlogits,  dx = dG W_gate^T + dU W_up^T +
+ *   dlogits_total W_r,  dw_router = dlogits_total^T x,  dbias = its column sums
+ * with w H^, dG and dU rounded to bf16 for the tensor cores, fp32 sums, and
+ * every gradient rounded once to bf16 (dbias and dlogits may be NULL; dlogits
+ * [T, E] fp32 as moe_balance_loss writes it).
+ * ckpt: moe_checkpoint_size_c8 bytes, written by the forward and read by the
+ * backward (same cfg, x and weights; it may be called again on it), laid out
+ * (256-byte aligned parts) as topk_idx [T, 2] int32 | topk_w [T, 2] fp32 |
+ * logits [T, E] fp32 | counts_raw [E], counts_kept [E], offsets [E + 1] int32 |
+ * perm [T*2] | slot_of [T, 2] int32 | row_scale [T*2] fp32 | G codes [T*2, f]
+ * int8 | U codes | G scales [T*2, f / 32] bf16 | U scales (rows from
+ * offsets[E] on are not written).  ws: moe_workspace_size_train_c8 bytes.
+ * Scope and errors as the bf16 pair (bf16, d and f multiples of 256, else
+ * MOE_ERR_UNSUPPORTED and sizes of 0); a ckpt or ws that is too small is
+ * MOE_ERR_WORKSPACE.  Reductions have a fixed order.  T == 0: the backward
+ * writes zero gradients. */
+MOE_API size_t moe_checkpoint_size_c8(const moe_config_t* cfg);
+MOE_API size_t moe_workspace_size_train_c8(const moe_config_t* cfg);
+MOE_API moe_status_t moe_layer_forward_train_c8(const moe_config_t* cfg, const void* x, const void* w_router,
+                                        const float* logit_bias, const void* w_gate, const void* w_up,
+                                        const void* w_down, void* out, void* ckpt, size_t ckpt_bytes, void* ws,
+                                        size_t ws_bytes, moe_stream_t stream);
+MOE_API moe_status_t moe_layer_backward_c8(const moe_config_t* cfg, const void* x, const void* w_router,
+                                   const void* w_gate, const void* w_up, const void* w_down, const void* dout,
+                                   const float* dlogits, void* dx, void* dw_router, void* dbias, void* dw_gate,
+                                   void* dw_up, void* dw_down, const void* ckpt, size_t ckpt_bytes, void* ws,
+                                   size_t ws_bytes, moe_stream_t stream);
+
 /* 8-bit expert weights ("Benchmarking xAI's Grok-1", section "Grok-1: In
  * Practice": the released weights were quantised; "Let Grok spill the beans
  * on Grok": 8-bit quantisation; the pages give no scheme).  Weight-only,

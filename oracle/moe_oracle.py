@@ -531,3 +531,58 @@ def balance_loss(logits, idx, mask=None, seq_offsets=None, balance_coef=0.01, z_
             z += lse * lse / n
             dl[t] = p * (balance_coef * E / n * (f - float(f @ p)) + 2.0 * z_coef / n * lse)
     return np.array([balance_coef * balance + z_coef * z, balance, z]), counts, dl
+
+
+# ----------------------------------------------------------------------------
+# 8-bit activation checkpoints
+# ----------------------------------------------------------------------------
+def code8(v):
+    """8-bit codes of rows of v in blocks of 32 columns: scale = bf16(max |v| / 127) (0 below 2^-126, NaN for a
+    block with a NaN or an infinity), code = rint(v / scale).  Returns (codes int64, scale float64 [rows, n / 32])."""
+    b = np.asarray(v, dtype=np.float64).reshape(v.shape[0], -1, 32)
+    amax = np.max(np.abs(b), axis=2)
+    bad = ~np.isfinite(b).all(axis=2)
+    s = np.where(bad, 0.0, amax) / 127.0
+    m, ex = np.frexp(s)
+    s = np.ldexp(np.rint(m * 256.0) / 256.0, ex)  # 8 significant bits, ties to even
+    s[s < 2.0 ** -126] = 0.0
+    c = np.where(s[:, :, None] > 0, np.rint(np.where(bad[:, :, None], 0.0, b) / np.where(s > 0, s, 1.0)[:, :, None]), 0.0)
+    s[bad] = np.nan
+    return c.astype(np.int64).reshape(v.shape), s
+
+
+def decode8(codes, scale):
+    c = np.asarray(codes, dtype=np.float64)
+    return (c.reshape(c.shape[0], -1, 32) * np.asarray(scale, dtype=np.float64)[:, :, None]).reshape(c.shape)
+
+
+def layer_backward_at(x, w_router, w_gate, w_up, w_down, dout, idx, w, slot_of, g_hat, u_hat, dlogits=None):
+    """layer_backward with the routing (idx, w, slot_of) and the pre-activations of every kept slot given: the
+    derivative is taken at g_hat, u_hat [slots, f] instead of x W_gate and x W_up.  dlogits [T, E]: a further
+    gradient to the logits."""
+    x64, wr, go = to_f64(x), to_f64(w_router), to_f64(dout)
+    T, E = x64.shape[0], wr.shape[0]
+    dweight, dx = np.zeros((T, 2)), np.zeros_like(x64)
+    grads = {"dw_gate": [], "dw_up": [], "dw_down": []}
+    for e in range(E):
+        wg, wu, wd = to_f64(w_gate[e]), to_f64(w_up[e]), to_f64(w_down[e])
+        ts, js = np.nonzero((np.asarray(idx) == e) & (np.asarray(slot_of) >= 0))
+        r = np.asarray(slot_of)[ts, js]
+        g, u = np.asarray(g_hat)[r], np.asarray(u_hat)[r]
+        h = silu(g) * u
+        dhu = go[ts] @ wd.T
+        dweight[ts, js] = np.sum(dhu * h, axis=1)
+        wt = np.asarray(w, dtype=np.float64)[ts, js][:, None]
+        dg, du = wt * dhu * u * silu_grad(g), wt * dhu * silu(g)
+        grads["dw_down"].append((wt * h).T @ go[ts])
+        grads["dw_gate"].append(x64[ts].T @ dg)
+        grads["dw_up"].append(x64[ts].T @ du)
+        np.add.at(dx, ts, dg @ wg.T + du @ wu.T)
+    dl = np.zeros((T, E)) if dlogits is None else np.array(dlogits, dtype=np.float64)
+    w64 = np.asarray(w, dtype=np.float64)
+    mean = np.sum(w64 * dweight, axis=1)
+    for j in range(2):
+        np.add.at(dl, (np.arange(T), np.asarray(idx)[:, j]), w64[:, j] * (dweight[:, j] - mean))
+    res = {k: np.stack(v) for k, v in grads.items()}
+    res.update(dx=dx + dl @ wr, dw_router=dl.T @ x64, dbias=dl.sum(axis=0), dlogits=dl, dweight=dweight)
+    return res

@@ -27,7 +27,8 @@ __all__ = [
     "workspace_size_train", "layer_forward_train", "layer_backward", "route_counts", "dispatch_shard", "gather_rows",
     "EP_MAX_WORLD", "EpPeers", "ep_dispatch_peers", "ep_expert_ffn_peers", "ep_combine_peers", "peer_export",
     "peer_import", "peer_release",
-    "balance_loss_workspace_size", "balance_loss",
+    "balance_loss_workspace_size", "balance_loss", "checkpoint_size_c8", "workspace_size_train_c8",
+    "checkpoint_views_c8", "layer_forward_train_c8", "layer_backward_c8",
     "GEMM_TILES", "set_gemm_tiles", "gemm_tiles", "PHASES", "profile_phases", "profile_read",
 ]
 
@@ -113,6 +114,11 @@ def _load():
         "moe_expert_ffn_w8": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "moe_layer_forward_w8": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "moe_expert_utilization": ([P, ctypes.c_int32, P, P, P], ctypes.c_int),
+        "moe_layer_backward_aux": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
+        "moe_checkpoint_size_c8": ([cfgp], sz),
+        "moe_workspace_size_train_c8": ([cfgp], sz),
+        "moe_layer_forward_train_c8": ([cfgp, P, P, P, P, P, P, P, P, sz, P, sz, P], ctypes.c_int),
+        "moe_layer_backward_c8": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P, sz, P], ctypes.c_int),
         "moe_balance_loss_workspace_size": ([cfgp, ctypes.c_int32], sz),
         "moe_balance_loss": ([cfgp, P, P, P, P, ctypes.c_int32, ctypes.c_float, ctypes.c_float, P, P, P, P, sz, P],
                              ctypes.c_int),
@@ -549,9 +555,11 @@ def layer_forward_train(cfg: Config, x, w_router, w_gate, w_up, w_down, ws, logi
 
 
 def layer_backward(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ws, grads=None, want_dbias=True,
-                   stream=None):
+                   stream=None, dlogits=None):
     """Gradients of sum(out * dout) after layer_forward_train on the same ws.  Returns a dict of
-    dx (layer dtype) and fp32 dw_router, dbias (or None), dw_gate, dw_up, dw_down."""
+    dx (layer dtype) and fp32 dw_router, dbias (or None), dw_gate, dw_up, dw_down.  dlogits [T, E] (fp32,
+    from balance_loss) adds the gradient of a loss on the router logits."""
+    _expect("dlogits", dlogits, cfg.T * cfg.E, torch.float32)
     _expect_layer(cfg, x, w_router, w_gate, w_up, w_down)
     _expect("dout", dout, cfg.T * cfg.d if cfg.T else dout.numel(), cfg.torch_dtype)
     E, d, f = cfg.E, cfg.d, cfg.f
@@ -565,11 +573,88 @@ def layer_backward(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ws, gra
     g.setdefault("dw_gate", _empty((E, d, f), torch.float32, x))
     g.setdefault("dw_up", _empty((E, d, f), torch.float32, x))
     g.setdefault("dw_down", _empty((E, f, d), torch.float32, x))
-    _check(lib.moe_layer_backward(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(w_gate), _dev_ptr(w_up),
-                                  _dev_ptr(w_down), _dev_ptr(dout), _dev_ptr(g["dx"]), _dev_ptr(g["dw_router"]),
-                                  _dev_ptr(g["dbias"]), _dev_ptr(g["dw_gate"]), _dev_ptr(g["dw_up"]),
-                                  _dev_ptr(g["dw_down"]), _dev_ptr(ws), ws.numel(), _stream(stream, x.device)),
-           "moe_layer_backward")
+    _check(lib.moe_layer_backward_aux(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(w_gate), _dev_ptr(w_up),
+                                      _dev_ptr(w_down), _dev_ptr(dout), _dev_ptr(dlogits), _dev_ptr(g["dx"]),
+                                      _dev_ptr(g["dw_router"]), _dev_ptr(g["dbias"]), _dev_ptr(g["dw_gate"]),
+                                      _dev_ptr(g["dw_up"]), _dev_ptr(g["dw_down"]), _dev_ptr(ws), ws.numel(),
+                                      _stream(stream, x.device)), "moe_layer_backward")
+    return g
+
+
+def checkpoint_size_c8(cfg: Config) -> int:
+    return lib.moe_checkpoint_size_c8(cfg.ref)
+
+
+def workspace_size_train_c8(cfg: Config) -> int:
+    return lib.moe_workspace_size_train_c8(cfg.ref)
+
+
+def checkpoint_views_c8(cfg: Config, ckpt):
+    """Named views into a checkpoint of layer_forward_train_c8 (layout stated in include/moe.h): the routing
+    (topk_idx and logits are what balance_loss takes) and the 8-bit codes with their scales."""
+    T, E, f, rows = cfg.T, cfg.E, cfg.f, cfg.T * cfg.top_k
+    i32, f32 = torch.int32, torch.float32
+    spec = [("topk_idx", i32, (T, 2)), ("topk_w", f32, (T, 2)), ("logits", f32, (T, E)), ("route", i32, (3 * E + 1,)),
+            ("perm", i32, (rows,)), ("slot_of", i32, (T, 2)), ("row_scale", f32, (rows,)),
+            ("g_codes", torch.int8, (rows, f)), ("u_codes", torch.int8, (rows, f)),
+            ("g_scale", torch.bfloat16, (rows, f // 32)), ("u_scale", torch.bfloat16, (rows, f // 32))]
+    flat = ckpt.view(torch.uint8).view(-1)
+    views, o = {}, 0
+    for name, dt, shape in spec:
+        nbytes = math.prod(shape) * dt.itemsize
+        views[name] = flat[o:o + nbytes].view(dt).view(shape)
+        o += _round256(nbytes)
+    route = views.pop("route")
+    views.update(counts_raw=route[:E], counts_kept=route[E:2 * E], offsets=route[2 * E:])
+    return views
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def layer_forward_train_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, ckpt, ws, logit_bias=None, out=None,
+                           stream=None):
+    """The layer forward that keeps its pre-activations as 8-bit codes in ckpt (checkpoint_size_c8 bytes); ws
+    (workspace_size_train_c8 bytes) is scratch that every layer of a model can share."""
+    _expect_layer(cfg, x, w_router, w_gate, w_up, w_down, logit_bias, out)
+    if out is None:
+        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x)
+    _same_device(x, w_router, w_gate, w_up, w_down, ckpt, ws, logit_bias, out)
+    with torch.cuda.device(x.device):
+        _check(lib.moe_layer_forward_train_c8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias),
+                                              _dev_ptr(w_gate), _dev_ptr(w_up), _dev_ptr(w_down), _dev_ptr(out),
+                                              _dev_ptr(ckpt), _nbytes(ckpt), _dev_ptr(ws), _nbytes(ws),
+                                              _stream(stream, x.device)), "moe_layer_forward_train_c8")
+    return out
+
+
+def layer_backward_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ckpt, ws, dlogits=None, grads=None,
+                      want_dbias=True, stream=None):
+    """Gradients of sum(out * dout) after layer_forward_train_c8 on the same ckpt, taken at the decoded
+    pre-activations; dlogits [T, E] (fp32, from balance_loss) adds the gradient of a loss on the router logits.
+    Returns a dict of dx, dw_router, dbias (or None), dw_gate, dw_up, dw_down, all in bf16."""
+    _expect_layer(cfg, x, w_router, w_gate, w_up, w_down)
+    E, d, f, dt = cfg.E, cfg.d, cfg.f, cfg.torch_dtype
+    _expect("dout", dout, cfg.T * d, dt)
+    _expect("dlogits", dlogits, cfg.T * E, torch.float32)
+    shapes = {"dx": (cfg.T, d), "dw_router": (E, d), "dbias": (E,), "dw_gate": (E, d, f), "dw_up": (E, d, f),
+              "dw_down": (E, f, d)}
+    g = dict(grads or {})
+    if not want_dbias:
+        g["dbias"] = None
+    for k, shape in shapes.items():
+        if k not in g:
+            g[k] = _empty(shape, dt, x)
+        _expect(k, g[k], math.prod(shape), dt)
+    _same_device(x, w_router, w_gate, w_up, w_down, dout, ckpt, ws, dlogits, *g.values())
+    with torch.cuda.device(x.device):
+        _check(lib.moe_layer_backward_c8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(w_gate), _dev_ptr(w_up),
+                                         _dev_ptr(w_down), _dev_ptr(dout), _dev_ptr(dlogits), _dev_ptr(g["dx"]),
+                                         _dev_ptr(g["dw_router"]), _dev_ptr(g["dbias"]), _dev_ptr(g["dw_gate"]),
+                                         _dev_ptr(g["dw_up"]), _dev_ptr(g["dw_down"]), _dev_ptr(ckpt), _nbytes(ckpt),
+                                         _dev_ptr(ws), _nbytes(ws), _stream(stream, x.device)),
+               "moe_layer_backward_c8")
     return g
 
 

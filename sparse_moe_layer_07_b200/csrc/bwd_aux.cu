@@ -69,11 +69,15 @@ __global__ void __launch_bounds__(256) bwd_gather_kernel(const uint4* __restrict
 // gradients, lanes 0-7 write the token's dlogits row, and the warp streams
 // dx[t] = round(dx32[t] + dl_0 W_r[i_0] + dl_1 W_r[i_1]) (slot 0 first), four
 // columns per lane and 16-byte vector, four vectors in flight per lane.
+// kAux: dl_aux (the gradient of a loss on the logits themselves, over all
+// experts) is added to the token's dlogits, and dx takes all eight rows of W_r
+// (in expert order): W_r comes from L1, eight loads where two were.
+template <bool kAux>
 __global__ void __launch_bounds__(256) router_bwd_token_kernel(
     const float* __restrict__ dw_part, int n_parts, const int32_t* __restrict__ slot_of,
     const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w, const __nv_bfloat16* __restrict__ wr,
     const float* __restrict__ dx32, int64_t T, int64_t d, int64_t max_slot, float* __restrict__ dlogits,
-    float* __restrict__ dweight, __nv_bfloat16* __restrict__ dx, int* err) {
+    float* __restrict__ dweight, __nv_bfloat16* __restrict__ dx, const float* __restrict__ dl_aux, int* err) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int nq = (int)(d / 4);  // 4-column groups of a row (d is a multiple of 128)
@@ -103,11 +107,37 @@ __global__ void __launch_bounds__(256) router_bwd_token_kernel(
     const float mean = w0 * dw0 + w1 * dw1;
     const float dl0 = w0 * (dw0 - mean);
     const float dl1 = w1 * (dw1 - mean);
+    float dl = 0.f;  // lane e < 8: the gradient of logit e
     if (lane < kE) {
-      float v = 0.f;
-      if (e0 == lane) v += dl0;
-      if (e1 == lane) v += dl1;
-      dlogits[t * kE + lane] = v;
+      if (e0 == lane) dl += dl0;
+      if (e1 == lane) dl += dl1;
+      if (kAux) dl += __ldg(dl_aux + t * kE + lane);
+      dlogits[t * kE + lane] = dl;
+    }
+    if (kAux) {
+      float g[kE];
+#pragma unroll
+      for (int k = 0; k < kE; ++k) g[k] = __shfl_sync(0xffffffffu, dl, k);
+      const float4* a4 = reinterpret_cast<const float4*>(dx32 + t * d);
+      uint2* o2 = reinterpret_cast<uint2*>(dx + t * d);
+      for (int i = lane; i < nq; i += 32) {
+        const float4 a = __ldcs(a4 + i);
+        uint2 r[kE];
+#pragma unroll
+        for (int k = 0; k < kE; ++k) r[k] = __ldg(reinterpret_cast<const uint2*>(wr + (int64_t)k * d) + i);
+        float v0 = a.x, v1 = a.y, v2 = a.z, v3 = a.w;
+#pragma unroll
+        for (int k = 0; k < kE; ++k) {
+          const float2 p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[k].x));
+          const float2 q = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[k].y));
+          v0 = fmaf(g[k], p.x, v0);
+          v1 = fmaf(g[k], p.y, v1);
+          v2 = fmaf(g[k], q.x, v2);
+          v3 = fmaf(g[k], q.y, v3);
+        }
+        o2[i] = make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
+      }
+      continue;
     }
     const float4* a4 = reinterpret_cast<const float4*>(dx32 + t * d);
     const uint2* p2 = reinterpret_cast<const uint2*>(wr + (int64_t)e0 * d);
@@ -200,15 +230,19 @@ __global__ void __launch_bounds__(256) router_bwd_weight_kernel(const float* __r
 
 // dW_r[e][i] = sum over chunks in order; block 0 also forms dbias[e] = sum_t dlogits[t, e]
 // (each thread a strided subset of tokens, then a fixed tree).
+__device__ __forceinline__ void store_as(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+template <typename Tout>
 __global__ void __launch_bounds__(256) router_bwd_reduce_kernel(const float* __restrict__ part, int chunks,
                                                                const float* __restrict__ dlogits, int64_t T,
-                                                               int64_t d, float* __restrict__ dw_router,
-                                                               float* __restrict__ dbias) {
+                                                               int64_t d, Tout* __restrict__ dw_router,
+                                                               Tout* __restrict__ dbias) {
   const int64_t n = (int64_t)kE * d;
   for (int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; k < n; k += (int64_t)gridDim.x * blockDim.x) {
     float acc = 0.f;
     for (int c = 0; c < chunks; ++c) acc += part[(int64_t)c * n + k];
-    dw_router[k] = acc;
+    store_as(dw_router + k, acc);
   }
   if (blockIdx.x != 0 || dbias == nullptr) return;
   __shared__ float s[kE][256];
@@ -227,7 +261,7 @@ __global__ void __launch_bounds__(256) router_bwd_reduce_kernel(const float* __r
       for (int e = 0; e < kE; ++e) s[e][threadIdx.x] += s[e][threadIdx.x + w];
     __syncthreads();
   }
-  if (threadIdx.x < kE) dbias[threadIdx.x] = s[threadIdx.x][0];
+  if (threadIdx.x < kE) store_as(dbias + threadIdx.x, s[threadIdx.x][0]);
 }
 
 unsigned capped(int64_t want, const Ctx& ctx, int per_sm = 8) {
@@ -249,12 +283,14 @@ cudaError_t launch_bwd_gather(const moe_config_t& c, const void* dout, const int
 
 cudaError_t launch_router_bwd(const moe_config_t& c, const float* dw_part, int n_parts, const int32_t* slot_of,
                               const int32_t* topk_idx, const float* topk_w, const void* w_router, const float* dx32,
-                              const void* x, float* dlogits, float* dweight, void* dx, float* dw_router,
-                              float* dbias, float* wr_part, cudaStream_t s, const Ctx& ctx) {
+                              const void* x, float* dlogits, float* dweight, void* dx, void* dw_router,
+                              void* dbias, float* wr_part, cudaStream_t s, const Ctx& ctx, const float* dl_aux,
+                              bool bf16_out) {
   if (c.T == 0) return cudaSuccess;
-  router_bwd_token_kernel<<<capped((c.T + 7) / 8, ctx), 256, 0, s>>>(
+  auto token_kernel = dl_aux ? router_bwd_token_kernel<true> : router_bwd_token_kernel<false>;
+  token_kernel<<<capped((c.T + 7) / 8, ctx), 256, 0, s>>>(
       dw_part, n_parts, slot_of, topk_idx, topk_w, static_cast<const __nv_bfloat16*>(w_router), dx32, c.T, c.d,
-      slot_rows(c), dlogits, dweight, static_cast<__nv_bfloat16*>(dx), ctx.err);
+      slot_rows(c), dlogits, dweight, static_cast<__nv_bfloat16*>(dx), dl_aux, ctx.err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)((c.d / 8 + 255) / 256), (unsigned)kRouterBwdChunks);
@@ -262,8 +298,14 @@ cudaError_t launch_router_bwd(const moe_config_t& c, const float* dw_part, int n
                                                 kRouterBwdChunks, wr_part);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  router_bwd_reduce_kernel<<<capped((kE * c.d + 255) / 256, ctx), 256, 0, s>>>(wr_part, kRouterBwdChunks, dlogits,
-                                                                             c.T, c.d, dw_router, dbias);
+  const unsigned blocks = capped((kE * c.d + 255) / 256, ctx);
+  if (bf16_out)
+    router_bwd_reduce_kernel<<<blocks, 256, 0, s>>>(wr_part, kRouterBwdChunks, dlogits, c.T, c.d,
+                                                    static_cast<__nv_bfloat16*>(dw_router),
+                                                    static_cast<__nv_bfloat16*>(dbias));
+  else
+    router_bwd_reduce_kernel<<<blocks, 256, 0, s>>>(wr_part, kRouterBwdChunks, dlogits, c.T, c.d,
+                                                    static_cast<float*>(dw_router), static_cast<float*>(dbias));
   return cudaGetLastError();
 }
 

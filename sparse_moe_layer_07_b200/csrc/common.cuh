@@ -65,6 +65,50 @@ __device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdiv
 // A no-op for a kernel launched without the attribute.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// 8-bit code of a block of 32 values (activation checkpoints): s = bf16(amax /
+// 127) and c = rint(v / s), so an element is off by at most s / 2 = amax / 254
+// (an e4m3 code of the same 8 bits would be off by up to 1/16 of the element:
+// for normally distributed rows a root mean square error of 2.6% against 0.5%).
+// A scale below 2^-126 counts as 0 (all codes 0); a block that holds a NaN or
+// an infinity gets the scale NaN and decodes to NaN.  amax is found on the bit
+// patterns (as unsigned integers NaN and inf are the largest).  |v / s| stays
+// under 127.25, since rounding s to bf16 moves it by at most 2^-9, so no clamp
+// is needed; adding 1.5 * 2^23 rounds to an integer (ties to even) whose low
+// byte is the code.
+__device__ __forceinline__ uint16_t code32(const uint32_t (&v)[32], uint32_t (&codes)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) m = max(m, v[i] & 0x7fffffffu);
+  const __nv_bfloat16 sb = __float2bfloat16_rn(__uint_as_float(m) / 127.0f);
+  uint16_t bits = __bfloat16_as_ushort(sb);
+  float inv = 0.f;
+  if (m >= 0x7f800000u)
+    bits = 0x7fc0;
+  else if (bits < 0x0080)
+    bits = 0;
+  else
+    inv = 1.0f / __bfloat162float(sb);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      q[k] = __float_as_uint(inv > 0.f ? fmaf(__uint_as_float(v[4 * i + k]), inv, 12582912.0f) : 12582912.0f);
+    codes[i] = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+  }
+  return bits;
+}
+
+// Four codes of a word as fp32 integers: the biased byte b under the exponent
+// of 2^23 reads 2^23 + b.
+__device__ __forceinline__ void codes4(uint32_t w, float (&v)[4]) {
+  w ^= 0x80808080u;
+  v[0] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)) - 8388736.0f;
+  v[1] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441)) - 8388736.0f;
+  v[2] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)) - 8388736.0f;
+  v[3] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443)) - 8388736.0f;
+}
+
 __device__ __forceinline__ void flag_error(int* err, int bits) {
   if (err) atomicOr(err, bits);
 }

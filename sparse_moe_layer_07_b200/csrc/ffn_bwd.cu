@@ -20,6 +20,10 @@
 //         16-row MMA steps that hold its rows, and the rows of the last step
 //         past the expert's end are zeroed in shared memory before the MMA
 //         (by warp 6, which only kWG has).
+// C8 variants (8-bit checkpoints): kDH decodes G and U from codes and bf16
+// scales (2.1 bytes a value pair where bf16 G, U and H are 6), forms H again
+// and writes hw = bf16(w * H), so that dW_down = hw^T dout takes dout as it is
+// and the product w * dout is rounded nowhere; kWG writes bf16.
 // Pipeline as in ffn_tc.cu: persistent CTAs, warp 0 TMA, warp 1 MMA (lane 0
 // alone) + TMEM (two 128 x 256 fp32 accumulators), warps 2-5 epilogue; every
 // wait bounded.
@@ -83,6 +87,8 @@ struct BwdArgs {
   const __nv_bfloat16* G;  // kDH inputs [rows, f]
   const __nv_bfloat16* U;
   const __nv_bfloat16* H;
+  Codes8 codes;            // kDH, C8: instead of G, U, H
+  __nv_bfloat16* hw;       // kDH, C8: output [rows, f]
   __nv_bfloat16* dG;       // kDH outputs [rows, f]
   __nv_bfloat16* dU;
   float* dw_part;          // kDH: [rows, n_tiles * parts per tile]
@@ -176,7 +182,7 @@ __device__ __forceinline__ void unpack8_bf16(const uint4 q, float (&v)[8]) {
   }
 }
 
-template <int MODE>
+template <int MODE, bool C8>
 __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
     bwd_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
@@ -436,7 +442,84 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
       const uint32_t tacc = tmem_base + buf * kAccStride + ((uint32_t)(q * 32) << 16);
       // tile row of this thread; M = 64 accumulators hold row 16 q + i in lane i (< 16) of quarter q
       const int r = (MODE != kWG && t.rows <= 64) ? (lane < 16 ? q * 16 + lane : BM) : q * 32 + lane;
-      if (MODE == kDH) {
+      if (MODE == kDH && C8) {
+        const bool valid = r < t.rows;
+        const int64_t row = t.m0 + r;
+        const float w = valid ? __ldg(args.row_scale + row) : 0.f;
+        const int64_t base = row * args.ld + t.n0;
+        float dot = 0.f;
+        // codes of a 32-column chunk: 2 x 16 bytes of G and of U, the next chunk's
+        // loaded while this one is computed; the tile's 8 scales of each are one load
+        uint4 qg[2], qu[2], sg4 = {}, su4 = {};
+        auto load_chunk = [&](int c, uint4 (&a)[2], uint4 (&b)[2]) {
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            a[p] = __ldcs(reinterpret_cast<const uint4*>(args.codes.g + base + c * 32) + p);
+            b[p] = __ldcs(reinterpret_cast<const uint4*>(args.codes.u + base + c * 32) + p);
+          }
+        };
+        if (valid) {
+          sg4 = __ldg(reinterpret_cast<const uint4*>(args.codes.sg + base / 32));
+          su4 = __ldg(reinterpret_cast<const uint4*>(args.codes.su + base / 32));
+          load_chunk(0, qg, qu);
+        }
+#pragma unroll
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t v[32];
+          tmem_ld32(tacc + c * 32, v);
+          const bool more = c + 1 < BN / 32;
+          uint4 ng[2], nu[2];
+          if (valid && more) load_chunk(c + 1, ng, nu);
+          tmem_wait_ld();
+          if (valid) {
+            const uint32_t pg = (&sg4.x)[c >> 1], pu = (&su4.x)[c >> 1];
+            const float sg = __uint_as_float((c & 1) ? pg & 0xffff0000u : pg << 16);
+            const float su = __uint_as_float((c & 1) ? pu & 0xffff0000u : pu << 16);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const int64_t o = base + c * 32 + p * 8;
+              uint32_t og[4], ou[4], oh[4];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int word = 2 * p + i;
+                float g4[4], u4[4], dg[4], du[4], hw[4];
+                codes4((&qg[word >> 2].x)[word & 3], g4);
+                codes4((&qu[word >> 2].x)[word & 3], u4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float g = sg * g4[k], u = su * u4[k];
+                  const float dhu = __uint_as_float(v[p * 8 + 4 * i + k]);
+                  const float sig = 1.0f / (1.0f + __expf(-g));
+                  const float sl = g * sig;
+                  const float h = sl * u;
+                  dot = fmaf(dhu, h, dot);
+                  const float dh = w * dhu;
+                  dg[k] = dh * u * (sig * (1.0f + g * (1.0f - sig)));
+                  du[k] = dh * sl;
+                  hw[k] = w * h;
+                }
+                og[2 * i] = pack_bf16x2(dg[0], dg[1]);
+                og[2 * i + 1] = pack_bf16x2(dg[2], dg[3]);
+                ou[2 * i] = pack_bf16x2(du[0], du[1]);
+                ou[2 * i + 1] = pack_bf16x2(du[2], du[3]);
+                oh[2 * i] = pack_bf16x2(hw[0], hw[1]);
+                oh[2 * i + 1] = pack_bf16x2(hw[2], hw[3]);
+              }
+              __stcs(reinterpret_cast<uint4*>(args.dG + o), make_uint4(og[0], og[1], og[2], og[3]));
+              __stcs(reinterpret_cast<uint4*>(args.dU + o), make_uint4(ou[0], ou[1], ou[2], ou[3]));
+              __stcs(reinterpret_cast<uint4*>(args.hw + o), make_uint4(oh[0], oh[1], oh[2], oh[3]));
+            }
+          }
+          if (more) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              qg[p] = ng[p];
+              qu[p] = nu[p];
+            }
+          }
+        }
+        if (valid) args.dw_part[row * (int64_t)args.n_tiles + t.nb] = dot;
+      } else if (MODE == kDH) {
         const bool valid = r < t.rows;
         const int64_t row = t.m0 + r;
         const float w = valid ? __ldg(args.row_scale + row) : 0.f;
@@ -529,6 +612,37 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
                                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
           }
         }
+      } else if (C8) {
+        // as below with 32 rows x 64 bf16 columns (128 bytes) per store
+        const bool zero = t.nkb == 0;
+        uint8_t* stage0 = sOut + (q * 2) * OUT_STAGE;
+        const int y = t.e * (int)args.M + t.m0 + q * 32;
+#pragma unroll 1
+        for (int c = 0; c < BN / 64; ++c) {
+          uint32_t v[32], v2[32];
+          tmem_ld32(tacc + c * 64, v);
+          tmem_ld32(tacc + c * 64 + 32, v2);
+          tmem_wait_ld();
+          uint8_t* st = stage0 + (c & 1) * OUT_STAGE;
+          if (lane == 0) bulk_wait_group_read<1>();
+          __syncwarp();
+          uint4* row = reinterpret_cast<uint4*>(st + lane * 128);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t* s8 = j < 4 ? v + 8 * j : v2 + 8 * (j - 4);
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[i] = zero ? 0u : pack_bf16x2(__uint_as_float(s8[2 * i]), __uint_as_float(s8[2 * i + 1]));
+            row[j ^ (lane & 7)] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmOut, st, t.n0 + c * 64, y);
+            bulk_commit_group();
+          }
+        }
       } else {
         // 32 rows x 32 columns per TMA store: lane = row, its 8 16-byte pieces
         // placed with the 128-byte swizzle (piece j of row r at j ^ (r % 8))
@@ -571,10 +685,10 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
   }
 }
 
-template <int MODE>
+template <int MODE, bool C8 = false>
 cudaError_t launch_bwd(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
                        const CUtensorMap& out, const BwdArgs& args, cudaStream_t s, const Ctx& ctx) {
-  auto kern = bwd_gemm_kernel<MODE>;
+  auto kern = bwd_gemm_kernel<MODE, C8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   kern<<<ctx.num_sms, Warps<MODE>::kThreads, SMEM_BYTES, s>>>(a0, a1, b0, b1, out, args);
@@ -632,6 +746,27 @@ cudaError_t launch_bwd_dh(const moe_config_t& c, const void* dout_perm, const in
   return launch_bwd<kDH>(ta, ta, tb, tb, ta, a, s, ctx);
 }
 
+cudaError_t launch_bwd_dh_c8(const moe_config_t& c, const void* dout_perm, const int32_t* offsets, const void* wd,
+                             const Codes8& codes, const float* row_scale, void* dG, void* dU, void* hw, float* dw_part,
+                             cudaStream_t s, const Ctx& ctx) {
+  static_assert(Warps<kDH>::kEpi == 4, "one partial per row and tile");
+  const int64_t rows = slot_rows(c);
+  if (rows == 0) return cudaSuccess;
+  CUtensorMap ta, tb;
+  if (!map_rows(&ta, dout_perm, rows, c.d, 128) || !map_weights(&tb, wd, c.E, c.f, c.d)) return cudaErrorInvalidValue;
+  BwdArgs a = base_args(c, offsets, ctx);
+  a.n_tiles = (int)(c.f / BN);
+  a.num_kb = (int)(c.d / BK);
+  a.row_scale = row_scale;
+  a.codes = codes;
+  a.hw = static_cast<__nv_bfloat16*>(hw);
+  a.dG = static_cast<__nv_bfloat16*>(dG);
+  a.dU = static_cast<__nv_bfloat16*>(dU);
+  a.dw_part = dw_part;
+  a.ld = c.f;
+  return launch_bwd<kDH, true>(ta, ta, tb, tb, ta, a, s, ctx);
+}
+
 cudaError_t launch_bwd_dx(const moe_config_t& c, const void* dG, const void* dU, const int32_t* offsets,
                           const void* wg, const void* wu, const int32_t* perm, float* dx32, cudaStream_t s,
                           const Ctx& ctx) {
@@ -653,7 +788,8 @@ cudaError_t launch_bwd_dx(const moe_config_t& c, const void* dG, const void* dU,
 }
 
 cudaError_t launch_bwd_wgrad(const moe_config_t& c, const void* a_rows, int64_t M, const void* b_rows, int64_t N,
-                             const int32_t* offsets, float* dW, bool m_outer, cudaStream_t s, const Ctx& ctx) {
+                             const int32_t* offsets, void* dW, bool m_outer, cudaStream_t s, const Ctx& ctx,
+                             bool bf16_out) {
   const int64_t rows = slot_rows(c);
   if (rows == 0 || M % BM != 0 || N % BN != 0) return rows == 0 ? cudaSuccess : cudaErrorInvalidValue;
   CUtensorMap ta, tb, to;
@@ -669,19 +805,22 @@ cudaError_t launch_bwd_wgrad(const moe_config_t& c, const void* a_rows, int64_t 
         !encode_tmap(&tb, b_rows, 3, b_dims, b_str, b_box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
   }
-  // dW [E * M, N] fp32, stored 32 x 32 at a time from the swizzled staging tiles
+  // dW [E * M, N] stored 32 rows x 128 bytes at a time from the swizzled staging tiles
+  const uint32_t esz = bf16_out ? 2 : 4;
   const uint64_t o_dims[2] = {(uint64_t)N, (uint64_t)c.E * M};
-  const uint64_t o_str[1] = {(uint64_t)N * 4};
-  const uint32_t o_box[2] = {32, 32};
-  if (!encode_tmap_dtype(&to, dW, 2, o_dims, o_str, o_box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
+  const uint64_t o_str[1] = {(uint64_t)N * esz};
+  const uint32_t o_box[2] = {128 / esz, 32};
+  if (!encode_tmap_dtype(&to, dW, 2, o_dims, o_str, o_box, CU_TENSOR_MAP_SWIZZLE_128B,
+                         bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
     return cudaErrorInvalidValue;
   BwdArgs a = base_args(c, offsets, ctx);
   a.m_tiles = (int)(M / BM);
   a.n_tiles = (int)(N / BN);
   a.m_outer = m_outer ? 1 : 0;
-  a.out = dW;
   a.ld = N;
   a.M = M;
+  if (bf16_out) return launch_bwd<kWG, true>(ta, ta, tb, tb, to, a, s, ctx);
+  a.out = static_cast<float*>(dW);
   return launch_bwd<kWG>(ta, ta, tb, tb, to, a, s, ctx);
 }
 

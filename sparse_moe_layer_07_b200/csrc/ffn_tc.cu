@@ -86,6 +86,10 @@ struct TcArgs {
   float* peer_out[MOE_EP_MAX_WORLD] = {};
   void* save_g;            // gate/up for training: also write G and U (bf16) or NULL
   void* save_u;
+  int8_t* code_g = nullptr;  // gate/up with 8-bit checkpoints: codes [rows, f] and
+  int8_t* code_u = nullptr;  // bf16 scales [rows, f / 32] of G and U
+  uint16_t* scale_g = nullptr;
+  uint16_t* scale_u = nullptr;
   int* err;
 };
 
@@ -156,7 +160,11 @@ __device__ __forceinline__ int source_token(const TcArgs& args, int row, int n_r
 // from TMEM column `tacc` on (gate/up: the matching up columns u_off further
 // on).  Rows with valid == false are read (the TMEM loads are warp-wide) but
 // not stored.  n_rows = kept rows.
-template <int MODE, bool kScatter>
+// kCodes (gate/up, tiles of 128 columns): the pre-activations are also kept as
+// 8-bit codes.  A thread holds 32 columns of one row at a time, which is a
+// block's worth, so amax needs no exchange between threads; the codes cost two
+// 16-byte stores a chunk and matrix where bf16 copies cost four.
+template <int MODE, bool kScatter, bool kCodes = false>
 __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, int row0, int r, bool valid, int n0,
                                               int n_cols, int u_off, uint32_t tacc) {
   if (MODE == kGateUp) {
@@ -166,6 +174,7 @@ __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, in
     // flight while chunk c is computed and stored (the loop is unrolled so the
     // two register sets stay in registers)
     const int nch = n_cols / 32;
+    uint32_t scales_g[2] = {0, 0}, scales_u[2] = {0, 0};
     uint32_t gb[2][32], ub[2][32];
     tmem_ld32(tacc, gb[0]);
     tmem_ld32(tacc + u_off, ub[0]);
@@ -192,7 +201,24 @@ __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, in
         uint4* d4 = reinterpret_cast<uint4*>(dst_row + c * 32);
 #pragma unroll
         for (int i = 0; i < 4; ++i) __stcs(d4 + i, make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]));
-        if (args.save_g) {
+        if (kCodes) {
+          const int64_t o = (int64_t)(row0 + r) * args.ld_out + n0 + c * 32;
+          uint32_t cg[8], cu[8];
+          scales_g[c >> 1] |= (uint32_t)code32(g, cg) << (16 * (c & 1));
+          scales_u[c >> 1] |= (uint32_t)code32(u, cu) << (16 * (c & 1));
+          uint4* g4 = reinterpret_cast<uint4*>(args.code_g + o);
+          uint4* u4 = reinterpret_cast<uint4*>(args.code_u + o);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            __stcs(g4 + i, make_uint4(cg[4 * i], cg[4 * i + 1], cg[4 * i + 2], cg[4 * i + 3]));
+            __stcs(u4 + i, make_uint4(cu[4 * i], cu[4 * i + 1], cu[4 * i + 2], cu[4 * i + 3]));
+          }
+          if (c == 3) {
+            const int64_t so = ((int64_t)(row0 + r) * args.ld_out + n0) / 32;
+            *reinterpret_cast<uint2*>(args.scale_g + so) = make_uint2(scales_g[0], scales_g[1]);
+            *reinterpret_cast<uint2*>(args.scale_u + so) = make_uint2(scales_u[0], scales_u[1]);
+          }
+        } else if (args.save_g) {
           // training: keep the pre-activations for the backward pass
           const int64_t o = (int64_t)(row0 + r) * args.ld_out + n0 + c * 32;
           uint4* g4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.save_g) + o);
@@ -261,13 +287,15 @@ __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, in
 // adds row_scale * (H W_down) into a zeroed fp32 out[token] with vector
 // atomics.  With top-2 a token receives at most two terms and 0 + a + b rounds
 // the same in either order, so the result is the combine's fp32 sum bit for
-// bit, without the Y buffer.
+// bit, without the Y buffer.  FUSED = true with gate/up keeps the
+// pre-activations as 8-bit codes (epilogue_rows).
 template <int MODE, int MMA_N, bool FUSED>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                            const __grid_constant__ CUtensorMap tmB1, const TcArgs args) {
   using C = Cfg<MODE, MMA_N>;
   constexpr bool kScatter = FUSED && MODE == kDown;
+  constexpr bool kCodes = FUSED && MODE == kGateUp;
   constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -421,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = t.rows <= 64 ? (lane < 16 ? q * 16 + lane : BM) : q * 32 + lane;
       const bool valid = r < t.rows;
       const uint32_t tacc = tmem_base + buf * kAccStride + ((uint32_t)(q * 32) << 16);
-      epilogue_rows<MODE, kScatter>(args, sched.offs[kE], t.m0, r, valid, t.n0, C::BN_OUT, C::BN_OUT, tacc);
+      epilogue_rows<MODE, kScatter, kCodes>(args, sched.offs[kE], t.m0, r, valid, t.n0, C::BN_OUT, C::BN_OUT, tacc);
       tc_fence_before();
       mbar_arrive(&tempty[buf]);
     }
@@ -755,7 +783,7 @@ bool use_pair_tiles(const moe_config_t& c) {
 
 cudaError_t launch_tc_gate_up(const moe_config_t& c, const void* x_perm, const int32_t* offsets,
                               const void* wg, const void* wu, void* h, cudaStream_t s, const Ctx& ctx, void* g_save,
-                              void* u_save) {
+                              void* u_save, const Codes8* codes) {
   const int64_t rows = slot_rows(c);
   if (rows == 0) return cudaSuccess;
   CUtensorMap ta, tg, tu;
@@ -782,6 +810,14 @@ cudaError_t launch_tc_gate_up(const moe_config_t& c, const void* x_perm, const i
   args.save_g = g_save;
   args.save_u = u_save;
   args.err = ctx.err;
+  if (codes) {
+    // single-CTA tiles whatever the tile mode (their 128 columns are four whole blocks)
+    args.code_g = codes->g;
+    args.code_u = codes->u;
+    args.scale_g = codes->sg;
+    args.scale_u = codes->su;
+    return launch_grouped<kGateUp, 256, true>(ta, tg, tu, args, s, ctx);
+  }
   if (use_pair_tiles(c)) return launch_pair<kGateUp, false>(ta, tg, tu, args, s, ctx);
   return launch_grouped<kGateUp, 256>(ta, tg, tu, args, s, ctx);
 }

@@ -119,11 +119,22 @@ cudaError_t launch_ffn_simt_down(const moe_config_t& c, const float* h, const in
                                  const float* wd, const float* row_scale, float* y,
                                  cudaStream_t s, const Ctx& ctx);
 
+// 8-bit checkpoint of the pre-activations: codes [T*k, f] and bf16 scales
+// [T*k, f / 32] of G and U (blocks of 32 columns).
+struct Codes8 {
+  int8_t* g;
+  int8_t* u;
+  uint16_t* sg;
+  uint16_t* su;
+};
+
 // bf16 expert FFN on the tcgen05 tensor cores.
+// codes (training with 8-bit checkpoints): also write the codes of G and U.
 // g_save / u_save (training): also write the pre-activations G, U [T*k, f] (bf16).
 cudaError_t launch_tc_gate_up(const moe_config_t& c, const void* x_perm, const int32_t* offsets,
                               const void* wg, const void* wu, void* h, cudaStream_t s,
-                              const Ctx& ctx, void* g_save = nullptr, void* u_save = nullptr);
+                              const Ctx& ctx, void* g_save = nullptr, void* u_save = nullptr,
+                              const Codes8* codes = nullptr);
 cudaError_t launch_tc_down(const moe_config_t& c, const void* h, const int32_t* offsets,
                            const void* wd, const float* row_scale, float* y, cudaStream_t s,
                            const Ctx& ctx);
@@ -149,21 +160,30 @@ int bwd_dh_parts_per_tile();
 cudaError_t launch_bwd_dh(const moe_config_t& c, const void* dout_perm, const int32_t* offsets, const void* wd,
                           const void* G, const void* U, const void* H, const float* row_scale, void* dG, void* dU,
                           float* dw_part, cudaStream_t s, const Ctx& ctx);
+// The same from 8-bit checkpoints: G, U decoded, H = silu(G) U formed again;
+// also writes hw = bf16(row_scale * H) [rows, f], an operand of dW_down.
+cudaError_t launch_bwd_dh_c8(const moe_config_t& c, const void* dout_perm, const int32_t* offsets, const void* wd,
+                             const Codes8& codes, const float* row_scale, void* dG, void* dU, void* hw, float* dw_part,
+                             cudaStream_t s, const Ctx& ctx);
 cudaError_t launch_bwd_dx(const moe_config_t& c, const void* dG, const void* dU, const int32_t* offsets,
                           const void* wg, const void* wu, const int32_t* perm, float* dx32, cudaStream_t s,
                           const Ctx& ctx);
 cudaError_t launch_bwd_wgrad(const moe_config_t& c, const void* a_rows, int64_t M, const void* b_rows, int64_t N,
-                             const int32_t* offsets, float* dW, bool m_outer, cudaStream_t s, const Ctx& ctx);
+                             const int32_t* offsets, void* dW, bool m_outer, cudaStream_t s, const Ctx& ctx,
+                             bool bf16_out = false);
 // dout_perm[r] = dout[perm[r]],  dy_perm[r] = bf16(row_scale[r] * dout[perm[r]])  (r < offsets[E])
 cudaError_t launch_bwd_gather(const moe_config_t& c, const void* dout, const int32_t* perm, const int32_t* offsets,
                               const float* row_scale, void* dout_perm, void* dy_perm, cudaStream_t s, const Ctx& ctx);
 // Router backward: routing-weight gradients from the partials, logit gradients
 // through the softmax over the two selected logits, dx = round(dx32 + dlogits W_r),
 // dW_r = dlogits^T x and dbias = column sums of dlogits (fixed summation orders).
+// dl_aux [T, E] or NULL: more gradient to the logits, added in.  bf16_out:
+// dw_router and dbias are bf16.
 cudaError_t launch_router_bwd(const moe_config_t& c, const float* dw_part, int n_parts, const int32_t* slot_of,
                               const int32_t* topk_idx, const float* topk_w, const void* w_router, const float* dx32,
-                              const void* x, float* dlogits, float* dweight, void* dx, float* dw_router,
-                              float* dbias, float* wr_part, cudaStream_t s, const Ctx& ctx);
+                              const void* x, float* dlogits, float* dweight, void* dx, void* dw_router,
+                              void* dbias, float* wr_part, cudaStream_t s, const Ctx& ctx,
+                              const float* dl_aux = nullptr, bool bf16_out = false);
 constexpr int kRouterBwdChunks = 128;  // token chunks of the dW_r partial sums
 
 // out32 <- 0 ([T, d] fp32), and out <- out32 rounded to cfg's dtype.

@@ -931,13 +931,21 @@ moe_status_t moe_layer_backward(const moe_config_t* cfg, const void* x, const vo
                                 const void* w_up, const void* w_down, const void* dout, void* dx, float* dw_router,
                                 float* dbias, float* dw_gate, float* dw_up, float* dw_down, void* ws,
                                 size_t ws_bytes, moe_stream_t stream) {
+  return moe_layer_backward_aux(cfg, x, w_router, w_gate, w_up, w_down, dout, nullptr, dx, dw_router, dbias, dw_gate,
+                                dw_up, dw_down, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_layer_backward_aux(const moe_config_t* cfg, const void* x, const void* w_router, const void* w_gate,
+                                    const void* w_up, const void* w_down, const void* dout, const float* dlogits,
+                                    void* dx, float* dw_router, float* dbias, float* dw_gate, float* dw_up,
+                                    float* dw_down, void* ws, size_t ws_bytes, moe_stream_t stream) {
   Range range_("moe_layer_backward");
   moe_status_t st = check_layer_args(cfg, w_router, nullptr, w_gate, w_up, w_down, ws, ws_bytes);
   if (st != MOE_OK) return st;
   if (!train_supported(*cfg)) return MOE_ERR_UNSUPPORTED;
   if (!dw_router || !dw_gate || !dw_up || !dw_down) return MOE_ERR_INVALID_ARG;
   if (!aligned16(dw_router) || !aligned16(dw_gate) || !aligned16(dw_up) || !aligned16(dw_down) ||
-      (dbias && !aligned16(dbias)))
+      (dbias && !aligned16(dbias)) || !aligned16(dlogits))
     return MOE_ERR_INVALID_ARG;
   if (cfg->T > 0 && (!x || !dout || !dx || !aligned16(x) || !aligned16(dout) || !aligned16(dx)))
     return MOE_ERR_INVALID_ARG;
@@ -988,7 +996,7 @@ moe_status_t moe_layer_backward(const moe_config_t* cfg, const void* x, const vo
     PhaseMark m(MOE_PHASE_BWD_ROUTER, stream);
     e = launch_router_bwd(c, dw_part, n_parts, slot_of, topk_idx, topk_w, w_router, dx32, x,
                           reinterpret_cast<float*>(w8 + TL.dlogits), reinterpret_cast<float*>(w8 + TL.dweight), dx,
-                          dw_router, dbias, reinterpret_cast<float*>(w8 + TL.wr_part), stream, ctx);
+                          dw_router, dbias, reinterpret_cast<float*>(w8 + TL.wr_part), stream, ctx, dlogits);
   }
   // weight gradients: the larger operand's blocks outermost, so the smaller one stays in L2
   if (e == cudaSuccess) {
@@ -1002,6 +1010,241 @@ moe_status_t moe_layer_backward(const moe_config_t* cfg, const void* x, const vo
   if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_BWD_WG_UP, stream);
     e = launch_bwd_wgrad(c, w8 + L.x_perm, c.d, w8 + TL.du, c.f, offsets, dw_up, c.d >= c.f, stream, ctx);
+  }
+  return cuda_status(e);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- training with 8-bit activation checkpoints
+namespace moe {
+namespace {
+
+// What one layer keeps from its forward to its backward.
+struct Ckpt8Layout {
+  size_t topk_idx, topk_w, logits, route, perm, slot_of, row_scale, g, u, sg, su, total;
+};
+
+Ckpt8Layout ckpt8_layout_of(const moe_config_t& c) {
+  Ckpt8Layout L;
+  const size_t rows = (size_t)slot_rows(c);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    size_t at = o;
+    o += round_up(bytes);
+    return at;
+  };
+  L.topk_idx = take(rows * 4);
+  L.topk_w = take(rows * 4);
+  L.logits = take((size_t)c.T * c.E * 4);
+  L.route = take((size_t)(3 * c.E + 1) * 4);  // counts_raw, counts_kept, offsets
+  L.perm = take(rows * 4);
+  L.slot_of = take(rows * 4);
+  L.row_scale = take(rows * 4);
+  L.g = take(rows * c.f);
+  L.u = take(rows * c.f);
+  L.sg = take(rows * (c.f / 32) * 2);
+  L.su = take(rows * (c.f / 32) * 2);
+  L.total = o;
+  return L;
+}
+
+// Scratch of one call, forward or backward (nothing in it outlives the call).
+struct Train8Layout {
+  size_t disp, x_perm, h, sum32, dout_perm, dg, du, dw_part, dlogits, dweight, wr_part, total;
+};
+
+Train8Layout train8_layout_of(const moe_config_t& c) {
+  Train8Layout L;
+  const size_t rows = (size_t)slot_rows(c);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    size_t at = o;
+    o += round_up(bytes);
+    return at;
+  };
+  L.disp = take(dispatch_ws(c));
+  L.x_perm = take(rows * c.d * 2);
+  L.h = take(rows * c.f * 2);
+  L.sum32 = take((size_t)c.T * c.d * 4);
+  L.dout_perm = take(rows * c.d * 2);
+  L.dg = take(rows * c.f * 2);
+  L.du = take(rows * c.f * 2);
+  L.dw_part = take(rows * (size_t)(c.f / 256) * 4);
+  L.dlogits = take((size_t)c.T * c.E * 4);
+  L.dweight = take(rows * 4);
+  L.wr_part = take((size_t)kRouterBwdChunks * c.E * c.d * 4);
+  L.total = o;
+  return L;
+}
+
+Codes8 codes_of(uint8_t* ckpt, const Ckpt8Layout& L) {
+  return {reinterpret_cast<int8_t*>(ckpt + L.g), reinterpret_cast<int8_t*>(ckpt + L.u),
+          reinterpret_cast<uint16_t*>(ckpt + L.sg), reinterpret_cast<uint16_t*>(ckpt + L.su)};
+}
+
+moe_status_t check_c8(const moe_config_t* cfg, const void* w_router, const float* logit_bias, const void* w_gate,
+                      const void* w_up, const void* w_down, const void* ckpt, size_t ckpt_bytes, const void* ws,
+                      size_t ws_bytes) {
+  moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (!train_supported(*cfg)) return MOE_ERR_UNSUPPORTED;
+  if (!w_router || !w_gate || !w_up || !w_down) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w_router) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down) || !aligned16(logit_bias))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  if (!ckpt || ckpt_bytes < ckpt8_layout_of(*cfg).total || !ws || ws_bytes < train8_layout_of(*cfg).total)
+    return MOE_ERR_WORKSPACE;
+  return aligned16(ckpt) && aligned16(ws) ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+size_t moe_checkpoint_size_c8(const moe_config_t* cfg) {
+  if (check_config(cfg) != MOE_OK || !train_supported(*cfg)) return 0;
+  return ckpt8_layout_of(*cfg).total;
+}
+
+size_t moe_workspace_size_train_c8(const moe_config_t* cfg) {
+  if (check_config(cfg) != MOE_OK || !train_supported(*cfg)) return 0;
+  return train8_layout_of(*cfg).total;
+}
+
+moe_status_t moe_layer_forward_train_c8(const moe_config_t* cfg, const void* x, const void* w_router,
+                                        const float* logit_bias, const void* w_gate, const void* w_up,
+                                        const void* w_down, void* out, void* ckpt, size_t ckpt_bytes, void* ws,
+                                        size_t ws_bytes, moe_stream_t stream) {
+  Range range_("moe_layer_forward_train_c8");
+  moe_status_t st = check_c8(cfg, w_router, logit_bias, w_gate, w_up, w_down, ckpt, ckpt_bytes, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x || !out || !aligned16(x) || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  Ctx ctx;
+  if ((st = get_ctx(ctx)) != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  const Ckpt8Layout L = ckpt8_layout_of(c);
+  const Train8Layout S = train8_layout_of(c);
+  uint8_t* k8 = static_cast<uint8_t*>(ckpt);
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  int32_t* topk_idx = reinterpret_cast<int32_t*>(k8 + L.topk_idx);
+  float* topk_w = reinterpret_cast<float*>(k8 + L.topk_w);
+  int32_t* route = reinterpret_cast<int32_t*>(k8 + L.route);
+  int32_t* offsets = route + 2 * c.E;
+  int32_t* perm = reinterpret_cast<int32_t*>(k8 + L.perm);
+  int32_t* slot_of = reinterpret_cast<int32_t*>(k8 + L.slot_of);
+  float* row_scale = reinterpret_cast<float*>(k8 + L.row_scale);
+  float* sum32 = reinterpret_cast<float*>(w8 + S.sum32);
+  const Codes8 codes = codes_of(k8, L);
+  cudaError_t e;
+  {
+    PhaseMark m(MOE_PHASE_FWD_ROUTER, stream);
+    e = launch_router(c, x, w_router, logit_bias, reinterpret_cast<float*>(k8 + L.logits), topk_idx, topk_w, stream,
+                      ctx);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_FWD_DISPATCH, stream);
+    e = launch_dispatch(c, capacity_of(c), topk_idx, topk_w, route, route + c.E, offsets, perm, slot_of, row_scale,
+                        reinterpret_cast<int32_t*>(w8 + S.disp), nullptr, stream, ctx);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_FWD_GATHER, stream);
+    e = launch_gather(c, x, perm, offsets, w8 + S.x_perm, stream, ctx);
+    if (e == cudaSuccess) e = launch_zero_rows(c, sum32, stream, ctx);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_FWD_GATE_UP, stream);
+    e = launch_tc_gate_up(c, w8 + S.x_perm, offsets, w_gate, w_up, w8 + S.h, stream, ctx, nullptr, nullptr, &codes);
+  }
+  // down summed straight into token order (any batch size), one rounding pass
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_FWD_DOWN, stream);
+    e = launch_tc_down_scatter(c, w8 + S.h, offsets, w_down, row_scale, perm, sum32, stream, ctx);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_FWD_COMBINE, stream);
+    e = launch_round_out(c, sum32, out, stream, ctx);
+  }
+  return cuda_status(e);
+}
+
+moe_status_t moe_layer_backward_c8(const moe_config_t* cfg, const void* x, const void* w_router, const void* w_gate,
+                                   const void* w_up, const void* w_down, const void* dout, const float* dlogits,
+                                   void* dx, void* dw_router, void* dbias, void* dw_gate, void* dw_up, void* dw_down,
+                                   const void* ckpt, size_t ckpt_bytes, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream) {
+  Range range_("moe_layer_backward_c8");
+  moe_status_t st = check_c8(cfg, w_router, nullptr, w_gate, w_up, w_down, ckpt, ckpt_bytes, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (!dw_router || !dw_gate || !dw_up || !dw_down) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dw_router) || !aligned16(dw_gate) || !aligned16(dw_up) || !aligned16(dw_down) ||
+      !aligned16(dbias) || !aligned16(dlogits))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 0 && (!x || !dout || !dx || !aligned16(x) || !aligned16(dout) || !aligned16(dx)))
+    return MOE_ERR_INVALID_ARG;
+  Ctx ctx;
+  if ((st = get_ctx(ctx)) != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (c.T == 0) {
+    // no tokens: every gradient is zero
+    const size_t w_bytes = (size_t)c.E * c.d * c.f * 2;
+    cudaError_t e = cudaMemsetAsync(dw_router, 0, (size_t)c.E * c.d * 2, stream);
+    if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, (size_t)c.E * 2, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dw_gate, 0, w_bytes, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dw_up, 0, w_bytes, stream);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dw_down, 0, w_bytes, stream);
+    return cuda_status(e);
+  }
+  const Ckpt8Layout L = ckpt8_layout_of(c);
+  const Train8Layout S = train8_layout_of(c);
+  uint8_t* k8 = const_cast<uint8_t*>(static_cast<const uint8_t*>(ckpt));  // read only
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  const int32_t* topk_idx = reinterpret_cast<const int32_t*>(k8 + L.topk_idx);
+  const float* topk_w = reinterpret_cast<const float*>(k8 + L.topk_w);
+  const int32_t* offsets = reinterpret_cast<const int32_t*>(k8 + L.route) + 2 * c.E;
+  const int32_t* perm = reinterpret_cast<const int32_t*>(k8 + L.perm);
+  const int32_t* slot_of = reinterpret_cast<const int32_t*>(k8 + L.slot_of);
+  const float* row_scale = reinterpret_cast<const float*>(k8 + L.row_scale);
+  float* dw_part = reinterpret_cast<float*>(w8 + S.dw_part);
+  float* dx32 = reinterpret_cast<float*>(w8 + S.sum32);
+  cudaError_t e;
+  {
+    PhaseMark m(MOE_PHASE_BWD_GATHER, stream);
+    e = launch_gather(c, dout, perm, offsets, w8 + S.dout_perm, stream, ctx);
+    if (e == cudaSuccess) e = launch_gather(c, x, perm, offsets, w8 + S.x_perm, stream, ctx);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_BWD_DH, stream);
+    e = launch_bwd_dh_c8(c, w8 + S.dout_perm, offsets, w_down, codes_of(k8, L), row_scale, w8 + S.dg, w8 + S.du,
+                         w8 + S.h, dw_part, stream, ctx);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_BWD_ZERO, stream);
+    e = launch_zero_rows(c, dx32, stream, ctx);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_BWD_DX, stream);
+    e = launch_bwd_dx(c, w8 + S.dg, w8 + S.du, offsets, w_gate, w_up, perm, dx32, stream, ctx);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_BWD_ROUTER, stream);
+    e = launch_router_bwd(c, dw_part, (int)(c.f / 256), slot_of, topk_idx, topk_w, w_router, dx32, x,
+                          reinterpret_cast<float*>(w8 + S.dlogits), reinterpret_cast<float*>(w8 + S.dweight), dx,
+                          dw_router, dbias, reinterpret_cast<float*>(w8 + S.wr_part), stream, ctx, dlogits, true);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_BWD_WG_DOWN, stream);
+    e = launch_bwd_wgrad(c, w8 + S.h, c.f, w8 + S.dout_perm, c.d, offsets, dw_down, c.f >= c.d, stream, ctx, true);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_BWD_WG_GATE, stream);
+    e = launch_bwd_wgrad(c, w8 + S.x_perm, c.d, w8 + S.dg, c.f, offsets, dw_gate, c.d >= c.f, stream, ctx, true);
+  }
+  if (e == cudaSuccess) {
+    PhaseMark m(MOE_PHASE_BWD_WG_UP, stream);
+    e = launch_bwd_wgrad(c, w8 + S.x_perm, c.d, w8 + S.du, c.f, offsets, dw_up, c.d >= c.f, stream, ctx, true);
   }
   return cuda_status(e);
 }

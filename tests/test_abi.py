@@ -349,3 +349,52 @@ def test_balance_loss_binding_checks(moe):
         moe.balance_loss(c, lg, idx, token_mask=torch.ones(3, dtype=torch.bool))
     with pytest.raises(ValueError, match="seq_offsets"):
         moe.balance_loss(c, lg, idx, seq_offsets=torch.zeros(1, dtype=torch.int32))
+
+
+def test_checkpointed_training_arguments_checked_before_launch(moe):
+    P = ctypes.c_void_p
+    c = _cfg(moe, T=64, d=256, f=512, dtype="bf16")
+    nk, nw = moe.checkpoint_size_c8(c), moe.workspace_size_train_c8(c)
+    # codes and scales of G and U, and the routing; far below the bf16 pair's workspace
+    assert nk >= 2 * 128 * 512 * (1 + 2 / 32) and nk < 1.3 * 2 * 128 * 512 and nw > 0
+    for bad in (_cfg(moe, T=64, d=128, f=512, dtype="bf16"), _cfg(moe, T=64, d=256, f=384, dtype="bf16"),
+                _cfg(moe, T=64, d=256, f=512, dtype="f32"), _cfg(moe, T=64, d=256, f=512, dtype="bf16", E=4)):
+        assert moe.checkpoint_size_c8(bad) == 0 and moe.workspace_size_train_c8(bad) == 0
+    p, odd = P(256), P(264)  # never dereferenced
+
+    def fwd(cfg=c, x=p, wr=p, bias=None, wg=p, wu=p, wd=p, out=p, ck=p, n=nk, ws=p, m=nw):
+        return moe.STATUS[moe.lib.moe_layer_forward_train_c8(cfg.ref, x, wr, bias, wg, wu, wd, out, ck, n, ws, m, None)]
+
+    def bwd(cfg=c, x=p, wr=p, wg=p, wu=p, wd=p, do=p, dl=None, dx=p, dwr=p, db=None, dg=p, du=p, dd=p, ck=p, n=nk, ws=p,
+            m=nw):
+        return moe.STATUS[moe.lib.moe_layer_backward_c8(cfg.ref, x, wr, wg, wu, wd, do, dl, dx, dwr, db, dg, du, dd, ck, n,
+                                                        ws, m, None)]
+
+    for call in (fwd, bwd):
+        assert call(cfg=_cfg(moe, T=64, d=256, f=384, dtype="bf16")) == "MOE_ERR_UNSUPPORTED"
+        assert call(n=nk - 1) == call(m=nw - 1) == call(ck=None) == call(ws=None) == "MOE_ERR_WORKSPACE"
+        for k in ("x", "wr", "wg", "wu", "wd"):
+            assert call(**{k: None}) == call(**{k: odd}) == "MOE_ERR_INVALID_ARG", k
+        assert call(ck=odd) == call(ws=odd) == "MOE_ERR_INVALID_ARG"
+    assert fwd(out=None) == fwd(bias=odd) == "MOE_ERR_INVALID_ARG"
+    for k in ("do", "dx", "dwr", "dg", "du", "dd"):
+        assert bwd(**{k: None}) == bwd(**{k: odd}) == "MOE_ERR_INVALID_ARG", k
+    assert bwd(dl=odd) == bwd(db=odd) == "MOE_ERR_INVALID_ARG"
+
+
+def test_checkpoint_views_cover_the_checkpoint(moe):
+    import torch
+
+    for T in (1, 37):
+        c = _cfg(moe, T=T, d=256, f=512, dtype="bf16")
+        ck = torch.zeros(moe.checkpoint_size_c8(c), dtype=torch.uint8)
+        v = moe.checkpoint_views_c8(c, ck)
+        assert v["g_codes"].shape == (2 * T, 512) and v["u_scale"].shape == (2 * T, 16)
+        last = v["u_scale"]
+        end = last.data_ptr() - ck.data_ptr() + last.numel() * 2
+        assert ck.numel() - 256 < end <= ck.numel()
+        assert v["offsets"].numel() == 9 and v["logits"].dtype == torch.float32
+    x = torch.zeros((37, 256), dtype=torch.bfloat16)
+    w = torch.zeros((8, 256, 512), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="dlogits must"):
+        moe.layer_backward_c8(c, x, x[:8], w, w, w.view(8, 512, 256), x, ck, ck, dlogits=torch.zeros(37, 8).double())
