@@ -400,6 +400,59 @@ MOE_API moe_status_t moe_layer_forward_w8(const moe_config_t* cfg, const void* x
                                           const float* s_down, void* out, int32_t* stats, void* ws,
                                           size_t ws_bytes, moe_stream_t stream);
 
+/* 4-bit expert weights in microscaled floating point (the pages name 8-bit
+ * quantisation of the released weights and give no scheme, see
+ * moe_quantize_int8; this is the block format that the B200's tensor cores
+ * take).  Blocks of 32 values along K share a power of two:
+ *   m = max |w|, x = floor(log2 m) - 2, one more if m > 1.75 * 2^floor(log2 m),
+ *   kept in [-127, 125];  code = w / 2^x rounded to the nearest of
+ *   {0, .5, 1, 1.5, 2, 3, 4, 6} and sign (ties to the even code, more than 6 to 6)
+ * w: bf16 [E, K, N] (gate and up [E, d, f], down [E, f, d]); codes [E, N, K / 2]
+ * bytes, the code of k in the low (even k) or high nibble of byte k / 2 of
+ * channel n: bit 3 sign, bits 0-2 the index in the list; scales: the byte x +
+ * 127 of channel n and block k at [E, N / 128, K / 128, 512] [e][n / 128]
+ * [k / 128][(n % 32) * 16 + (n % 128) / 32 * 4 + k % 128 / 32].  A block that
+ * holds a NaN or an infinity gets the scale byte 255 (NaN) and decodes to NaN;
+ * a block of zeros the byte 0.  moe_dequantize_mx4 writes the values the codes
+ * stand for, exact in bf16.  cfg->dtype must be MOE_BF16, K and N multiples of
+ * 128 (MOE_ERR_UNSUPPORTED), codes 32-byte aligned. */
+MOE_API moe_status_t moe_quantize_mx4(const moe_config_t* cfg, const void* w, int64_t K, int64_t N, uint8_t* codes,
+                                      uint8_t* scales, moe_stream_t stream);
+MOE_API moe_status_t moe_dequantize_mx4(const moe_config_t* cfg, const uint8_t* codes, const uint8_t* scales,
+                                        int64_t K, int64_t N, void* w, moe_stream_t stream);
+
+/* moe_expert_ffn on 4-bit weights, any number of tokens.  Activation rows enter
+ * each product in microscaled 8-bit floating point: blocks of 32 along K of a
+ * row of x_perm, then of H (formed in fp32), share a power of two as above with
+ * x = floor(log2 m) - 8 and e4m3 elements (the largest element is at most 448,
+ * so none is cut off; relative error of an element at most 2^-4, of a row in
+ * the root mean square about 2.6%, where the 4-bit weights have about 11%):
+ *   h = silu(x^ W^_gate) * (x^ W^_up),  y = row_scale * (h^ W^_down)
+ * with fp32 accumulation.  A row block with a NaN or an infinity makes its row
+ * NaN.  c_*, s_*: codes and scales of moe_quantize_mx4; y [T*2, d] fp32.  bf16
+ * layers, d a multiple of 256 (f of 128), else MOE_ERR_UNSUPPORTED and sizes of
+ * 0.  ws: moe_expert_ffn_mx4_workspace_size bytes, laid out (256-byte aligned)
+ * as x codes [T*2, d] | x scales [R, d / 128, 512] | H codes [T*2, f] | H scales
+ * [R, f / 128, 512] | K-split partials, with R = T*2 / 128 + E: the scales of
+ * rows lie in blocks like the weights', by row tiles of 128 that start anew at
+ * each expert (expert e's first tile is the sum of ceil(rows / 128) of the
+ * experts before it; bytes of rows that a tile does not have are unspecified). */
+MOE_API size_t moe_expert_ffn_mx4_workspace_size(const moe_config_t* cfg);
+MOE_API moe_status_t moe_expert_ffn_mx4(const moe_config_t* cfg, const void* x_perm, const int32_t* offsets,
+                                        const uint8_t* c_gate, const uint8_t* s_gate, const uint8_t* c_up,
+                                        const uint8_t* s_up, const uint8_t* c_down, const uint8_t* s_down,
+                                        const float* row_scale, float* y, void* ws, size_t ws_bytes,
+                                        moe_stream_t stream);
+
+/* moe_layer_forward with 4-bit expert weights (router weight stays bf16).
+ * ws: moe_workspace_size_mx4 bytes. */
+MOE_API size_t moe_workspace_size_mx4(const moe_config_t* cfg);
+MOE_API moe_status_t moe_layer_forward_mx4(const moe_config_t* cfg, const void* x, const void* w_router,
+                                           const float* logit_bias, const uint8_t* c_gate, const uint8_t* s_gate,
+                                           const uint8_t* c_up, const uint8_t* s_up, const uint8_t* c_down,
+                                           const uint8_t* s_down, void* out, int32_t* stats, void* ws,
+                                           size_t ws_bytes, moe_stream_t stream);
+
 /* Largest T accepted by moe_dispatch_noalloc. */
 #define MOE_NOALLOC_MAX_TOKENS (1 << 20)
 

@@ -586,3 +586,78 @@ def layer_backward_at(x, w_router, w_gate, w_up, w_down, dout, idx, w, slot_of, 
     res = {k: np.stack(v) for k, v in grads.items()}
     res.update(dx=dx + dl @ wr, dw_router=dl.T @ x64, dbias=dl.sum(axis=0), dlogits=dl, dweight=dweight)
     return res
+
+
+# ----------------------------------------------------------------------------
+# microscaled 4-bit weights, microscaled 8-bit activations
+# ----------------------------------------------------------------------------
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mx_exponent(amax, emax, top):
+    """floor(log2 amax) - emax, one more where amax > 1.75 * 2^floor(log2 amax), within [-127, top] (-127 for 0)."""
+    m, ex = np.frexp(np.asarray(amax, dtype=np.float64))  # amax = m 2^ex, m in [1/2, 1)
+    x = ex - 1 - emax + (m > 0.875)
+    return np.clip(np.where(np.asarray(amax) > 0, x, -127), -127, top)
+
+
+def mx4_blocks(w):
+    """Codes (0..15) and exponents of w [K, N] in blocks of 32 along K; exponent 128 marks a NaN block (codes 0)."""
+    v = to_f64(w)
+    K, N = v.shape
+    b = v.reshape(K // 32, 32, N)
+    bad = ~np.isfinite(b).all(axis=1)
+    b = np.where(bad[:, None], 0.0, b)
+    x = mx_exponent(np.abs(b).max(axis=1), 2, 125)
+    a = np.abs(b) / np.ldexp(1.0, x)[:, None]
+    dist = np.abs(a[..., None] - E2M1)
+    # nearest entry, on a tie the even one
+    best = np.argmin(dist * 4 + 0.0, axis=-1)
+    tie = (best < 7) & (np.take_along_axis(dist, np.minimum(best + 1, 7)[..., None], -1)[..., 0] ==
+                        np.take_along_axis(dist, best[..., None], -1)[..., 0])
+    best = np.where(tie & (best % 2 == 1), best + 1, best)
+    codes = best + 8 * np.signbit(b)
+    codes[np.broadcast_to(bad[:, None], codes.shape)] = 0
+    return codes.reshape(K, N), np.where(bad, 128, x)
+
+
+def mx4_pack(codes, x):
+    """The stored bytes of one matrix: codes [N, K / 2] and scales [N / 128, K / 128, 512]."""
+    K, N = codes.shape
+    c = codes.T.astype(np.uint8)
+    s = np.zeros((N // 128, K // 128, 512), dtype=np.uint8)
+    for n in range(N):
+        for k in range(K // 32):
+            s[n // 128, k // 4, n % 32 * 16 + n % 128 // 32 * 4 + k % 4] = x[k, n] + 127
+    return c[:, 0::2] | (c[:, 1::2] << 4), s
+
+
+def mx4_values(codes, x):
+    v = np.where(codes >= 8, -E2M1[codes % 8], E2M1[codes % 8]).reshape(len(x), 32, -1)
+    v = v * np.ldexp(1.0, np.where(x > 127, 0, x))[:, None]
+    return np.where((x > 127)[:, None], np.nan, v).reshape(codes.shape)
+
+
+def e4m3_round(a):
+    """Nearest multiple of the e4m3 step at a (3 fraction bits, steps of 2^-9 below 2^-6), ties to even."""
+    _, ex = np.frexp(np.asarray(a, dtype=np.float64))
+    step = np.ldexp(1.0, np.maximum(ex - 1, -6) - 3)
+    return np.rint(a / step) * step
+
+
+def mx8_rows(v):
+    """Rows of v in microscaled e4m3: (values, exponents [rows, K / 32])."""
+    v = np.asarray(v, dtype=np.float64)
+    b = v.reshape(v.shape[0], -1, 32)
+    x = mx_exponent(np.abs(b).max(axis=2), 8, 127)
+    s = np.ldexp(1.0, x)[:, :, None]
+    return (e4m3_round(b / s) * s).reshape(v.shape), x
+
+
+def e4m3_values(byte):
+    """Values of e4m3 codes (uint8): sign, 4 exponent bits with bias 7, 3 fraction bits; 0x7f and 0xff are NaN."""
+    byte = np.asarray(byte).astype(np.int64)
+    e, m = (byte >> 3) & 15, byte & 7
+    v = np.where(e == 0, np.ldexp(m / 8.0, -6), np.ldexp(1 + m / 8.0, e - 7))
+    v = np.where((byte & 127) == 127, np.nan, v)
+    return np.where(byte >= 128, -v, v)

@@ -29,6 +29,8 @@ __all__ = [
     "peer_import", "peer_release",
     "balance_loss_workspace_size", "balance_loss", "checkpoint_size_c8", "workspace_size_train_c8",
     "checkpoint_views_c8", "layer_forward_train_c8", "layer_backward_c8",
+    "quantize_mx4", "dequantize_mx4", "MxExperts", "expert_ffn_mx4", "mx4_workspace_views",
+    "expert_ffn_mx4_workspace_size", "workspace_size_mx4", "layer_forward_mx4",
     "GEMM_TILES", "set_gemm_tiles", "gemm_tiles", "PHASES", "profile_phases", "profile_read",
 ]
 
@@ -114,6 +116,12 @@ def _load():
         "moe_expert_ffn_w8": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "moe_layer_forward_w8": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "moe_expert_utilization": ([P, ctypes.c_int32, P, P, P], ctypes.c_int),
+        "moe_quantize_mx4": ([cfgp, P, ctypes.c_int64, ctypes.c_int64, P, P, P], ctypes.c_int),
+        "moe_dequantize_mx4": ([cfgp, P, P, ctypes.c_int64, ctypes.c_int64, P, P], ctypes.c_int),
+        "moe_expert_ffn_mx4_workspace_size": ([cfgp], sz),
+        "moe_workspace_size_mx4": ([cfgp], sz),
+        "moe_expert_ffn_mx4": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
+        "moe_layer_forward_mx4": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "moe_layer_backward_aux": ([cfgp, P, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         "moe_checkpoint_size_c8": ([cfgp], sz),
         "moe_workspace_size_train_c8": ([cfgp], sz),
@@ -774,6 +782,137 @@ def layer_forward_w8(cfg: Config, x, w_router, qw: QuantizedExperts, logit_bias=
     _check(lib.moe_layer_forward_w8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias), *qw.ptrs(),
                                     _dev_ptr(out), _dev_ptr(stats), _dev_ptr(ws), ws.numel(),
                                     _stream(stream, x.device)), "moe_layer_forward_w8")
+    return out
+
+
+def quantize_mx4(cfg: Config, w, codes=None, scales=None, stream=None):
+    """Microscaled 4-bit codes [E, N, K / 2] and scales [E, N / 128, K / 128, 512] of expert weights w [E, K, N]
+    (bf16, ``moe_quantize_mx4``)."""
+    if w.dim() != 3 or w.dtype != torch.bfloat16 or w.shape[0] != cfg.E:
+        raise ValueError(f"w must be bf16 [{cfg.E}, K, N]")
+    E, K, N = w.shape
+    if codes is None:
+        codes = _empty((E, N, K // 2), torch.uint8, w)
+    if scales is None:
+        scales = _empty((E, N // 128, K // 128, 512), torch.uint8, w)
+    _expect("codes", codes, E * N * (K // 2), torch.uint8)
+    _expect("scales", scales, E * (N // 128) * (K // 128) * 512, torch.uint8)
+    _same_device(w, codes, scales)
+    with torch.cuda.device(w.device):
+        _check(lib.moe_quantize_mx4(cfg.ref, _dev_ptr(w), K, N, _dev_ptr(codes), _dev_ptr(scales),
+                                    _stream(stream, w.device)), "moe_quantize_mx4")
+    return codes, scales
+
+
+def _mx4_shape(cfg, codes, scales):
+    """(K, N) of a matrix from its codes [E, N, K / 2], the scales checked against it."""
+    if codes.dim() != 3 or codes.dtype != torch.uint8 or codes.shape[0] != cfg.E:
+        raise ValueError(f"codes must be uint8 [{cfg.E}, N, K / 2]")
+    N, K = codes.shape[1], 2 * codes.shape[2]
+    _expect("scales", scales, cfg.E * (N // 128) * (K // 128) * 512, torch.uint8)
+    return K, N
+
+
+def dequantize_mx4(cfg: Config, codes, scales, out=None, stream=None):
+    """The weights [E, K, N] in bf16 that quantize_mx4's codes and scales stand for (exact)."""
+    K, N = _mx4_shape(cfg, codes, scales)
+    if out is None:
+        out = _empty((cfg.E, K, N), torch.bfloat16, codes)
+    _expect("out", out, cfg.E * K * N, torch.bfloat16)
+    _same_device(codes, scales, out)
+    with torch.cuda.device(codes.device):
+        _check(lib.moe_dequantize_mx4(cfg.ref, _dev_ptr(codes), _dev_ptr(scales), K, N, _dev_ptr(out),
+                                      _stream(stream, codes.device)), "moe_dequantize_mx4")
+    return out
+
+
+class MxExperts:
+    """Microscaled 4-bit expert weights of one layer: codes and scales of gate, up and down."""
+
+    def __init__(self, cfg: Config, w_gate, w_up, w_down, stream=None):
+        self.c_gate, self.s_gate = quantize_mx4(cfg, w_gate, stream=stream)
+        self.c_up, self.s_up = quantize_mx4(cfg, w_up, stream=stream)
+        self.c_down, self.s_down = quantize_mx4(cfg, w_down, stream=stream)
+
+    @classmethod
+    def from_codes(cls, c_gate, s_gate, c_up, s_up, c_down, s_down):
+        """From arrays already in the library's layout (a checkpoint of quantised weights)."""
+        q = cls.__new__(cls)
+        q.c_gate, q.s_gate, q.c_up, q.s_up, q.c_down, q.s_down = c_gate, s_gate, c_up, s_up, c_down, s_down
+        return q
+
+    def tensors(self):
+        return (self.c_gate, self.s_gate, self.c_up, self.s_up, self.c_down, self.s_down)
+
+    def check(self, cfg: Config):
+        for name, c, s, kn in (("gate", self.c_gate, self.s_gate, (cfg.d, cfg.f)), ("up", self.c_up, self.s_up,
+                               (cfg.d, cfg.f)), ("down", self.c_down, self.s_down, (cfg.f, cfg.d))):
+            if _mx4_shape(cfg, c, s) != kn:
+                raise ValueError(f"{name} weights are [K, N] = {list(_mx4_shape(cfg, c, s))}, the layer needs {list(kn)}")
+
+    def ptrs(self):
+        return [_dev_ptr(t) for t in self.tensors()]
+
+
+def expert_ffn_mx4_workspace_size(cfg: Config) -> int:
+    return lib.moe_expert_ffn_mx4_workspace_size(cfg.ref)
+
+
+def mx4_workspace_views(cfg: Config, ws):
+    """Named views into the scratch of expert_ffn_mx4 (layout stated in include/moe.h): the e4m3 codes and scale
+    blocks of the grouped rows of x and of H."""
+    rows, d, f = cfg.T * cfg.top_k, cfg.d, cfg.f
+    R = rows // 128 + cfg.E
+    spec = [("x_codes", (rows, d)), ("x_scales", (R, d // 128, 512)), ("h_codes", (rows, f)),
+            ("h_scales", (R, f // 128, 512))]
+    flat = ws.view(torch.uint8).view(-1)
+    views, o = {}, 0
+    for name, shape in spec:
+        n = math.prod(shape)
+        views[name] = flat[o:o + n].view(shape)
+        o += _round256(n)
+    return views
+
+
+def expert_ffn_mx4(cfg: Config, x_perm, offsets, qw: MxExperts, row_scale=None, y=None, ws=None, stream=None):
+    """SwiGLU experts with 4-bit weights over the grouped rows (``moe_expert_ffn_mx4``).  Returns y [T*2, d] fp32."""
+    qw.check(cfg)
+    rows = cfg.T * cfg.top_k
+    if y is None:
+        y = _empty((rows, cfg.d), torch.float32, x_perm)
+    if ws is None:
+        ws = _empty((max(expert_ffn_mx4_workspace_size(cfg), 1),), torch.uint8, x_perm)
+    _expect("x_perm", x_perm, rows * cfg.d, cfg.torch_dtype)
+    _expect("offsets", offsets, cfg.E + 1, torch.int32)
+    _expect("row_scale", row_scale, rows, torch.float32)
+    _expect("y", y, rows * cfg.d, torch.float32)
+    _same_device(x_perm, offsets, row_scale, y, ws, *qw.tensors())
+    with torch.cuda.device(x_perm.device):
+        _check(lib.moe_expert_ffn_mx4(cfg.ref, _dev_ptr(x_perm), _dev_ptr(offsets), *qw.ptrs(), _dev_ptr(row_scale),
+                                      _dev_ptr(y), _dev_ptr(ws), _nbytes(ws), _stream(stream, x_perm.device)),
+               "moe_expert_ffn_mx4")
+    return y
+
+
+def workspace_size_mx4(cfg: Config) -> int:
+    return lib.moe_workspace_size_mx4(cfg.ref)
+
+
+def layer_forward_mx4(cfg: Config, x, w_router, qw: MxExperts, logit_bias=None, out=None, stats=None, ws=None,
+                      stream=None):
+    """The whole layer with 4-bit expert weights, any number of tokens; returns out [T, d]."""
+    _expect_layer(cfg, x=x, w_router=w_router, logit_bias=logit_bias, out=out)
+    qw.check(cfg)
+    if out is None:
+        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x)
+    if ws is None:
+        ws = _empty((max(workspace_size_mx4(cfg), 1),), torch.uint8, x)
+    _expect("stats", stats, 3 * cfg.E + 2, torch.int32)
+    _same_device(x, w_router, logit_bias, out, stats, ws, *qw.tensors())
+    with torch.cuda.device(x.device):
+        _check(lib.moe_layer_forward_mx4(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias), *qw.ptrs(),
+                                         _dev_ptr(out), _dev_ptr(stats), _dev_ptr(ws), _nbytes(ws),
+                                         _stream(stream, x.device)), "moe_layer_forward_mx4")
     return out
 
 

@@ -1,0 +1,533 @@
+// Expert GEMMs on microscaled 4-bit weights and 8-bit activations, on the
+// block-scaled tcgen05 MMA (kind::mxf8f6f4: e4m3 rows x e2m1 weights, one e8m0
+// scale for 32 values along K on both sides, fp32 accumulation).
+//
+//   gate/up : H[r, n] = silu(sum_k x^ g^) * (sum_k x^ u^), 128 gate and the 128
+//             matching up columns of a tile in one 128 x 256 accumulator; the
+//             epilogue holds 32 consecutive columns of a row per thread, one
+//             block of the next GEMM's K, so it writes H as e4m3 codes and
+//             scales without an exchange between threads.
+//   down    : Y[r, n] = row_scale[r] * sum_k h^ d^, 256 columns; added into the
+//             tokens' fp32 sums (two terms a token: the order does not matter),
+//             or stored as K-split partials where there are few rows.
+//
+// The weights stay 4 bits until the tensor core: TMA reads packed codes and
+// spreads 16 of them over 16 bytes of shared memory (8 bytes of padding), the
+// form in which the MMA takes 4-bit operands beside 8-bit ones, so no thread
+// decodes anything.  Memory traffic is 0.53 bytes a weight, which bounds calls
+// of few rows; the MMA runs at twice the bf16 rate, which bounds the others.
+//
+// TMEM: two 128 x 256 fp32 accumulators would fill all 512 columns and leave
+// none for the scales, so the second starts 32 columns early, [224, 480), and
+// the scales live in [480, 512) (two sets of 16: 4 columns for the rows, 8 for
+// the weights).  The epilogue reads the 32 shared columns first and releases
+// them; the next tile's MMAs start then, while the rest is still being read.
+//
+// Row tiles of 128; a tile with at most 96 rows loads its rows in boxes of 32,
+// so that a decode tile moves 4 KB of rows beside 17 KB of weights a stage.
+// Rows past an expert's end are computed from whatever is there and never
+// stored (rows of an MMA are independent).  Schedule, roles and bounded waits as
+// in the bf16 GEMMs (ffn_tc.cu): persistent CTAs, warp 0 TMA, warp 1 MMA, warps
+// 2-5 epilogue.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace ptx;
+
+constexpr int kE = 8;
+constexpr int BM = 128;
+constexpr int BK = 128;
+constexpr int kThreads = 192;
+constexpr int kStages = 4;
+constexpr int A_BYTES = BM * BK;       // 16 KB of e4m3
+constexpr int B_HALF = 128 * BK;       // 16 KB: 128 channels x 128 codes, spread
+constexpr int B_BYTES = 2 * B_HALF;
+constexpr int B_TX = B_BYTES / 2;      // bytes that the spreading loads report: those read, not the padding
+constexpr int SF_BYTES = 3 * 512;      // rows, first and second 128 channels
+constexpr int kTmemCols = 512;
+constexpr int kAccSecond = 224;        // first column of the second accumulator
+constexpr int kScaleCol = 480;
+constexpr int SMEM_BYTES = 1024 + kStages * (A_BYTES + B_BYTES + SF_BYTES) + 256;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+
+enum Mode { kGateUp = 0, kDownSum = 1, kDownParts = 2 };
+
+struct MxArgs {
+  const int32_t* offsets;    // [E + 1]
+  int64_t rows_alloc;
+  int n_tiles;               // gate/up: f / 128;  down: d / 256
+  int num_kb;                // K / 128
+  int splits;                // K splits (kDownParts; 1 otherwise)
+  const uint8_t* a_scales;   // [row tiles][K / 128][512]
+  const uint8_t* b_scales0;  // [E][N / 128][K / 128][512]
+  const uint8_t* b_scales1;  // gate/up: of the up weights
+  int nb_scales;             // N / 128
+  uint8_t* h;                // gate/up: codes [rows, f]
+  uint8_t* h_scales;         // gate/up: [row tiles][f / 128][512]
+  float* out;                // down: sums [T, d] or partials [splits][rows][d]
+  int64_t ld;                // gate/up: f;  down: d
+  const float* row_scale;    // down; NULL means 1
+  const int32_t* perm;       // kDownSum
+  int64_t n_tok;
+  int* err;
+};
+
+struct Sched {
+  int offs[kE + 1];
+  int mt[kE];
+  int tile0[kE];             // first row tile of the expert's scales
+  int prefix[kE + 1];
+};
+
+struct Tile {
+  int e, m0, rows, nt, mtile, kb0, kb1, split;
+};
+
+__device__ __forceinline__ Tile decode_tile(const Sched& s, const MxArgs& a, int L) {
+  int e = 0;
+#pragma unroll
+  for (int k = 1; k < kE; ++k)
+    if (L >= s.prefix[k]) e = k;
+  int local = L - s.prefix[e];
+  Tile t;
+  t.e = e;
+  t.split = 0;
+  if (a.splits > 1) {
+    t.split = local % a.splits;
+    local /= a.splits;
+  }
+  t.nt = local / s.mt[e];
+  const int mi = local - t.nt * s.mt[e];
+  t.m0 = s.offs[e] + mi * BM;
+  t.mtile = s.tile0[e] + mi;
+  const int left = s.offs[e + 1] - t.m0;
+  t.rows = left < BM ? left : BM;
+  t.kb0 = a.num_kb * t.split / a.splits;
+  t.kb1 = a.num_kb * (t.split + 1) / a.splits;
+  return t;
+}
+
+__device__ __forceinline__ void build_schedule(Sched& sched, const MxArgs& args) {
+  bool ok = true;
+  int prev = 0;
+  for (int k = 0; k <= kE; ++k) {
+    const int v = args.offsets[k];
+    sched.offs[k] = v;
+    if (v < prev || (int64_t)v > args.rows_alloc) ok = false;
+    prev = v;
+  }
+  int acc = 0, tiles = 0;
+  for (int k = 0; k < kE; ++k) {
+    const int n = ok ? sched.offs[k + 1] - sched.offs[k] : 0;
+    sched.mt[k] = (n + BM - 1) / BM;
+    sched.tile0[k] = tiles;
+    sched.prefix[k] = acc;
+    tiles += sched.mt[k];
+    acc += sched.mt[k] * args.n_tiles * args.splits;
+  }
+  sched.prefix[kE] = acc;
+  if (!ok) flag_error(args.err, MOE_DEVERR_OFFSETS);
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
+                    const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                    const MxArgs args) {
+  constexpr int S = kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + S * A_BYTES;
+  uint8_t* sSF = smem + S * (A_BYTES + B_BYTES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sSF + S * SF_BYTES);
+  uint64_t* empty = full + S;
+  uint64_t* tfull = empty + S;   // accumulator 0 / 1 complete
+  uint64_t* tshared = tfull + 2; // the columns both accumulators use have been read
+  uint64_t* drain = tshared + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ Sched sched;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&tfull[0], 1);
+    mbar_init(&tfull[1], 1);
+    mbar_init(tshared, 128);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 1) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmA32);
+    prefetch_tmap(&tmB0);
+    prefetch_tmap(&tmB1);
+  }
+  pdl_wait();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  if (warp == 2 && lane == 0) build_schedule(sched, args);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = sched.prefix[kE];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      uint32_t it = 0;
+      bool ok = true;
+      const uint64_t keep = policy_evict_last();
+      for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
+        const Tile t = decode_tile(sched, args, L);
+        const int boxes = t.rows > 96 ? 0 : (t.rows + 31) / 32;
+        const uint32_t bytes = (boxes ? (uint32_t)boxes * 32 * BK : A_BYTES) + B_TX + SF_BYTES;
+        const uint8_t* sa = args.a_scales + (int64_t)t.mtile * args.num_kb * 512;
+        const int64_t eb = (int64_t)t.e * args.nb_scales;
+        const uint8_t *sb0, *sb1;
+        int n0, n1;
+        if (MODE == kGateUp) {
+          n0 = n1 = t.nt * 128;
+          sb0 = args.b_scales0 + (eb + t.nt) * args.num_kb * 512;
+          sb1 = args.b_scales1 + (eb + t.nt) * args.num_kb * 512;
+        } else {
+          n0 = t.nt * 256;
+          n1 = n0 + 128;
+          sb0 = args.b_scales0 + (eb + 2 * t.nt) * args.num_kb * 512;
+          sb1 = sb0 + (int64_t)args.num_kb * 512;
+        }
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const int s = it % S;
+          const uint32_t ph = (it / S) & 1u;
+          if (!mbar_wait(&empty[s], ph ^ 1u, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], bytes);
+          uint8_t* a = sA + s * A_BYTES;
+          uint8_t* b = sB + s * B_BYTES;
+          uint8_t* f = sSF + s * SF_BYTES;
+          tma_load_3d_hint(b, &tmB0, &full[s], kb * BK, n0, t.e, keep);
+          tma_load_3d_hint(b + B_HALF, MODE == kGateUp ? &tmB1 : &tmB0, &full[s], kb * BK, n1, t.e, keep);
+          if (boxes == 0) {
+            tma_load_2d_hint(a, &tmA, &full[s], kb * BK, t.m0, keep);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d_hint(a + i * 32 * BK, &tmA32, &full[s], kb * BK, t.m0 + 32 * i, keep);
+          }
+          bulk_load(f, sa + (int64_t)kb * 512, 512, &full[s], keep);
+          bulk_load(f + 512, sb0 + (int64_t)kb * 512, 512, &full[s], keep);
+          bulk_load(f + 1024, sb1 + (int64_t)kb * 512, 512, &full[s], keep);
+        }
+      }
+      if (!ok) {
+        flag_error(args.err, MOE_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // drain: every issued load must land before the CTA can exit
+      const uint32_t first = it > (uint32_t)S ? it - S : 0u;
+      for (uint32_t j = first; j < it; ++j) mbar_wait(&full[j % S], (j / S) & 1u, nullptr, 100000000ull);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      uint32_t it = 0, tc = 0;
+      bool ok = true, issued = false;
+      for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
+        const Tile t = decode_tile(sched, args, L);
+        // the previous tile's epilogue has read the shared columns (and so has
+        // finished the tile before, whose accumulator this one takes)
+        if (tc > 0 && !mbar_wait(tshared, (tc - 1) & 1u, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + ((tc & 1u) ? kAccSecond : 0);
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const int s = it % S;
+          const uint32_t ph = (it / S) & 1u;
+          if (!mbar_wait(&full[s], ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(sA + s * A_BYTES);
+          const uint32_t b_addr = smem_u32(sB + s * B_BYTES);
+          const uint32_t f_addr = smem_u32(sSF + s * SF_BYTES);
+          const uint32_t sfa = tmem_base + kScaleCol + (it & 1u) * 16;
+          const uint32_t sfb = sfa + 4;
+          tmem_cp_scales(sfa, plain_desc(f_addr));
+          tmem_cp_scales(sfb, plain_desc(f_addr + 512));
+          tmem_cp_scales(sfb + 4, plain_desc(f_addr + 1024));
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_mxf8f6f4(d_tmem, sw128_desc(a_addr + kk * 32, 16, 1024), sw128_desc(b_addr + kk * 32, 16, 1024),
+                          idesc_mx_e4m3_e2m1(BM, 256, kk), sfa, sfb, (kb > t.kb0 || kk > 0) ? 1u : 0u);
+          issued = true;
+          umma_commit(&empty[s]);
+        }
+        if (!ok) break;
+        umma_commit(&tfull[tc & 1u]);
+      }
+      if (!ok) {
+        flag_error(args.err, MOE_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      if (issued) {
+        // all MMAs must finish before TMEM and shared memory are released
+        umma_commit(drain);
+        mbar_wait(drain, 0, nullptr, 100000000ull);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;
+    const int r = q * 32 + lane;
+    uint32_t tc = 0;
+    for (int L = blockIdx.x; L < total; L += gridDim.x, ++tc) {
+      const Tile t = decode_tile(sched, args, L);
+      const uint32_t buf = tc & 1u;
+      if (!mbar_wait(&tfull[buf], (tc >> 1) & 1u, abort_flag)) {
+        if (lane == 0) flag_error(args.err, MOE_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      const bool valid = r < t.rows;
+      const int row = t.m0 + r;
+      const uint32_t tacc = tmem_base + (buf ? kAccSecond : 0) + ((uint32_t)(q * 32) << 16);
+      if (MODE == kGateUp) {
+        uint32_t scales = 0;
+        uint8_t* dst = args.h + (int64_t)row * args.ld + t.nt * 128;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          // the first accumulator's last 32 columns are the shared ones, the second's first 32
+          const int c = buf ? i : (i + 3) & 3;
+          uint32_t g[32], u[32];
+          tmem_ld32(tacc + c * 32, g);
+          tmem_ld32(tacc + 128 + c * 32, u);
+          tmem_wait_ld();
+          if (i == 0) {
+            tc_fence_before();
+            mbar_arrive(tshared);
+          }
+          float h[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) h[k] = silu_mul_fast(__uint_as_float(g[k]), __uint_as_float(u[k]));
+          uint32_t codes[8];
+          scales |= mx8_block(h, codes) << (8 * c);
+          if (valid) {
+            __stcs(reinterpret_cast<uint4*>(dst + c * 32), make_uint4(codes[0], codes[1], codes[2], codes[3]));
+            __stcs(reinterpret_cast<uint4*>(dst + c * 32 + 16), make_uint4(codes[4], codes[5], codes[6], codes[7]));
+          }
+        }
+        if (valid)
+          *reinterpret_cast<uint32_t*>(args.h_scales + ((int64_t)t.mtile * (args.ld / 128) + t.nt) * 512 +
+                                       mx_scale_at(r, 0)) = scales;
+      } else {
+        int64_t drow = (int64_t)t.split * args.rows_alloc + row;
+        bool store = valid;
+        if (MODE == kDownSum && valid) {
+          const int tok = __ldg(args.perm + row);
+          if (tok < 0 || (int64_t)tok >= args.n_tok) {
+            flag_error(args.err, MOE_DEVERR_SLOT_INDEX);
+            store = false;
+          }
+          drow = tok;
+        }
+        const float sc = (store && args.row_scale) ? __ldg(args.row_scale + row) : 1.0f;
+        float* dst = args.out + (store ? drow : 0) * args.ld + t.nt * 256;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          const int c = buf ? i : (i + 7) & 7;
+          uint32_t v[32];
+          tmem_ld32(tacc + c * 32, v);
+          tmem_wait_ld();
+          if (i == 0) {
+            tc_fence_before();
+            mbar_arrive(tshared);
+          }
+          if (store) {
+            float4* d4 = reinterpret_cast<float4*>(dst + c * 32);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float4 o = make_float4(sc * __uint_as_float(v[4 * k]), sc * __uint_as_float(v[4 * k + 1]),
+                                           sc * __uint_as_float(v[4 * k + 2]), sc * __uint_as_float(v[4 * k + 3]));
+              if (MODE == kDownSum)
+                atomicAdd(d4 + k, o);
+              else
+                d4[k] = o;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+    }
+  }
+
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// y[r, :] = sum over p of parts[p][r, :] in order, rows below offsets[8].
+__global__ void __launch_bounds__(256) mx4_sum_parts_kernel(const float4* __restrict__ parts, int n_parts,
+                                                           const int32_t* __restrict__ offsets, int64_t max_rows,
+                                                           int64_t row_vec, float4* __restrict__ y) {
+  pdl_wait();
+  int64_t n = offsets[kE];
+  if (n < 0 || n > max_rows) n = 0;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n * row_vec;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    float4 a = __ldg(parts + i);
+    for (int p = 1; p < n_parts; ++p) {
+      const float4 b = __ldg(parts + p * max_rows * row_vec + i);
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+    y[i] = a;
+  }
+}
+
+template <int MODE>
+cudaError_t launch_mx(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b0, const CUtensorMap& b1,
+                      const MxArgs& args, cudaStream_t s, const Ctx& ctx) {
+  auto kern = mx4_gemm_kernel<MODE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(ctx.num_sms), dim3(kThreads), SMEM_BYTES, s, no_extra_attr(), a, a32, b0, b1, args);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// [rows, K] e4m3 codes, box of 128 columns x box_rows rows.
+bool map_rows8(CUtensorMap* m, const void* base, int64_t rows, int64_t K, uint32_t box_rows) {
+  const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows};
+  const uint64_t str[1] = {(uint64_t)K};
+  const uint32_t box[2] = {BK, box_rows};
+  return encode_tmap_dtype(m, base, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
+// [E, N, K / 2] packed e2m1 codes, box of 128 codes x 128 channels, spread to 16 bytes per 16 codes.
+bool map_codes4(CUtensorMap* m, const void* base, int E, int64_t N, int64_t K) {
+  const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E};
+  const uint64_t str[2] = {(uint64_t)K / 2, (uint64_t)N * K / 2};
+  const uint32_t box[3] = {BK, 128, 1};
+  return encode_tmap_dtype(m, base, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B);
+}
+
+MxArgs base_args(const moe_config_t& c, const int32_t* offsets, const Ctx& ctx) {
+  MxArgs a = {};
+  a.offsets = offsets;
+  a.rows_alloc = slot_rows(c);
+  a.splits = 1;
+  a.n_tok = c.T;
+  a.err = ctx.err;
+  return a;
+}
+
+}  // namespace
+
+int64_t mx_row_tiles(const moe_config_t& c) { return slot_rows(c) / 128 + c.E; }
+
+// K splits of the down pass where at most 64 rows an expert are expected (the
+// weight-streaming sizes): the smallest count that leaves the last wave of tiles
+// at least 97% full, assuming min(8, rows) experts in use; else the fullest.
+int mx4_down_splits(const moe_config_t& c, int num_sms) {
+  const int64_t rows = slot_rows(c);
+  if (rows > 64 * (int64_t)c.E) return 1;
+  const int64_t base = (rows < c.E ? rows : c.E) * (c.d / 256), kb = c.f / BK;
+  int best = 1;
+  double best_eff = 0.0;
+  for (int sp = 1; sp <= kMaxDownSplits && sp <= kb; ++sp) {
+    const int64_t tiles = base * sp, waves = (tiles + num_sms - 1) / num_sms;
+    const double eff = (double)tiles / (double)(waves * num_sms);
+    if (eff > best_eff + 1e-9) {
+      best_eff = eff;
+      best = sp;
+    }
+    if (eff >= 0.97) break;
+  }
+  return best;
+}
+
+cudaError_t launch_mx4_gate_up(const moe_config_t& c, const uint8_t* x8, const uint8_t* x_scales,
+                               const int32_t* offsets, const Mx4Weights& gate, const Mx4Weights& up, uint8_t* h8,
+                               uint8_t* h_scales, cudaStream_t s, const Ctx& ctx) {
+  const int64_t rows = slot_rows(c);
+  if (rows == 0) return cudaSuccess;
+  CUtensorMap ta, ta32, tg, tu;
+  if (!map_rows8(&ta, x8, rows, c.d, 128) || !map_rows8(&ta32, x8, rows, c.d, 32) ||
+      !map_codes4(&tg, gate.codes, c.E, c.f, c.d) || !map_codes4(&tu, up.codes, c.E, c.f, c.d))
+    return cudaErrorInvalidValue;
+  MxArgs a = base_args(c, offsets, ctx);
+  a.n_tiles = (int)(c.f / 128);
+  a.num_kb = (int)(c.d / BK);
+  a.a_scales = x_scales;
+  a.b_scales0 = gate.scales;
+  a.b_scales1 = up.scales;
+  a.nb_scales = (int)(c.f / 128);
+  a.h = h8;
+  a.h_scales = h_scales;
+  a.ld = c.f;
+  return launch_mx<kGateUp>(ta, ta32, tg, tu, a, s, ctx);
+}
+
+cudaError_t launch_mx4_down(const moe_config_t& c, const uint8_t* h8, const uint8_t* h_scales, const int32_t* offsets,
+                            const Mx4Weights& down, const float* row_scale, const int32_t* perm, float* out, int splits,
+                            cudaStream_t s, const Ctx& ctx) {
+  const int64_t rows = slot_rows(c);
+  if (rows == 0) return cudaSuccess;
+  CUtensorMap ta, ta32, td;
+  if (!map_rows8(&ta, h8, rows, c.f, 128) || !map_rows8(&ta32, h8, rows, c.f, 32) ||
+      !map_codes4(&td, down.codes, c.E, c.d, c.f))
+    return cudaErrorInvalidValue;
+  MxArgs a = base_args(c, offsets, ctx);
+  a.n_tiles = (int)(c.d / 256);
+  a.num_kb = (int)(c.f / BK);
+  a.splits = splits;
+  a.a_scales = h_scales;
+  a.b_scales0 = down.scales;
+  a.nb_scales = (int)(c.d / 128);
+  a.out = out;
+  a.ld = c.d;
+  a.row_scale = row_scale;
+  a.perm = perm;
+  if (perm) return launch_mx<kDownSum>(ta, ta32, td, td, a, s, ctx);
+  return launch_mx<kDownParts>(ta, ta32, td, td, a, s, ctx);
+}
+
+cudaError_t launch_mx4_sum_parts(const moe_config_t& c, const float* parts, int n_parts, const int32_t* offsets,
+                                 float* y, cudaStream_t s, const Ctx& ctx) {
+  const int64_t rows = slot_rows(c);
+  if (rows == 0) return cudaSuccess;
+  const cudaError_t e = launch_pdl(mx4_sum_parts_kernel, dim3(ctx.num_sms * 4), dim3(256), 0, s, no_extra_attr(),
+                                   reinterpret_cast<const float4*>(parts), n_parts, offsets, rows, c.d / 4,
+                                   reinterpret_cast<float4*>(y));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace moe

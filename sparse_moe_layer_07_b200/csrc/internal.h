@@ -197,6 +197,34 @@ cudaError_t launch_wait_check(int64_t limit_ns, cudaStream_t s, const Ctx& ctx);
 // counts[e] += stats[e] and utilization[e] = counts[e] * E / sum(counts) (one block).
 cudaError_t launch_utilization(const int32_t* stats, int E, int64_t* counts, float* util, cudaStream_t s);
 
+// Microscaled 4-bit weights of one projection: packed e2m1 codes [E, N, K / 2]
+// and scales [E, N / 128, K / 128, 512].
+struct Mx4Weights {
+  const uint8_t* codes;
+  const uint8_t* scales;
+};
+cudaError_t launch_quantize_mx4(int E, const void* w, int64_t K, int64_t N, uint8_t* codes, uint8_t* scales,
+                                cudaStream_t s);
+cudaError_t launch_dequantize_mx4(int E, const uint8_t* codes, const uint8_t* scales, int64_t K, int64_t N, void* w,
+                                  cudaStream_t s);
+// Grouped rows (src[r], or src[perm[r]]) as e4m3 codes [rows, K] and scales
+// [mx_row_tiles, K / 128, 512]; K a multiple of 256.
+cudaError_t launch_quantize_rows_mx8(const void* src, const int32_t* perm, int64_t n_src, const int32_t* offsets,
+                                     int64_t max_rows, int64_t K, uint8_t* codes, uint8_t* scales, cudaStream_t s,
+                                     const Ctx& ctx);
+int64_t mx_row_tiles(const moe_config_t& c);  // most row tiles of 128 over all experts
+int mx4_down_splits(const moe_config_t& c, int num_sms);
+cudaError_t launch_mx4_gate_up(const moe_config_t& c, const uint8_t* x8, const uint8_t* x_scales,
+                               const int32_t* offsets, const Mx4Weights& gate, const Mx4Weights& up, uint8_t* h8,
+                               uint8_t* h_scales, cudaStream_t s, const Ctx& ctx);
+// perm given: adds row_scale * (h^ W^) into zeroed sums out [T, d] by token
+// (splits = 1); NULL: partials out [splits][T*k][d].
+cudaError_t launch_mx4_down(const moe_config_t& c, const uint8_t* h8, const uint8_t* h_scales, const int32_t* offsets,
+                            const Mx4Weights& down, const float* row_scale, const int32_t* perm, float* out, int splits,
+                            cudaStream_t s, const Ctx& ctx);
+cudaError_t launch_mx4_sum_parts(const moe_config_t& c, const float* parts, int n_parts, const int32_t* offsets,
+                                 float* y, cudaStream_t s, const Ctx& ctx);
+
 // Balance loss, z-loss, per-sequence counts and the gradient to the logits
 // (ws: balance_slot_bytes bytes).
 int64_t balance_slot_bytes(int64_t T, int64_t n_seq);

@@ -7,6 +7,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
@@ -1246,6 +1247,205 @@ moe_status_t moe_layer_backward_c8(const moe_config_t* cfg, const void* x, const
     PhaseMark m(MOE_PHASE_BWD_WG_UP, stream);
     e = launch_bwd_wgrad(c, w8 + S.x_perm, c.d, w8 + S.du, c.f, offsets, dw_up, c.d >= c.f, stream, ctx, true);
   }
+  return cuda_status(e);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------- microscaled 4-bit experts
+namespace moe {
+namespace {
+
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+// Scratch of the 4-bit expert FFN: rows and H as e4m3 codes with their scales,
+// and the down pass's K-split partials where the batch is small enough for splits.
+struct Mx4Layout {
+  size_t x8, x_scales, h8, h_scales, parts, total;
+};
+
+Mx4Layout mx4_layout_of(const moe_config_t& c) {
+  Mx4Layout L;
+  const size_t rows = (size_t)slot_rows(c), tiles = (size_t)mx_row_tiles(c);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    size_t at = o;
+    o += round_up(bytes);
+    return at;
+  };
+  L.x8 = take(rows * c.d);
+  L.x_scales = take(tiles * (c.d / 128) * 512);
+  L.h8 = take(rows * c.f);
+  L.h_scales = take(tiles * (c.f / 128) * 512);
+  L.parts = take(weight_streaming(c) ? kMaxDownSplits * rows * c.d * 4 : 0);
+  L.total = o;
+  return L;
+}
+
+// Workspace of moe_layer_forward_mx4: the routing, the tokens' fp32 sums, then the FFN's scratch.
+struct Mx4LayerLayout {
+  size_t topk_idx, topk_w, route, perm, slot_of, row_scale, disp, sum32, ffn, total;
+};
+
+Mx4LayerLayout mx4_layer_layout_of(const moe_config_t& c) {
+  Mx4LayerLayout L;
+  const size_t rows = (size_t)slot_rows(c);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    size_t at = o;
+    o += round_up(bytes);
+    return at;
+  };
+  L.topk_idx = take(rows * 4);
+  L.topk_w = take(rows * 4);
+  L.route = take((size_t)(3 * c.E + 1) * 4);
+  L.perm = take(rows * 4);
+  L.slot_of = take(rows * 4);
+  L.row_scale = take(rows * 4);
+  L.disp = take(dispatch_ws(c));
+  L.sum32 = take(weight_streaming(c) ? 0 : (size_t)c.T * c.d * 4);
+  L.ffn = take(mx4_layout_of(c).total);
+  L.total = o;
+  return L;
+}
+
+bool mx4_supported(const moe_config_t& c) { return c.dtype == MOE_BF16 && c.d % 256 == 0 && c.f % 128 == 0; }
+
+moe_status_t check_mx4(const moe_config_t* cfg, const Mx4Weights& g, const Mx4Weights& u, const Mx4Weights& d) {
+  moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (!mx4_supported(*cfg)) return MOE_ERR_UNSUPPORTED;
+  for (const Mx4Weights* w : {&g, &u, &d})
+    if (!w->codes || !w->scales || !aligned32(w->codes) || !aligned16(w->scales)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// Rows (x_perm, or x by slot with perm) to e4m3, gate/up, down.  Down adds into
+// the zeroed sums by token when sum32 is given (perm too), else writes `splits`
+// partials to out.
+cudaError_t run_ffn_mx4(const moe_config_t& c, const void* x, const int32_t* x_perm_idx, const int32_t* offsets,
+                        const Mx4Weights& g, const Mx4Weights& u, const Mx4Weights& d, const float* row_scale,
+                        const int32_t* sum_perm, float* out, int splits, uint8_t* ws, cudaStream_t s, const Ctx& ctx) {
+  const Mx4Layout L = mx4_layout_of(c);
+  cudaError_t e = launch_quantize_rows_mx8(x, x_perm_idx, c.T, offsets, slot_rows(c), c.d, ws + L.x8, ws + L.x_scales,
+                                           s, ctx);
+  if (e == cudaSuccess)
+    e = launch_mx4_gate_up(c, ws + L.x8, ws + L.x_scales, offsets, g, u, ws + L.h8, ws + L.h_scales, s, ctx);
+  if (e == cudaSuccess)
+    e = launch_mx4_down(c, ws + L.h8, ws + L.h_scales, offsets, d, row_scale, sum_perm, out, splits, s, ctx);
+  return e;
+}
+
+moe_status_t check_mx4_matrix(const moe_config_t* cfg, const void* w, int64_t K, int64_t N, const uint8_t* codes,
+                              const uint8_t* scales) {
+  moe_status_t st = check_config(cfg);
+  if (st != MOE_OK) return st;
+  if (cfg->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (K <= 0 || N <= 0 || K > ((int64_t)1 << 20) || N > ((int64_t)1 << 20)) return MOE_ERR_INVALID_ARG;
+  if (K % 128 != 0 || N % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (!w || !codes || !scales || !aligned16(w) || !aligned32(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" {
+
+moe_status_t moe_quantize_mx4(const moe_config_t* cfg, const void* w, int64_t K, int64_t N, uint8_t* codes,
+                              uint8_t* scales, moe_stream_t stream) {
+  Range range_("moe_quantize_mx4");
+  const moe_status_t st = check_mx4_matrix(cfg, w, K, N, codes, scales);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_quantize_mx4(cfg->E, w, K, N, codes, scales, stream));
+}
+
+moe_status_t moe_dequantize_mx4(const moe_config_t* cfg, const uint8_t* codes, const uint8_t* scales, int64_t K,
+                                int64_t N, void* w, moe_stream_t stream) {
+  Range range_("moe_dequantize_mx4");
+  const moe_status_t st = check_mx4_matrix(cfg, w, K, N, codes, scales);
+  if (st != MOE_OK) return st;
+  return cuda_status(launch_dequantize_mx4(cfg->E, codes, scales, K, N, w, stream));
+}
+
+size_t moe_expert_ffn_mx4_workspace_size(const moe_config_t* cfg) {
+  if (check_config(cfg) != MOE_OK || !mx4_supported(*cfg)) return 0;
+  return mx4_layout_of(*cfg).total;
+}
+
+size_t moe_workspace_size_mx4(const moe_config_t* cfg) {
+  if (check_config(cfg) != MOE_OK || !mx4_supported(*cfg)) return 0;
+  return mx4_layer_layout_of(*cfg).total;
+}
+
+moe_status_t moe_expert_ffn_mx4(const moe_config_t* cfg, const void* x_perm, const int32_t* offsets,
+                                const uint8_t* c_gate, const uint8_t* s_gate, const uint8_t* c_up, const uint8_t* s_up,
+                                const uint8_t* c_down, const uint8_t* s_down, const float* row_scale, float* y,
+                                void* ws, size_t ws_bytes, moe_stream_t stream) {
+  Range range_("moe_expert_ffn_mx4");
+  const Mx4Weights g{c_gate, s_gate}, u{c_up, s_up}, d{c_down, s_down};
+  moe_status_t st = check_mx4(cfg, g, u, d);
+  if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;
+  if (!x_perm || !offsets || !y || !aligned16(x_perm) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < mx4_layout_of(*cfg).total) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  Ctx ctx;
+  if ((st = get_ctx(ctx)) != MOE_OK) return st;
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  const int splits = mx4_down_splits(*cfg, ctx.num_sms);
+  float* out = splits > 1 ? reinterpret_cast<float*>(w8 + mx4_layout_of(*cfg).parts) : y;
+  cudaError_t e = run_ffn_mx4(*cfg, x_perm, nullptr, offsets, g, u, d, row_scale, nullptr, out, splits, w8, stream,
+                              ctx);
+  if (e == cudaSuccess && splits > 1) e = launch_mx4_sum_parts(*cfg, out, splits, offsets, y, stream, ctx);
+  return cuda_status(e);
+}
+
+moe_status_t moe_layer_forward_mx4(const moe_config_t* cfg, const void* x, const void* w_router,
+                                   const float* logit_bias, const uint8_t* c_gate, const uint8_t* s_gate,
+                                   const uint8_t* c_up, const uint8_t* s_up, const uint8_t* c_down,
+                                   const uint8_t* s_down, void* out, int32_t* stats, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream) {
+  Range range_("moe_layer_forward_mx4");
+  const Mx4Weights g{c_gate, s_gate}, u{c_up, s_up}, d{c_down, s_down};
+  moe_status_t st = check_mx4(cfg, g, u, d);
+  if (st != MOE_OK) return st;
+  if (!w_router || !aligned16(w_router) || !aligned16(logit_bias)) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  if (!ws || ws_bytes < mx4_layer_layout_of(*cfg).total) return MOE_ERR_WORKSPACE;
+  if (!x || !out || !aligned16(x) || !aligned16(out) || !aligned16(stats) || !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  Ctx ctx;
+  if ((st = get_ctx(ctx)) != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  const Mx4LayerLayout L = mx4_layer_layout_of(c);
+  uint8_t* w8 = static_cast<uint8_t*>(ws);
+  int32_t* topk_idx = reinterpret_cast<int32_t*>(w8 + L.topk_idx);
+  float* topk_w = reinterpret_cast<float*>(w8 + L.topk_w);
+  int32_t* route = reinterpret_cast<int32_t*>(w8 + L.route);
+  int32_t* offsets = route + 2 * c.E;
+  int32_t* perm = reinterpret_cast<int32_t*>(w8 + L.perm);
+  int32_t* slot_of = reinterpret_cast<int32_t*>(w8 + L.slot_of);
+  float* row_scale = reinterpret_cast<float*>(w8 + L.row_scale);
+  cudaError_t e = launch_router(c, x, w_router, logit_bias, nullptr, topk_idx, topk_w, stream, ctx);
+  if (e == cudaSuccess)
+    e = launch_dispatch(c, capacity_of(c), topk_idx, topk_w, route, route + c.E, offsets, perm, slot_of, row_scale,
+                        reinterpret_cast<int32_t*>(w8 + L.disp), stats, stream, ctx);
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
+  if (weight_streaming(c)) {
+    // K-split partials, added in split order by the combine
+    const int splits = mx4_down_splits(c, ctx.num_sms);
+    float* parts = reinterpret_cast<float*>(w8 + L.ffn + mx4_layout_of(c).parts);
+    e = run_ffn_mx4(c, x, perm, offsets, g, u, d, row_scale, nullptr, parts, splits, w8 + L.ffn, stream, ctx);
+    if (e == cudaSuccess)
+      e = launch_combine(c, parts, slot_of, topk_w, 1, out, stream, ctx, splits, slot_rows(c) * c.d);
+    return cuda_status(e);
+  }
+  float* sum32 = reinterpret_cast<float*>(w8 + L.sum32);
+  e = launch_zero_rows(c, sum32, stream, ctx);
+  if (e == cudaSuccess)
+    e = run_ffn_mx4(c, x, perm, offsets, g, u, d, row_scale, perm, sum32, 1, w8 + L.ffn, stream, ctx);
+  if (e == cudaSuccess) e = launch_round_out(c, sum32, out, stream, ctx);
   return cuda_status(e);
 }
 

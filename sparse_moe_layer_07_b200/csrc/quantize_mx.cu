@@ -1,0 +1,197 @@
+// Microscaled 4-bit weights and 8-bit activation rows.
+//
+// quantize: w [E, K, N] bf16 (N contiguous) -> codes [E, N, K / 2] (K
+// contiguous: the 4-bit operand of the block-scaled MMA has to be K-major) and
+// scales in blocks of 128 channels x 128 K.  Bound by memory (2 + 0.53 bytes a
+// weight).  A block of 256 threads takes 128 K x 128 channels: a thread reads
+// one 32-block of two channels (rows of 256 bytes across the block), so the
+// largest magnitude needs no exchange, and the codes turn through shared memory
+// into 64-byte runs.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "mx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRow = 80;  // bytes of a channel's 64 code bytes in shared memory (16-byte pieces, banks shifted)
+
+__global__ void __launch_bounds__(256) quantize_mx4_kernel(const __nv_bfloat16* __restrict__ w, int64_t K, int64_t N,
+                                                          uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  __shared__ __align__(16) uint8_t s_codes[128 * kRow];
+  __shared__ __align__(16) uint8_t s_scale[512];
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  const int64_t kb = blockIdx.x, nb = blockIdx.y, e = blockIdx.z;
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(w + (e * K + kb * 128 + ty * 32) * N + nb * 128) + tx;
+  uint32_t v[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v[k] = __ldcs(src + k * (N / 2));
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) m = max(m, (j == 0 ? v[k] << 16 : v[k] & 0xffff0000u) & 0x7fffffffu);
+    const int x = mx_exponent<2, kMxTopE2m1>(m);
+    const bool bad = m >= 0x7f800000u;
+    const float inv = mx_inverse(x);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        f[k] = __uint_as_float(j == 0 ? v[8 * i + k] << 16 : v[8 * i + k] & 0xffff0000u) * inv;
+      c[i] = bad ? 0u : e2m1x8(f);
+    }
+    const int n = 2 * tx + j;
+    *reinterpret_cast<uint4*>(s_codes + n * kRow + ty * 16) = make_uint4(c[0], c[1], c[2], c[3]);
+    s_scale[mx_scale_at(n, ty)] = bad ? 255 : (uint8_t)(x + 127);
+  }
+  __syncthreads();
+  uint8_t* dst = codes + ((e * N + nb * 128) * K + kb * 128) / 2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = threadIdx.x + 256 * i, n = p >> 2, q = p & 3;
+    *reinterpret_cast<uint4*>(dst + n * (K / 2) + q * 16) = *reinterpret_cast<const uint4*>(s_codes + n * kRow + q * 16);
+  }
+  if (threadIdx.x < 32)
+    reinterpret_cast<uint4*>(scales + ((e * (N / 128) + nb) * (K / 128) + kb) * 512)[threadIdx.x] =
+        reinterpret_cast<const uint4*>(s_scale)[threadIdx.x];
+}
+
+// The same tiles back: a thread decodes 32 K of two channels and writes rows of 256 bytes across the block.
+__global__ void __launch_bounds__(256) dequantize_mx4_kernel(const uint8_t* __restrict__ codes,
+                                                            const uint8_t* __restrict__ scales, int64_t K, int64_t N,
+                                                            __nv_bfloat16* __restrict__ w) {
+  __shared__ __align__(16) uint8_t s_codes[128 * kRow];
+  __shared__ __align__(16) uint8_t s_scale[512];
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+  const int64_t kb = blockIdx.x, nb = blockIdx.y, e = blockIdx.z;
+  const uint8_t* src = codes + ((e * N + nb * 128) * K + kb * 128) / 2;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = threadIdx.x + 256 * i, n = p >> 2, q = p & 3;
+    *reinterpret_cast<uint4*>(s_codes + n * kRow + q * 16) = __ldcs(reinterpret_cast<const uint4*>(src + n * (K / 2) + q * 16));
+  }
+  if (threadIdx.x < 32)
+    reinterpret_cast<uint4*>(s_scale)[threadIdx.x] =
+        __ldcs(reinterpret_cast<const uint4*>(scales + ((e * (N / 128) + nb) * (K / 128) + kb) * 512) + threadIdx.x);
+  __syncthreads();
+  uint32_t c[2][4];
+  float sc[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int n = 2 * tx + j;
+    const uint4 q = *reinterpret_cast<const uint4*>(s_codes + n * kRow + ty * 16);
+    c[j][0] = q.x; c[j][1] = q.y; c[j][2] = q.z; c[j][3] = q.w;
+    const int b = s_scale[mx_scale_at(n, ty)];
+    // 2^(b - 127), 2^-127 (b = 0) as the subnormal it is, 255 as NaN
+    sc[j] = b == 255 ? __uint_as_float(0x7fc00000u) : (b == 0 ? 0x1p-127f : __uint_as_float((uint32_t)b << 23));
+  }
+  uint32_t* dst = reinterpret_cast<uint32_t*>(w + (e * K + kb * 128 + ty * 32) * N + nb * 128) + tx;
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    dst[k * (N / 2)] = pack_bf16x2(e2m1_value(c[0][k >> 3] >> (4 * (k & 7))) * sc[0],
+                                   e2m1_value(c[1][k >> 3] >> (4 * (k & 7))) * sc[1]);
+}
+
+// Grouped rows to e4m3: row r < offsets[8] of the codes is src row r, or
+// src[perm[r]] when perm is given.  A thread takes 8 values (16 bytes), four
+// neighbours one 32-block; work items of 256 columns over all rows, so that a
+// few rows still spread over the SMs.  The scale of row r goes to the 512-byte
+// block of its tile (row tiles of 128 start anew at each expert).
+__global__ void __launch_bounds__(256) quantize_rows_mx8_kernel(const __nv_bfloat16* __restrict__ src,
+                                                               const int32_t* __restrict__ perm, int64_t n_src,
+                                                               const int32_t* __restrict__ offsets, int64_t max_rows,
+                                                               int64_t K, uint8_t* __restrict__ codes,
+                                                               uint8_t* __restrict__ scales, int* err) {
+  __shared__ int s_off[9], s_tile[9];
+  pdl_wait();
+  if (threadIdx.x == 0) {
+    bool ok = true;
+    int tile = 0;
+    for (int k = 0; k <= 8; ++k) {
+      const int v = offsets[k];
+      s_off[k] = v;
+      if (v < (k ? s_off[k - 1] : 0) || (int64_t)v > max_rows) ok = false;
+      if (k && ok) tile += (v - s_off[k - 1] + 127) / 128;
+      s_tile[k] = tile;
+    }
+    if (!ok) {
+      s_off[8] = 0;
+      flag_error(err, MOE_DEVERR_OFFSETS);
+    }
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const int per_row = (int)(K / 256);
+  const int64_t n_items = (int64_t)s_off[8] * per_row;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < n_items; i += warps) {
+    const int64_t r = i / per_row;
+    const int c = (int)(i - r * per_row);
+    int64_t sr = r;
+    if (perm) {
+      sr = __ldg(perm + r);
+      if (sr < 0 || sr >= n_src) {
+        if (lane == 0) flag_error(err, MOE_DEVERR_SLOT_INDEX);
+        continue;
+      }
+    }
+    int e = 0;
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+      if (r >= s_off[k]) e = k;
+    float v[8];
+    load8(src + sr * K + c * 256 + lane * 8, v);
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const int x = mx_exponent<8, kMxTopE4m3>(m);
+    const float inv = mx_inverse(x);
+    uint2 q = make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16,
+                         e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16);
+    const bool bad = m >= 0x7f800000u;
+    if (bad) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+    reinterpret_cast<uint2*>(codes + r * K + c * 256)[lane] = q;
+    if ((lane & 3) == 0) {
+      const int in_tile = (int)(r - s_off[e]) & 127;
+      const int64_t tile = s_tile[e] + (int)(r - s_off[e]) / 128;
+      const int kblock = c * 8 + (lane >> 2);
+      scales[(tile * (K / 128) + kblock / 4) * 512 + mx_scale_at(in_tile, kblock)] = bad ? 255 : (uint8_t)(x + 127);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_mx4(int E, const void* w, int64_t K, int64_t N, uint8_t* codes, uint8_t* scales,
+                                cudaStream_t s) {
+  dim3 grid((unsigned)(K / 128), (unsigned)(N / 128), (unsigned)E);
+  quantize_mx4_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(w), K, N, codes, scales);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dequantize_mx4(int E, const uint8_t* codes, const uint8_t* scales, int64_t K, int64_t N, void* w,
+                                  cudaStream_t s) {
+  dim3 grid((unsigned)(K / 128), (unsigned)(N / 128), (unsigned)E);
+  dequantize_mx4_kernel<<<grid, 256, 0, s>>>(codes, scales, K, N, static_cast<__nv_bfloat16*>(w));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_quantize_rows_mx8(const void* src, const int32_t* perm, int64_t n_src, const int32_t* offsets,
+                                     int64_t max_rows, int64_t K, uint8_t* codes, uint8_t* scales, cudaStream_t s,
+                                     const Ctx& ctx) {
+  if (max_rows == 0) return cudaSuccess;
+  const int64_t want = (max_rows * (K / 256) + 7) / 8, cap = (int64_t)ctx.num_sms * 8;
+  const cudaError_t e =
+      launch_pdl(quantize_rows_mx8_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s, no_extra_attr(),
+                 static_cast<const __nv_bfloat16*>(src), perm, n_src, offsets, max_rows, K, codes, scales, ctx.err);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace moe

@@ -153,6 +153,15 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Untiled copy of `bytes` (a multiple of 16, both addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
 // Pair forms (CTA pairs of a 2-CTA MMA): the tile lands in this CTA's shared
 // memory and its bytes are counted on the mbarrier at cluster-window address
 // `bar`, which may be the pair leader's.
@@ -276,6 +285,27 @@ __device__ __forceinline__ void umma_s8(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
+// D[tmem] (+)= (A scale_A) (B scale_B), 8/6/4-bit floating point in blocks of 32
+// along K with e8m0 scales in TMEM -> fp32, one CTA.  The types and the byte of
+// each scale word are in the instruction descriptor.
+__device__ __forceinline__ void umma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// Copies 512 bytes of scales (32 rows of 16 bytes) from shared memory into four
+// TMEM columns, repeated in each of the four lane quarters: byte b of column j
+// of lane i is byte 4 j + b of row i.  Ordered before later MMAs of this thread.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
 // Arrives once on `bar` when every tcgen05 op issued so far by this thread is done.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
@@ -333,6 +363,24 @@ __device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[32]) {
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The same without a swizzle: 8-row x 16-byte core matrices of 128 contiguous
+// bytes, one after the other along the rows.
+__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+
+// Instruction descriptor, kind::mxf8f6f4, K-major e4m3 A and e2m1 B with e8m0
+// scales, of which byte `sf` of each scale word is used.
+__host__ __device__ constexpr uint32_t idesc_mx_e4m3_e2m1(int M, int N, int sf) {
+  return ((uint32_t)sf << 4)                        // B: scale byte
+         | (0u << 7)                                // A format: e4m3
+         | (5u << 10)                               // B format: e2m1
+         | ((uint32_t)(N >> 3) << 17)               // N / 8
+         | (1u << 23)                               // scales: e8m0
+         | ((uint32_t)(M >> 4) << 24)               // M / 16
+         | ((uint32_t)sf << 29);                    // A: scale byte
 }
 
 // Instruction descriptor, kind::f16 with bf16 A/B and fp32 accumulator.

@@ -398,3 +398,60 @@ def test_checkpoint_views_cover_the_checkpoint(moe):
     w = torch.zeros((8, 256, 512), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="dlogits must"):
         moe.layer_backward_c8(c, x, x[:8], w, w, w.view(8, 512, 256), x, ck, ck, dlogits=torch.zeros(37, 8).double())
+
+
+def test_mx4_arguments_checked_before_launch(moe):
+    P = ctypes.c_void_p
+    p, odd, by16 = P(256), P(264), P(272)  # never dereferenced
+    c = _cfg(moe, T=64, d=256, f=384, dtype="bf16")
+
+    def quant(cfg=c, w=p, K=256, N=384, q=p, s=p):
+        a = moe.STATUS[moe.lib.moe_quantize_mx4(cfg.ref, w, K, N, q, s, None)]
+        assert a == moe.STATUS[moe.lib.moe_dequantize_mx4(cfg.ref, q, s, K, N, w, None)]
+        return a
+
+    assert quant(K=192) == quant(N=64) == quant(cfg=_cfg(moe, dtype="f32")) == "MOE_ERR_UNSUPPORTED"
+    assert quant(K=0) == quant(N=-128) == quant(K=1 << 21) == "MOE_ERR_INVALID_ARG"
+    assert quant(w=None) == quant(q=None) == quant(s=None) == quant(q=by16) == quant(s=odd) == "MOE_ERR_INVALID_ARG"
+
+    n, m = moe.expert_ffn_mx4_workspace_size(c), moe.workspace_size_mx4(c)
+    assert 0 < n < m
+    for bad in (_cfg(moe, T=64, d=128, f=384, dtype="bf16"), _cfg(moe, dtype="f32"), _cfg(moe, dtype="bf16", top_k=1)):
+        assert moe.expert_ffn_mx4_workspace_size(bad) == 0 and moe.workspace_size_mx4(bad) == 0
+
+    def ffn(cfg=c, x=p, off=p, w=(p,) * 6, y=p, ws=p, size=n):
+        return moe.STATUS[moe.lib.moe_expert_ffn_mx4(cfg.ref, x, off, *w, None, y, ws, size, None)]
+
+    def layer(cfg=c, x=p, wr=p, bias=None, w=(p,) * 6, out=p, stats=None, ws=p, size=m):
+        return moe.STATUS[moe.lib.moe_layer_forward_mx4(cfg.ref, x, wr, bias, *w, out, stats, ws, size, None)]
+
+    for call, need in ((ffn, n), (layer, m)):
+        assert call(cfg=_cfg(moe, T=64, d=128, f=384, dtype="bf16")) == "MOE_ERR_UNSUPPORTED"
+        assert call(size=need - 1) == call(ws=None) == "MOE_ERR_WORKSPACE"
+        assert call(x=None) == call(x=odd) == call(ws=odd) == "MOE_ERR_INVALID_ARG"
+        for i in range(6):
+            for v in (None, by16 if i % 2 == 0 else odd):
+                w = [p] * 6
+                w[i] = v
+                assert call(w=w) == "MOE_ERR_INVALID_ARG", (i, v)
+    assert ffn(off=None) == ffn(y=None) == layer(wr=None) == layer(out=None) == layer(bias=odd) == "MOE_ERR_INVALID_ARG"
+    assert layer(cfg=_cfg(moe, T=0, d=256, f=384, dtype="bf16"), x=None, out=None) == "MOE_OK"
+
+
+def test_mx4_binding_checks(moe):
+    import torch
+
+    c = _cfg(moe, T=4, d=256, f=384, dtype="bf16")
+    w = torch.zeros((8, 256, 384), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="w must be bf16"):
+        moe.quantize_mx4(c, w.float())
+    with pytest.raises(ValueError, match="codes must hold"):
+        moe.quantize_mx4(c, w, codes=torch.zeros(4, dtype=torch.uint8))
+    q, s = torch.zeros((8, 384, 128), dtype=torch.uint8), torch.zeros((8, 3, 2, 512), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="scales must hold"):
+        moe.dequantize_mx4(c, q, s[:4])
+    qw = moe.MxExperts.from_codes(q, s, q, s, q, s)  # down is [K, N] = [256, 384] here, not [384, 256]
+    with pytest.raises(ValueError, match="down weights"):
+        moe.layer_forward_mx4(c, torch.zeros((4, 256), dtype=torch.bfloat16), w[:, 0, :256], qw)
+    views = moe.mx4_workspace_views(c, torch.zeros(moe.expert_ffn_mx4_workspace_size(c), dtype=torch.uint8))
+    assert views["h_codes"].shape == (8, 384) and views["h_scales"].shape == (8, 3, 512)
