@@ -11,6 +11,7 @@ this package fails if the library has not been built
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -232,11 +233,17 @@ def _empty(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _same_device(first, *others):
-    """Tensors of one call live on one CUDA device (None is allowed among the others)."""
+    """Tensors of one call live on one CUDA device (None is allowed among the others): the context in which that
+    device is current."""
+    i = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != i:
             raise ValueError(f"tensors on {first.device} and {t.device} in one call")
+    return _HERE if i == torch.cuda.current_device() else torch.cuda.device(first.device)
 
 
 def abi_version() -> int:
@@ -628,8 +635,7 @@ def layer_forward_train_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, ckpt,
     _expect_layer(cfg, x, w_router, w_gate, w_up, w_down, logit_bias, out)
     if out is None:
         out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x)
-    _same_device(x, w_router, w_gate, w_up, w_down, ckpt, ws, logit_bias, out)
-    with torch.cuda.device(x.device):
+    with _same_device(x, w_router, w_gate, w_up, w_down, ckpt, ws, logit_bias, out):
         _check(lib.moe_layer_forward_train_c8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias),
                                               _dev_ptr(w_gate), _dev_ptr(w_up), _dev_ptr(w_down), _dev_ptr(out),
                                               _dev_ptr(ckpt), _nbytes(ckpt), _dev_ptr(ws), _nbytes(ws),
@@ -655,8 +661,7 @@ def layer_backward_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ckpt
         if k not in g:
             g[k] = _empty(shape, dt, x)
         _expect(k, g[k], math.prod(shape), dt)
-    _same_device(x, w_router, w_gate, w_up, w_down, dout, ckpt, ws, dlogits, *g.values())
-    with torch.cuda.device(x.device):
+    with _same_device(x, w_router, w_gate, w_up, w_down, dout, ckpt, ws, dlogits, *g.values()):
         _check(lib.moe_layer_backward_c8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(w_gate), _dev_ptr(w_up),
                                          _dev_ptr(w_down), _dev_ptr(dout), _dev_ptr(dlogits), _dev_ptr(g["dx"]),
                                          _dev_ptr(g["dw_router"]), _dev_ptr(g["dbias"]), _dev_ptr(g["dw_gate"]),
@@ -712,8 +717,7 @@ def balance_loss(cfg: Config, logits, topk_idx, token_mask=None, seq_offsets=Non
     _expect("dlogits", o["dlogits"], cfg.T * cfg.E, torch.float32)
     if ws is None:
         ws = _empty((max(balance_loss_workspace_size(cfg, n_seq), 1),), torch.uint8, logits)
-    _same_device(logits, topk_idx, token_mask, seq_offsets, ws, *o.values())
-    with torch.cuda.device(logits.device):
+    with _same_device(logits, topk_idx, token_mask, seq_offsets, ws, *o.values()):
         _check(lib.moe_balance_loss(cfg.ref, _dev_ptr(logits), _dev_ptr(topk_idx), _dev_ptr(token_mask),
                                     _dev_ptr(seq_offsets), n_seq, float(balance_coef), float(z_coef),
                                     _dev_ptr(o["counts"]), _dev_ptr(o["loss"]), _dev_ptr(o["dlogits"]), _dev_ptr(ws),
@@ -797,8 +801,7 @@ def quantize_mx4(cfg: Config, w, codes=None, scales=None, stream=None):
         scales = _empty((E, N // 128, K // 128, 512), torch.uint8, w)
     _expect("codes", codes, E * N * (K // 2), torch.uint8)
     _expect("scales", scales, E * (N // 128) * (K // 128) * 512, torch.uint8)
-    _same_device(w, codes, scales)
-    with torch.cuda.device(w.device):
+    with _same_device(w, codes, scales):
         _check(lib.moe_quantize_mx4(cfg.ref, _dev_ptr(w), K, N, _dev_ptr(codes), _dev_ptr(scales),
                                     _stream(stream, w.device)), "moe_quantize_mx4")
     return codes, scales
@@ -819,8 +822,7 @@ def dequantize_mx4(cfg: Config, codes, scales, out=None, stream=None):
     if out is None:
         out = _empty((cfg.E, K, N), torch.bfloat16, codes)
     _expect("out", out, cfg.E * K * N, torch.bfloat16)
-    _same_device(codes, scales, out)
-    with torch.cuda.device(codes.device):
+    with _same_device(codes, scales, out):
         _check(lib.moe_dequantize_mx4(cfg.ref, _dev_ptr(codes), _dev_ptr(scales), K, N, _dev_ptr(out),
                                       _stream(stream, codes.device)), "moe_dequantize_mx4")
     return out
@@ -886,8 +888,7 @@ def expert_ffn_mx4(cfg: Config, x_perm, offsets, qw: MxExperts, row_scale=None, 
     _expect("offsets", offsets, cfg.E + 1, torch.int32)
     _expect("row_scale", row_scale, rows, torch.float32)
     _expect("y", y, rows * cfg.d, torch.float32)
-    _same_device(x_perm, offsets, row_scale, y, ws, *qw.tensors())
-    with torch.cuda.device(x_perm.device):
+    with _same_device(x_perm, offsets, row_scale, y, ws, *qw.tensors()):
         _check(lib.moe_expert_ffn_mx4(cfg.ref, _dev_ptr(x_perm), _dev_ptr(offsets), *qw.ptrs(), _dev_ptr(row_scale),
                                       _dev_ptr(y), _dev_ptr(ws), _nbytes(ws), _stream(stream, x_perm.device)),
                "moe_expert_ffn_mx4")
@@ -908,8 +909,7 @@ def layer_forward_mx4(cfg: Config, x, w_router, qw: MxExperts, logit_bias=None, 
     if ws is None:
         ws = _empty((max(workspace_size_mx4(cfg), 1),), torch.uint8, x)
     _expect("stats", stats, 3 * cfg.E + 2, torch.int32)
-    _same_device(x, w_router, logit_bias, out, stats, ws, *qw.tensors())
-    with torch.cuda.device(x.device):
+    with _same_device(x, w_router, logit_bias, out, stats, ws, *qw.tensors()):
         _check(lib.moe_layer_forward_mx4(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias), *qw.ptrs(),
                                          _dev_ptr(out), _dev_ptr(stats), _dev_ptr(ws), _nbytes(ws),
                                          _stream(stream, x.device)), "moe_layer_forward_mx4")

@@ -20,14 +20,18 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kE = 8;
+constexpr int kNT = 512;       // threads of a block
 constexpr int kChunk = 1024;   // tokens of a chunk
-constexpr int kWindow = 1024;  // sequences whose counts are held at once (a chunk meets more only if most are empty)
+constexpr int kTok = kChunk / kNT;
+constexpr int kWindow = 1024;  // sequences held at once (a chunk meets more only if most are empty)
 constexpr int kSlot = 16;      // int32 of a slot: 8 counts, live tokens, padding to 64 bytes
+constexpr int kCluster = 8;    // most blocks of the one-launch form
 
 struct BalanceArgs {
   const float* logits;         // [T, E]
@@ -53,105 +57,127 @@ __device__ __forceinline__ int bound_of(const BalanceArgs& a, int s) {
   return (int)(v < 0 ? 0 : (v > a.T ? a.T : v));
 }
 
-// Number of sequences in [lo, hi) that end at or before token t, plus lo: the
-// sequence of t when t lies in one (empty sequences are passed over).
-__device__ __forceinline__ int seq_of(const BalanceArgs& a, int t, int lo, int hi) {
+struct __align__(16) Shared {
+  int hist[kWindow][kE + 1];  // pass 1: counts and live tokens; pass 2: f (as float bits) in [0, E)
+  int bound[kWindow + 1];     // offsets of the window's sequences
+  int4 red[kNT / 32][3];
+  float2 fred[kNT / 32];
+  int ired[kNT / 32];
+  int done;
+};
+
+// Sequence of every token of a chunk, in windows of kWindow sequences.
+struct Chunk {
+  int first, last;   // sequences that its tokens can belong to; last < first: none
+  int t0;            // first token
+  bool live[kTok];   // unmasked, inside the range of all sequences
+};
+
+// Sequences that end at or before token t, by the whole block: every round
+// tests kNT evenly spaced ones at once (empty sequences are passed over, so this
+// is the sequence of t when t lies in one).
+__device__ __forceinline__ int block_seq_of(const BalanceArgs& a, int t) {
+  int lo = 0, hi = a.n_seq;
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (bound_of(a, mid + 1) <= t)
-      lo = mid + 1;
-    else
-      hi = mid;
+    const int step = (hi - lo + kNT - 1) / kNT;
+    const int64_t s = lo + (int64_t)threadIdx.x * step;
+    const int c = __syncthreads_count(s < hi && bound_of(a, (int)s + 1) <= t);
+    if (step == 1) return lo + c;
+    if (c == 0) return lo;
+    const int64_t next = lo + (int64_t)c * step;
+    lo += (c - 1) * step + 1;
+    if (next < hi) hi = (int)next;
   }
   return lo;
 }
 
-template <int NT>
-struct Shared {
-  int hist[kWindow][kE + 1];  // pass 1: counts and live tokens; pass 2: f (as float bits) in [0, E)
-  int first, last;            // sequences that tokens of the chunk can belong to
-  int red[NT / 16][kSlot];
-  float2 fred[NT / 32];
-  int ired[NT / 32];
-  int done;
-};
-
-// Sequence range [first, last] of chunk c; last < first when the chunk has no token in a sequence.
-template <int NT>
-__device__ __forceinline__ void chunk_range(const BalanceArgs& a, int c, Shared<NT>& sh) {
-  if (threadIdx.x == 0 || threadIdx.x == 32) {
-    const int begin = bound_of(a, 0), end = bound_of(a, a.n_seq);
-    int64_t t0 = (int64_t)c * kChunk, t1 = t0 + kChunk;
-    if (t1 > a.T) t1 = a.T;
-    if (t0 < begin) t0 = begin;
-    if (t1 > end) t1 = end;
-    if (threadIdx.x == 0)
-      sh.first = t0 < t1 ? seq_of(a, (int)t0, 0, a.n_seq) : 0;
-    else
-      sh.last = t0 < t1 ? seq_of(a, (int)t1 - 1, 0, a.n_seq) : -1;
+__device__ __forceinline__ Chunk open_chunk(const BalanceArgs& a, int c) {
+  Chunk k;
+  k.t0 = c * kChunk;
+  const int begin = bound_of(a, 0), end = bound_of(a, a.n_seq);
+  int64_t t1 = (int64_t)k.t0 + kChunk;
+  if (t1 > end) t1 = end;
+  const int t0 = k.t0 > begin ? k.t0 : begin;
+  k.first = 0;
+  k.last = -1;
+  if (t0 < t1) {
+    k.first = a.n_seq == 1 ? 0 : block_seq_of(a, t0);
+    k.last = a.n_seq == 1 ? 0 : block_seq_of(a, (int)t1 - 1);
+    if (k.last >= a.n_seq) k.last = a.n_seq - 1;
   }
-  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    const int64_t t = (int64_t)k.t0 + j * kNT + threadIdx.x;
+    k.live[j] = t < a.T && t >= begin && t < end && (!a.mask || __ldg(a.mask + t));
+  }
+  return k;
 }
 
-// Sequence of token t of the chunk, or -1 for a token that does not count.
-template <int NT>
-__device__ __forceinline__ int live_seq(const BalanceArgs& a, int64_t t, const Shared<NT>& sh) {
-  if (t >= a.T || sh.last < sh.first) return -1;
-  if (t < bound_of(a, 0) || t >= bound_of(a, a.n_seq)) return -1;
-  if (a.mask && !__ldg(a.mask + t)) return -1;
-  const int s = seq_of(a, (int)t, sh.first, sh.last);
-  return s < a.n_seq ? s : -1;
+// Window of n sequences from w0 on: offsets to shared memory, and for each of
+// the thread's live tokens its sequence relative to w0, or -1.
+__device__ __forceinline__ void open_window(const BalanceArgs& a, const Chunk& k, int w0, int n, int (&seq)[kTok],
+                                            Shared& sh) {
+  for (int i = threadIdx.x; i <= n; i += kNT) sh.bound[i] = bound_of(a, w0 + i);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    const int t = k.t0 + j * kNT + (int)threadIdx.x;
+    seq[j] = -1;
+    if (k.live[j] && t >= sh.bound[0] && t < sh.bound[n]) {
+      int lo = 0, hi = n - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.bound[mid + 1] <= t)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      seq[j] = lo;
+    }
+  }
 }
 
 // Pass 1 over chunk c: counts of every sequence that meets the chunk, into its slot.
-template <int NT>
-__device__ __forceinline__ void count_chunk(const BalanceArgs& a, int c, Shared<NT>& sh) {
-  constexpr int kTok = kChunk / NT;
-  chunk_range(a, c, sh);
-  const int first = sh.first, last = sh.last;
-  int seq[kTok], e0[kTok], e1[kTok], live = 0;
+__device__ __forceinline__ void count_chunk(const BalanceArgs& a, int c, const Chunk& k, int (&seq)[kTok], Shared& sh) {
+  int2 e[kTok];
+  int live = 0;
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
-    const int64_t t = (int64_t)c * kChunk + j * NT + threadIdx.x;
-    seq[j] = live_seq(a, t, sh);
-    e0[j] = e1[j] = -1;
-    if (seq[j] >= 0) {
-      const int2 p = __ldg(reinterpret_cast<const int2*>(a.idx) + t);
-      e0[j] = p.x;
-      e1[j] = p.y;
-      if ((unsigned)p.x >= kE || (unsigned)p.y >= kE) flag_error(a.err, MOE_DEVERR_EXPERT_INDEX);
+    e[j] = make_int2(-1, -1);
+    if (k.live[j]) {
+      e[j] = __ldg(reinterpret_cast<const int2*>(a.idx) + k.t0 + j * kNT + threadIdx.x);
+      if ((unsigned)e[j].x >= kE || (unsigned)e[j].y >= kE) flag_error(a.err, MOE_DEVERR_EXPERT_INDEX);
       ++live;
     }
   }
-  for (int w0 = first; w0 <= last; w0 += kWindow) {
-    const int n = min(last - w0 + 1, kWindow);
-    for (int i = threadIdx.x; i < n * (kE + 1); i += NT) (&sh.hist[0][0])[i] = 0;
-    __syncthreads();
+  for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
+    const int n = min(k.last - w0 + 1, kWindow);
+    for (int i = threadIdx.x; i < n * (kE + 1); i += kNT) (&sh.hist[0][0])[i] = 0;
+    open_window(a, k, w0, n, seq, sh);  // its barrier also covers the zeros
     if (n == 1) {
       // one sequence: ballots instead of atomics on the same few words
 #pragma unroll
-      for (int e = 0; e <= kE; ++e) {
+      for (int q = 0; q <= kE; ++q) {
         int cnt = 0;
 #pragma unroll
         for (int j = 0; j < kTok; ++j)
-          cnt += e < kE ? __popc(__ballot_sync(~0u, seq[j] == w0 && e0[j] == e)) +
-                              __popc(__ballot_sync(~0u, seq[j] == w0 && e1[j] == e))
-                        : __popc(__ballot_sync(~0u, seq[j] == w0));
-        if ((threadIdx.x & 31) == 0 && cnt) atomicAdd(&sh.hist[0][e], cnt);
+          cnt += q < kE ? __popc(__ballot_sync(~0u, seq[j] == 0 && e[j].x == q)) +
+                              __popc(__ballot_sync(~0u, seq[j] == 0 && e[j].y == q))
+                        : __popc(__ballot_sync(~0u, seq[j] == 0));
+        if ((threadIdx.x & 31) == 0 && cnt) atomicAdd(&sh.hist[0][q], cnt);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < kTok; ++j) {
-        const int s = seq[j] - w0;
-        if (seq[j] >= 0 && s >= 0 && s < n) {
-          if ((unsigned)e0[j] < kE) atomicAdd(&sh.hist[s][e0[j]], 1);
-          if ((unsigned)e1[j] < kE) atomicAdd(&sh.hist[s][e1[j]], 1);
-          atomicAdd(&sh.hist[s][kE], 1);
+        if (seq[j] >= 0) {
+          if ((unsigned)e[j].x < kE) atomicAdd(&sh.hist[seq[j]][e[j].x], 1);
+          if ((unsigned)e[j].y < kE) atomicAdd(&sh.hist[seq[j]][e[j].y], 1);
+          atomicAdd(&sh.hist[seq[j]][kE], 1);
         }
       }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n * (kE + 1); i += NT) {
+    for (int i = threadIdx.x; i < n * (kE + 1); i += kNT) {
       const int s = i / (kE + 1), q = i - s * (kE + 1);
       a.slots[((int64_t)c + w0 + s) * kSlot + q] = sh.hist[s][q];
     }
@@ -162,77 +188,91 @@ __device__ __forceinline__ void count_chunk(const BalanceArgs& a, int c, Shared<
   __syncthreads();
   if (threadIdx.x == 0) {
     int sum = 0;
-    for (int w = 0; w < NT / 32; ++w) sum += sh.ired[w];
+    for (int w = 0; w < kNT / 32; ++w) sum += sh.ired[w];
     a.chunk_live[c] = sum;
   }
 }
 
-// Chunk that writes the counts of sequence s: the one that holds its first token (empty ones: the place it would have).
-__device__ __forceinline__ int owner_of(const BalanceArgs& a, int s) {
-  const int c = bound_of(a, s) / kChunk;
-  return c < a.n_chunks ? c : a.n_chunks - 1;
-}
-
-// Value q (counts, live tokens) of sequence s, summed over its slots from `at` on in steps.
-__device__ __forceinline__ int sum_slots(const BalanceArgs& a, int s, int q, int at, int step) {
-  const int lo = bound_of(a, s), hi = bound_of(a, s + 1);
-  if (lo >= hi) return 0;
-  int v = 0;
-  const int c1 = (hi - 1) / kChunk;
-#pragma unroll 4
-  for (int c = lo / kChunk + at; c <= c1; c += step) v += __ldcg(a.slots + ((int64_t)c + s) * kSlot + q);
-  return v;
-}
-
-// Pass 2 over chunk c: f of its sequences, then the tokens' losses and gradients.
-template <int NT>
-__device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, float inv_n, Shared<NT>& sh) {
-  constexpr int kTok = kChunk / NT;
-  chunk_range(a, c, sh);
-  const int first = sh.first, last = sh.last;
-  float sum_f = 0.f, sum_z = 0.f;
-  float l[kTok][kE];
-  int seq[kTok];
+__device__ __forceinline__ void load_logits(const BalanceArgs& a, const Chunk& k, float (&l)[kTok][kE]) {
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
-    const int64_t t = (int64_t)c * kChunk + j * NT + threadIdx.x;
-    seq[j] = live_seq(a, t, sh);
-    if (seq[j] >= 0) {
-      const float4* p = reinterpret_cast<const float4*>(a.logits) + 2 * t;
+    if (k.live[j]) {
+      const float4* p = reinterpret_cast<const float4*>(a.logits) + 2 * ((int64_t)k.t0 + j * kNT + threadIdx.x);
       const float4 u = __ldg(p), v = __ldg(p + 1);
       l[j][0] = u.x; l[j][1] = u.y; l[j][2] = u.z; l[j][3] = u.w;
       l[j][4] = v.x; l[j][5] = v.y; l[j][6] = v.z; l[j][7] = v.w;
-    } else if (t < a.T && a.dlogits) {
+    }
+  }
+}
+
+// Pass 2 over chunk c: f of its sequences, then the tokens' losses and
+// gradients.  same: seq and sh.bound still hold the chunk's one window.
+__device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, const Chunk& k, const float (&l)[kTok][kE],
+                                               float inv_n, bool same, int (&seq)[kTok], Shared& sh) {
+  float sum_f = 0.f, sum_z = 0.f;
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    const int64_t t = (int64_t)k.t0 + j * kNT + threadIdx.x;
+    if (!k.live[j] && t < a.T && a.dlogits) {
       float4* p = reinterpret_cast<float4*>(a.dlogits) + 2 * t;
       p[0] = p[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  for (int w0 = first; w0 <= last; w0 += kWindow) {
-    const int n = min(last - w0 + 1, kWindow);
-    // the chunk's first and last sequence may run through many chunks: all threads sum their slots
-    for (int k = 0; k < 2; ++k) {
-      const int s = k == 0 ? first : last;
-      if ((k == 1 && last == first) || s < w0 || s >= w0 + n) continue;
-      const int q = threadIdx.x & (kSlot - 1), g = threadIdx.x / kSlot;
-      sh.red[g][q] = q <= kE ? sum_slots(a, s, q, g, NT / kSlot) : 0;
+  for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
+    const int n = min(k.last - w0 + 1, kWindow);
+    if (!same) open_window(a, k, w0, n, seq, sh);
+    // the chunk's first and last sequence may run through many chunks: the block
+    // sums their slots, 16 bytes a thread, 128 slots at a time
+    for (int i = 0; i < 2; ++i) {
+      const int s = (i == 0 ? k.first : k.last) - w0;
+      if ((i == 1 && k.last == k.first) || s < 0 || s >= n) continue;
+      const int lo = sh.bound[s], hi = sh.bound[s + 1];
+      const int c0 = lo / kChunk, c1 = lo < hi ? (hi - 1) / kChunk : c0 - 1;
+      const int q = threadIdx.x & 3, g = threadIdx.x >> 2;
+      int4 v = make_int4(0, 0, 0, 0);
+      if (q < 3) {
+        const int4* p = reinterpret_cast<const int4*>(a.slots + ((int64_t)w0 + s) * kSlot) + q;
+#pragma unroll 4
+        for (int cc = c0 + g; cc <= c1; cc += kNT / 4) {
+          const int4 u = __ldcg(p + (int64_t)cc * (kSlot / 4));
+          v.x += u.x;
+          v.y += u.y;
+          v.z += u.z;
+          v.w += u.w;
+        }
+        // the eight groups of a warp, then the warps
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          v.x += __shfl_xor_sync(0x77777777u, v.x, o);
+          v.y += __shfl_xor_sync(0x77777777u, v.y, o);
+          v.z += __shfl_xor_sync(0x77777777u, v.z, o);
+          v.w += __shfl_xor_sync(0x77777777u, v.w, o);
+        }
+        if ((threadIdx.x & 31) < 3) sh.red[threadIdx.x >> 5][q] = v;
+      }
       __syncthreads();
       if (threadIdx.x <= kE) {
-        int v = 0;
-        for (int i = 0; i < NT / kSlot; ++i) v += sh.red[i][threadIdx.x];
-        sh.hist[s - w0][threadIdx.x] = v;
+        int sum = 0;
+        for (int w = 0; w < kNT / 32; ++w) sum += reinterpret_cast<const int*>(&sh.red[w][0])[threadIdx.x];
+        sh.hist[s][threadIdx.x] = sum;
       }
       __syncthreads();
     }
-    // the others lie in this chunk alone: one slot each
-    for (int i = threadIdx.x; i < n * (kE + 1); i += NT) {
-      const int s = w0 + i / (kE + 1), q = i % (kE + 1);
-      if (s != first && s != last) sh.hist[s - w0][q] = sum_slots(a, s, q, 0, 1);
+    // the others lie in this chunk alone: one slot each (an empty one has none)
+    for (int i = threadIdx.x; i < n * (kE + 1); i += kNT) {
+      const int s = i / (kE + 1), q = i - s * (kE + 1);
+      if (w0 + s != k.first && w0 + s != k.last)
+        sh.hist[s][q] = sh.bound[s] < sh.bound[s + 1] ? __ldcg(a.slots + ((int64_t)c + w0 + s) * kSlot + q) : 0;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += NT) {
-      const int s = w0 + i;
-      if (bound_of(a, s) < bound_of(a, s + 1) && owner_of(a, s) == c)
-        for (int e = 0; e < kE; ++e) a.counts[(int64_t)s * kE + e] = sh.hist[i][e];
+    for (int i = threadIdx.x; i < n; i += kNT) {
+      // the chunk that holds a sequence's first token writes its counts
+      const bool mine = sh.bound[i] < sh.bound[i + 1] && sh.bound[i] / kChunk == c;
+      if (mine) {
+        int4* o = reinterpret_cast<int4*>(a.counts + ((int64_t)w0 + i) * kE);
+        o[0] = make_int4(sh.hist[i][0], sh.hist[i][1], sh.hist[i][2], sh.hist[i][3]);
+        o[1] = make_int4(sh.hist[i][4], sh.hist[i][5], sh.hist[i][6], sh.hist[i][7]);
+      }
       const int live = sh.hist[i][kE];
       const float half = live > 0 ? 0.5f / (float)live : 0.f;
 #pragma unroll
@@ -241,8 +281,7 @@ __device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, floa
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
-      const int s = seq[j] - w0;
-      if (seq[j] < 0 || s < 0 || s >= n) continue;
+      if (seq[j] < 0) continue;
       float top = l[j][0];
 #pragma unroll
       for (int e = 1; e < kE; ++e) top = fmaxf(top, l[j][e]);
@@ -251,7 +290,7 @@ __device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, floa
       for (int e = 0; e < kE; ++e) {
         p[e] = expf(l[j][e] - top);
         total += p[e];
-        f[e] = __int_as_float(sh.hist[s][e]);
+        f[e] = __int_as_float(sh.hist[seq[j]][e]);
       }
       const float inv = 1.0f / total;
       const float lse = top + logf(total);
@@ -266,7 +305,7 @@ __device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, floa
         const float ka = a.a * (float)kE * inv_n, kb = 2.0f * a.b * inv_n * lse;
 #pragma unroll
         for (int e = 0; e < kE; ++e) p[e] *= fmaf(ka, f[e] - dot, kb);
-        float4* o = reinterpret_cast<float4*>(a.dlogits) + 2 * ((int64_t)c * kChunk + j * NT + threadIdx.x);
+        float4* o = reinterpret_cast<float4*>(a.dlogits) + 2 * ((int64_t)k.t0 + j * kNT + threadIdx.x);
         o[0] = make_float4(p[0], p[1], p[2], p[3]);
         o[1] = make_float4(p[4], p[5], p[6], p[7]);
       }
@@ -282,7 +321,7 @@ __device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, floa
   __syncthreads();
   if (threadIdx.x == 0) {
     float2 s = sh.fred[0];
-    for (int w = 1; w < NT / 32; ++w) {
+    for (int w = 1; w < kNT / 32; ++w) {
       s.x += sh.fred[w].x;
       s.y += sh.fred[w].y;
     }
@@ -290,10 +329,9 @@ __device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, floa
   }
 }
 
-// Zero counts of the empty sequences, shared out over `parts` blocks.
-template <int NT>
+// Zero counts of the empty sequences and the check of the offsets, shared out over `parts` blocks.
 __device__ __forceinline__ void empty_counts(const BalanceArgs& a, int part, int parts) {
-  for (int64_t s = (int64_t)part * NT + threadIdx.x; s < a.n_seq; s += (int64_t)parts * NT) {
+  for (int64_t s = (int64_t)part * kNT + threadIdx.x; s < a.n_seq; s += (int64_t)parts * kNT) {
     if (a.seq) {
       const int64_t lo = __ldg(a.seq + s), hi = __ldg(a.seq + s + 1);
       if (lo > hi || (s == 0 && lo < 0) || (s == a.n_seq - 1 && hi > a.T)) flag_error(a.err, MOE_DEVERR_OFFSETS);
@@ -306,67 +344,72 @@ __device__ __forceinline__ void empty_counts(const BalanceArgs& a, int part, int
 }
 
 // N, the live tokens of all chunks, by all threads of a block.
-template <int NT>
-__device__ __forceinline__ int64_t total_live(const BalanceArgs& a, Shared<NT>& sh) {
+__device__ __forceinline__ int total_live(const BalanceArgs& a, Shared& sh) {
   int v = 0;
-  for (int c = threadIdx.x; c < a.n_chunks; c += NT) v += __ldcg(a.chunk_live + c);
+  for (int c = threadIdx.x; c < a.n_chunks; c += kNT) v += __ldcg(a.chunk_live + c);
   v = __reduce_add_sync(~0u, v);
   if ((threadIdx.x & 31) == 0) sh.ired[threadIdx.x >> 5] = v;
   __syncthreads();
   int n = 0;
-  for (int w = 0; w < NT / 32; ++w) n += sh.ired[w];
+  for (int w = 0; w < kNT / 32; ++w) n += sh.ired[w];
   __syncthreads();
   return n;
 }
 
 // The losses from the chunks' sums, in double and in a fixed order, by one block.
-template <int NT>
-__device__ __forceinline__ void write_loss(const BalanceArgs& a, int64_t n, Shared<NT>& sh) {
+__device__ __forceinline__ void write_loss(const BalanceArgs& a, int n, Shared& sh) {
   double f = 0.0, z = 0.0;
-  for (int c = threadIdx.x; c < a.n_chunks; c += NT) {
+  for (int c = threadIdx.x; c < a.n_chunks; c += kNT) {
     const float2 v = __ldcg(a.chunk_sum + c);
     f += (double)v.x;
     z += (double)v.y;
   }
-  double2* red = reinterpret_cast<double2*>(&sh.hist[0][0]);
-  red[threadIdx.x] = make_double2(f, z);
-  __syncthreads();
-  for (int w = NT / 2; w > 0; w >>= 1) {
-    if ((int)threadIdx.x < w) {
-      red[threadIdx.x].x += red[threadIdx.x + w].x;
-      red[threadIdx.x].y += red[threadIdx.x + w].y;
-    }
+  if (a.n_chunks > 1) {
+    double2* red = reinterpret_cast<double2*>(&sh.hist[0][0]);
+    red[threadIdx.x] = make_double2(f, z);
     __syncthreads();
+    for (int w = kNT / 2; w > 0; w >>= 1) {
+      if ((int)threadIdx.x < w) {
+        red[threadIdx.x].x += red[threadIdx.x + w].x;
+        red[threadIdx.x].y += red[threadIdx.x + w].y;
+      }
+      __syncthreads();
+    }
+    f = red[0].x;
+    z = red[0].y;
   }
   if (threadIdx.x == 0) {
     const double inv = n > 0 ? 1.0 / (double)n : 0.0;
-    const double balance = (double)kE * red[0].x * inv, zl = red[0].y * inv;
+    const double balance = (double)kE * f * inv, zl = z * inv;
     a.loss[0] = (float)((double)a.a * balance + (double)a.b * zl);
     a.loss[1] = (float)balance;
     a.loss[2] = (float)zl;
   }
 }
 
-template <int NT>
-__global__ void __launch_bounds__(NT) balance_count_kernel(const BalanceArgs a) {
-  __shared__ __align__(16) Shared<NT> sh;
+__global__ void __launch_bounds__(kNT, 2) balance_count_kernel(const BalanceArgs a) {
+  __shared__ Shared sh;
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
-  empty_counts<NT>(a, blockIdx.x, gridDim.x);
+  empty_counts(a, blockIdx.x, gridDim.x);
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
-    count_chunk<NT>(a, c, sh);
+    int seq[kTok];
+    count_chunk(a, c, open_chunk(a, c), seq, sh);
     __syncthreads();
   }
 }
 
-template <int NT>
-__global__ void __launch_bounds__(NT) balance_gradient_kernel(const BalanceArgs a) {
-  __shared__ __align__(16) Shared<NT> sh;
+__global__ void __launch_bounds__(kNT, 2) balance_gradient_kernel(const BalanceArgs a) {
+  __shared__ Shared sh;
   pdl_wait();
-  const int64_t n = total_live<NT>(a, sh);
-  const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
+  int n = -1;
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
-    gradient_chunk<NT>(a, c, inv_n, sh);
+    const Chunk k = open_chunk(a, c);
+    float l[kTok][kE];
+    load_logits(a, k, l);
+    if (n < 0) n = total_live(a, sh);
+    int seq[kTok];
+    gradient_chunk(a, c, k, l, n > 0 ? 1.0f / (float)n : 0.f, false, seq, sh);
     __syncthreads();
   }
   // the block that finishes last adds up the chunks' sums
@@ -376,7 +419,26 @@ __global__ void __launch_bounds__(NT) balance_gradient_kernel(const BalanceArgs 
     __threadfence();
   }
   __syncthreads();
-  if (sh.done) write_loss<NT>(a, n, sh);
+  if (sh.done) write_loss(a, n, sh);
+}
+
+// Both passes in one launch, for at most kCluster chunks: one cluster, a block
+// a chunk, which keeps its logits in registers across the cluster's barrier.
+__global__ void __launch_bounds__(kNT, 1) balance_cluster_kernel(const BalanceArgs a) {
+  __shared__ Shared sh;
+  pdl_wait();
+  const int c = blockIdx.x;
+  const Chunk k = open_chunk(a, c);
+  float l[kTok][kE];
+  load_logits(a, k, l);
+  empty_counts(a, blockIdx.x, gridDim.x);
+  int seq[kTok];
+  count_chunk(a, c, k, seq, sh);
+  ptx::cluster_sync();  // the slots and live tokens of all chunks are written
+  const int n = total_live(a, sh);
+  gradient_chunk(a, c, k, l, n > 0 ? 1.0f / (float)n : 0.f, k.last - k.first < kWindow, seq, sh);
+  ptx::cluster_sync();  // and their sums
+  if (c == 0) write_loss(a, n, sh);
 }
 
 }  // namespace
@@ -407,11 +469,19 @@ cudaError_t launch_balance(const moe_config_t& c, const float* logits, const int
   a.chunk_live = reinterpret_cast<int32_t*>(a.chunk_sum + a.n_chunks);
   a.ticket = a.chunk_live + a.n_chunks;
   a.err = ctx.err;
-  const int cap = ctx.num_sms * 4;
+  if (a.n_chunks <= kCluster) {
+    cudaLaunchAttribute cl = {};
+    cl.id = cudaLaunchAttributeClusterDimension;
+    cl.val.clusterDim.x = (unsigned)a.n_chunks;
+    cl.val.clusterDim.y = cl.val.clusterDim.z = 1;
+    const cudaError_t e = launch_pdl(balance_cluster_kernel, dim3(a.n_chunks), dim3(kNT), 0, s, cl, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  const int cap = ctx.num_sms * 2;
   const int grid = a.n_chunks < cap ? a.n_chunks : cap;
-  cudaError_t e = launch_pdl(balance_count_kernel<256>, dim3(grid), dim3(256), 0, s, no_extra_attr(), a);
+  cudaError_t e = launch_pdl(balance_count_kernel, dim3(grid), dim3(kNT), 0, s, no_extra_attr(), a);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(balance_gradient_kernel<256>, dim3(grid), dim3(256), 0, s, no_extra_attr(), a);
+  e = launch_pdl(balance_gradient_kernel, dim3(grid), dim3(kNT), 0, s, no_extra_attr(), a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

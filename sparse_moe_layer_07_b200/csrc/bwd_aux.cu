@@ -240,8 +240,18 @@ __global__ void __launch_bounds__(256) router_bwd_reduce_kernel(const float* __r
                                                                Tout* __restrict__ dbias) {
   const int64_t n = (int64_t)kE * d;
   for (int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; k < n; k += (int64_t)gridDim.x * blockDim.x) {
+    // sixteen chunks' loads in flight, added in chunk order (one load at a time
+    // left the kernel waiting: 42 us at any size)
     float acc = 0.f;
-    for (int c = 0; c < chunks; ++c) acc += part[(int64_t)c * n + k];
+    int c = 0;
+    for (; c + 16 <= chunks; c += 16) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __ldg(part + (int64_t)(c + i) * n + k);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc += v[i];
+    }
+    for (; c < chunks; ++c) acc += part[(int64_t)c * n + k];
     store_as(dw_router + k, acc);
   }
   if (blockIdx.x != 0 || dbias == nullptr) return;

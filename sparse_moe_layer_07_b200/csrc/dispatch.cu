@@ -181,6 +181,95 @@ __global__ void __launch_bounds__(kBT) dispatch_rank_kernel(const int32_t* __res
   reinterpret_cast<int2*>(slot_of)[t] = make_int2(slots[0], slots[1]);
 }
 
+// The three passes in one launch, for a batch of one block (T <= kBT): the
+// block's own counts are the totals, so no histogram goes through memory.  Same
+// ranks, counts and slots as the passes above.  Small batches are bound by
+// launches (2.5 to 4 us each): one for three.
+__global__ void __launch_bounds__(kBT) dispatch_small_kernel(const int32_t* __restrict__ idx, const float* __restrict__ w,
+                                                            int64_t T, int64_t cap,
+                                                            const int32_t* __restrict__ shard_counts, int shard,
+                                                            int32_t* __restrict__ counts_raw,
+                                                            int32_t* __restrict__ counts_kept,
+                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ stats,
+                                                            int32_t* __restrict__ perm, int32_t* __restrict__ slot_of,
+                                                            float* __restrict__ row_scale, int* err) {
+  __shared__ int s_cnt[kWarps][kE];
+  __shared__ int s_raw[kE], s_kept[kE], s_off[kE];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = threadIdx.x;
+  pdl_wait();
+  int e0, e1;
+  load_pair(idx, t, T, e0, e1, err);
+  const float2 wt = t < T ? __ldg(reinterpret_cast<const float2*>(w) + t) : make_float2(0.f, 0.f);
+  const unsigned lt = (1u << lane) - 1u;
+  int pre0 = 0, pre1 = 0;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    const unsigned b0 = __ballot_sync(0xffffffffu, e0 == e);
+    const unsigned b1 = __ballot_sync(0xffffffffu, e1 == e);
+    const int p = __popc(b0 & lt) + __popc(b1 & lt);
+    if (e0 == e) pre0 = p;
+    if (e1 == e) pre1 = p + (e0 == e ? 1 : 0);
+    if (lane == 0) s_cnt[warp][e] = __popc(b0) + __popc(b1);
+  }
+  __syncthreads();
+  if (threadIdx.x < kE) {
+    const int e = threadIdx.x;
+    int raw = 0;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) raw += s_cnt[k][e];
+    int64_t left = cap - prior_count(shard_counts, shard, e);
+    if (left < 0) left = 0;
+    s_raw[e] = raw;
+    s_kept[e] = (int64_t)raw < left ? raw : (int)left;
+  }
+  __syncthreads();
+  if (threadIdx.x < kE) {
+    const int e = threadIdx.x;
+    int off = 0, kept = 0, dropped = 0;
+#pragma unroll
+    for (int k = 0; k < kE; ++k) {
+      if (k < e) off += s_kept[k];
+      kept += s_kept[k];
+      dropped += s_raw[k] - s_kept[k];
+    }
+    s_off[e] = off;
+    counts_raw[e] = s_raw[e];
+    counts_kept[e] = s_kept[e];
+    offsets[e] = off;
+    if (e == 0) offsets[kE] = kept;
+    if (stats) {
+      stats[e] = s_raw[e];
+      stats[kE + e] = s_kept[e];
+      stats[2 * kE + e] = off;
+      if (e == 0) {
+        stats[3 * kE] = kept;
+        stats[3 * kE + 1] = dropped;
+      }
+    }
+  }
+  __syncthreads();
+  if (t >= T) return;
+  int slots[2] = {-1, -1};
+  const int es[2] = {e0, e1};
+  const int pres[2] = {pre0, pre1};
+  const float ws[2] = {wt.x, wt.y};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = es[j];
+    if (e < 0) continue;
+    int r = pres[j];
+    for (int k = 0; k < warp; ++k) r += s_cnt[k][e];
+    if (r < s_kept[e]) {
+      const int s = s_off[e] + r;
+      slots[j] = s;
+      perm[s] = (int32_t)t;
+      row_scale[s] = ws[j];
+    }
+  }
+  reinterpret_cast<int2*>(slot_of)[t] = make_int2(slots[0], slots[1]);
+}
+
 // x_perm[s, :] = x[perm[s], :] for s < offsets[E]; one warp per row, 16-byte vectors.
 __global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ perm,
                                                          const int32_t* __restrict__ offsets, int64_t T,
@@ -223,6 +312,11 @@ cudaError_t launch_dispatch(const moe_config_t& c, int64_t cap, const int32_t* i
                             int shard) {
   const int64_t nblk = dispatch_blocks(c);
   cudaError_t e = cudaSuccess;
+  if (nblk == 1) {
+    e = launch_pdl(dispatch_small_kernel, dim3(1), dim3(kBT), 0, s, no_extra_attr(), idx, w, c.T, cap, shard_counts,
+                   shard, counts_raw, counts_kept, offsets, stats, perm, slot_of, row_scale, ctx.err);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
   if (nblk > 0) {
     e = launch_pdl(dispatch_hist_kernel, dim3((unsigned)nblk), dim3(kBT), 0, s, no_extra_attr(), idx, c.T, block_hist,
                    ctx.err);

@@ -412,6 +412,48 @@ __global__ void __launch_bounds__(256) mx4_sum_parts_kernel(const float4* __rest
   }
 }
 
+// out[t, :] = the token's kept slots' rows (slot 0 first), each the sum of its
+// partials in order, rounded to bf16: moe_combine with weights_applied = 1, one
+// float4 a thread, so that a few tokens fill the device (a block per token took
+// 17 us for 32 tokens of 6144, the time of its chain of loads).
+__global__ void __launch_bounds__(256) mx4_combine_kernel(const float4* __restrict__ parts, int n_parts, int64_t stride,
+                                                         const int32_t* __restrict__ slot_of, int64_t n,
+                                                         int64_t row_vec, int64_t max_slot, uint2* __restrict__ out,
+                                                         int* err) {
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  const int64_t t = i / row_vec, v = i - t * row_vec;
+  const int2 sl = __ldg(reinterpret_cast<const int2*>(slot_of) + t);
+  const int s[2] = {sl.x, sl.y};
+  float4 r[2][kMaxDownSplits];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const bool on = s[j] >= 0 && s[j] < max_slot;
+    if (s[j] >= max_slot || s[j] < -1) flag_error(err, MOE_DEVERR_SLOT_INDEX);
+#pragma unroll
+    for (int p = 0; p < kMaxDownSplits; ++p)
+      r[j][p] = on && p < n_parts ? __ldg(parts + p * stride + s[j] * row_vec + v) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float4 y = r[j][0];
+#pragma unroll
+    for (int p = 1; p < kMaxDownSplits; ++p) {
+      y.x += r[j][p].x;
+      y.y += r[j][p].y;
+      y.z += r[j][p].z;
+      y.w += r[j][p].w;
+    }
+    a.x += y.x;
+    a.y += y.y;
+    a.z += y.z;
+    a.w += y.w;
+  }
+  out[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+}
+
 template <int MODE>
 cudaError_t launch_mx(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b0, const CUtensorMap& b1,
                       const MxArgs& args, cudaStream_t s, const Ctx& ctx) {
@@ -527,6 +569,17 @@ cudaError_t launch_mx4_sum_parts(const moe_config_t& c, const float* parts, int 
   const cudaError_t e = launch_pdl(mx4_sum_parts_kernel, dim3(ctx.num_sms * 4), dim3(256), 0, s, no_extra_attr(),
                                    reinterpret_cast<const float4*>(parts), n_parts, offsets, rows, c.d / 4,
                                    reinterpret_cast<float4*>(y));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_mx4_combine(const moe_config_t& c, const float* parts, int n_parts, const int32_t* slot_of, void* out,
+                               cudaStream_t s, const Ctx& ctx) {
+  const int64_t n = c.T * c.d / 4;
+  if (n == 0) return cudaSuccess;
+  const cudaError_t e = launch_pdl(mx4_combine_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+                                   no_extra_attr(), reinterpret_cast<const float4*>(parts), n_parts,
+                                   slot_rows(c) * c.d / 4, slot_of, n, c.d / 4, slot_rows(c),
+                                   static_cast<uint2*>(out), ctx.err);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

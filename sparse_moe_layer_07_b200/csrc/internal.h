@@ -222,6 +222,9 @@ cudaError_t launch_mx4_gate_up(const moe_config_t& c, const uint8_t* x8, const u
 cudaError_t launch_mx4_down(const moe_config_t& c, const uint8_t* h8, const uint8_t* h_scales, const int32_t* offsets,
                             const Mx4Weights& down, const float* row_scale, const int32_t* perm, float* out, int splits,
                             cudaStream_t s, const Ctx& ctx);
+// out [T, d] bf16 = the tokens' kept slots' partials summed (routing weight applied).
+cudaError_t launch_mx4_combine(const moe_config_t& c, const float* parts, int n_parts, const int32_t* slot_of, void* out,
+                               cudaStream_t s, const Ctx& ctx);
 cudaError_t launch_mx4_sum_parts(const moe_config_t& c, const float* parts, int n_parts, const int32_t* offsets,
                                  float* y, cudaStream_t s, const Ctx& ctx);
 

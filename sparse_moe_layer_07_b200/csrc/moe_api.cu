@@ -1437,8 +1437,7 @@ moe_status_t moe_layer_forward_mx4(const moe_config_t* cfg, const void* x, const
     const int splits = mx4_down_splits(c, ctx.num_sms);
     float* parts = reinterpret_cast<float*>(w8 + L.ffn + mx4_layout_of(c).parts);
     e = run_ffn_mx4(c, x, perm, offsets, g, u, d, row_scale, nullptr, parts, splits, w8 + L.ffn, stream, ctx);
-    if (e == cudaSuccess)
-      e = launch_combine(c, parts, slot_of, topk_w, 1, out, stream, ctx, splits, slot_rows(c) * c.d);
+    if (e == cudaSuccess) e = launch_mx4_combine(c, parts, splits, slot_of, out, stream, ctx);
     return cuda_status(e);
   }
   float* sum32 = reinterpret_cast<float*>(w8 + L.sum32);
