@@ -18,9 +18,9 @@
 // of few rows; the MMA runs at twice the bf16 rate, which bounds the others.
 //
 // TMEM: two 128 x 256 fp32 accumulators would fill all 512 columns and leave
-// none for the scales, so the second starts 32 columns early, [224, 480), and
-// the scales live in [480, 512) (two sets of 16: 4 columns for the rows, 8 for
-// the weights).  The epilogue reads the 32 shared columns first and releases
+// none for the scales, so the second starts 48 columns early, [208, 464), and
+// the scales live in [464, 512): one set a stage, 4 columns for the rows and 8
+// for the weights.  The epilogue reads the 48 shared columns first and releases
 // them; the next tile's MMAs start then, while the rest is still being read.
 //
 // Row tiles of 128; a tile with at most 96 rows loads its rows in boxes of 32,
@@ -45,7 +45,7 @@ using namespace ptx;
 constexpr int kE = 8;
 constexpr int BM = 128;
 constexpr int BK = 128;
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;  // 10 warps: TMA, MMA, 4 epilogue, 4 scales
 constexpr int kStages = 4;
 constexpr int A_BYTES = BM * BK;       // 16 KB of e4m3
 constexpr int B_HALF = 128 * BK;       // 16 KB: 128 channels x 128 codes, spread
@@ -53,8 +53,9 @@ constexpr int B_BYTES = 2 * B_HALF;
 constexpr int B_TX = B_BYTES / 2;      // bytes that the spreading loads report: those read, not the padding
 constexpr int SF_BYTES = 3 * 512;      // rows, first and second 128 channels
 constexpr int kTmemCols = 512;
-constexpr int kAccSecond = 224;        // first column of the second accumulator
-constexpr int kScaleCol = 480;
+constexpr int kAccSecond = 208;        // first column of the second accumulator
+constexpr int kScaleCol = 464;         // kStages sets of 12 columns
+static_assert(kScaleCol + 12 * kStages <= kTmemCols, "TMEM columns");
 constexpr int SMEM_BYTES = 1024 + kStages * (A_BYTES + B_BYTES + SF_BYTES) + 256;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
@@ -153,7 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;   // accumulator 0 / 1 complete
   uint64_t* tshared = tfull + 2; // the columns both accumulators use have been read
-  uint64_t* drain = tshared + 1;
+  uint64_t* sfull = tshared + 1; // the stage's scales are in TMEM
+  uint64_t* drain = sfull + S;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Sched sched;
@@ -169,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&tfull[0], 1);
     mbar_init(&tfull[1], 1);
     mbar_init(tshared, 128);
+    for (int s = 0; s < S; ++s) mbar_init(&sfull[s], 4);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -248,55 +251,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t j = first; j < it; ++j) mbar_wait(&full[j % S], (j / S) & 1u, nullptr, 100000000ull);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      uint32_t it = 0, tc = 0;
-      bool ok = true, issued = false;
-      for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
-        const Tile t = decode_tile(sched, args, L);
-        // the previous tile's epilogue has read the shared columns (and so has
-        // finished the tile before, whose accumulator this one takes)
-        if (tc > 0 && !mbar_wait(tshared, (tc - 1) & 1u, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + ((tc & 1u) ? kAccSecond : 0);
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const int s = it % S;
-          const uint32_t ph = (it / S) & 1u;
-          if (!mbar_wait(&full[s], ph, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a_addr = smem_u32(sA + s * A_BYTES);
-          const uint32_t b_addr = smem_u32(sB + s * B_BYTES);
-          const uint32_t f_addr = smem_u32(sSF + s * SF_BYTES);
-          const uint32_t sfa = tmem_base + kScaleCol + (it & 1u) * 16;
-          const uint32_t sfb = sfa + 4;
-          tmem_cp_scales(sfa, plain_desc(f_addr));
-          tmem_cp_scales(sfb, plain_desc(f_addr + 512));
-          tmem_cp_scales(sfb + 4, plain_desc(f_addr + 1024));
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_mxf8f6f4(d_tmem, sw128_desc(a_addr + kk * 32, 16, 1024), sw128_desc(b_addr + kk * 32, 16, 1024),
-                          idesc_mx_e4m3_e2m1(BM, 256, kk), sfa, sfb, (kb > t.kb0 || kk > 0) ? 1u : 0u);
-          issued = true;
-          umma_commit(&empty[s]);
-        }
+    // -------------------------------------------------------------- MMA issuer
+    // The whole warp runs the loop and one elected lane issues: what the MMAs
+    // take is then uniform over the warp.
+    const bool lead = elect_one();
+    uint32_t it = 0, tc = 0;
+    bool ok = true;
+    for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
+      const Tile t = decode_tile(sched, args, L);
+      const int n_kb = __shfl_sync(0xffffffffu, t.kb1 - t.kb0, 0);
+      // the previous tile's epilogue has read the shared columns (and so has
+      // finished the tile before, whose accumulator this one takes)
+      if (tc > 0) ok = __all_sync(0xffffffffu, mbar_wait(tshared, (tc - 1) & 1u, abort_flag));
+      if (!ok) break;
+      const uint32_t d_tmem = tmem_base + ((tc & 1u) ? kAccSecond : 0);
+      for (int i = 0; i < n_kb; ++i, ++it) {
+        const uint32_t s = it % S, ph = (it / S) & 1u;
+        ok = __all_sync(0xffffffffu, mbar_wait2(&full[s], ph, &sfull[s], ph, abort_flag));
         if (!ok) break;
-        umma_commit(&tfull[tc & 1u]);
+        tc_fence_after();
+        const uint64_t ad = sw128_desc(smem_u32(sA + s * A_BYTES), 16, 1024);
+        const uint64_t bd = sw128_desc(smem_u32(sB + s * B_BYTES), 16, 1024);
+        const uint32_t sfa = tmem_base + kScaleCol + s * 12;
+        if (lead) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)  // 32 bytes of K further each: 2 in the descriptors' 16-byte units
+            umma_mxf8f6f4(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc_mx_e4m3_e2m1(BM, 256, kk), sfa, sfa + 4,
+                          (i > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&empty[s]);
+          if (i == n_kb - 1) umma_commit(&tfull[tc & 1u]);
+        }
+        __syncwarp();
       }
-      if (!ok) {
-        flag_error(args.err, MOE_DEVERR_TIMEOUT);
-        *abort_flag = 1;
+    }
+    if (!ok) {
+      if (lead) flag_error(args.err, MOE_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+    if (lead && it > 0) {
+      // all MMAs must finish before TMEM and shared memory are released
+      umma_commit(drain);
+      mbar_wait(drain, 0, nullptr, 100000000ull);
+    }
+    __syncwarp();
+  } else if (warp >= 6) {
+    // ---------------------------------------------------------------- scales
+    // Each stage's scales from shared memory to the stage's 12 TMEM columns: all
+    // four lane quarters hold the same 32 lanes, one warp each.  A stage whose
+    // loads have landed was released by its last MMAs, and its columns with it.
+    const int q = warp & 3;
+    uint32_t it = 0;
+    bool ok = true;
+    for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
+      const Tile t = decode_tile(sched, args, L);
+      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+        const int s = it % S;
+        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (it / S) & 1u, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const uint4* f = reinterpret_cast<const uint4*>(sSF + s * SF_BYTES) + lane;
+        const uint4 va = f[0], vb = f[32], vc = f[64];
+        const uint32_t dst = tmem_base + kScaleCol + s * 12 + ((uint32_t)(q * 32) << 16);
+        tmem_st4(dst, va);
+        tmem_st8(dst + 4, vb, vc);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfull[s]);
       }
-      if (issued) {
-        // all MMAs must finish before TMEM and shared memory are released
-        umma_commit(drain);
-        mbar_wait(drain, 0, nullptr, 100000000ull);
-      }
+    }
+    if (!ok) {
+      if (lane == 0) flag_error(args.err, MOE_DEVERR_TIMEOUT);
+      *abort_flag = 1;
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -320,13 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* dst = args.h + (int64_t)row * args.ld + t.nt * 128;
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-          // the first accumulator's last 32 columns are the shared ones, the second's first 32
-          const int c = buf ? i : (i + 3) & 3;
+          // the first accumulator's last 48 columns are the shared ones, the second's first 48
+          const int c = buf ? i : 3 - i;
           uint32_t g[32], u[32];
           tmem_ld32(tacc + c * 32, g);
           tmem_ld32(tacc + 128 + c * 32, u);
           tmem_wait_ld();
-          if (i == 0) {
+          if (i == 1) {
             tc_fence_before();
             mbar_arrive(tshared);
           }
@@ -358,11 +384,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* dst = args.out + (store ? drow : 0) * args.ld + t.nt * 256;
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-          const int c = buf ? i : (i + 7) & 7;
+          const int c = buf ? i : 7 - i;
           uint32_t v[32];
           tmem_ld32(tacc + c * 32, v);
           tmem_wait_ld();
-          if (i == 0) {
+          if (i == 1) {
             tc_fence_before();
             mbar_arrive(tshared);
           }
