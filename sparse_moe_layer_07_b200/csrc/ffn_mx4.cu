@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- MMA issuer
     // The whole warp runs the loop and one elected lane issues: what the MMAs
     // take is then uniform over the warp.
-    const bool lead = elect_one();
+    const uint32_t lead = elect_one() ? 1u : 0u;
     uint32_t it = 0, tc = 0;
     bool ok = true;
     for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
@@ -273,16 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t ad = sw128_desc(smem_u32(sA + s * A_BYTES), 16, 1024);
         const uint64_t bd = sw128_desc(smem_u32(sB + s * B_BYTES), 16, 1024);
         const uint32_t sfa = tmem_base + kScaleCol + s * 12;
-        if (lead) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)  // 32 bytes of K further each: 2 in the descriptors' 16-byte units
-            umma_mxf8f6f4(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc_mx_e4m3_e2m1(BM, 256, kk), sfa, sfa + 4,
-                          (i > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&empty[s]);
-          if (i == n_kb - 1) umma_commit(&tfull[tc & 1u]);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < 4; ++kk)  // 32 bytes of K further each: 2 in the descriptors' 16-byte units
+          umma_mxf8f6f4_if(lead, d_tmem, ad + 2 * kk, bd + 2 * kk, idesc_mx_e4m3_e2m1(BM, 256, kk), sfa, sfa + 4,
+                           (i > 0 || kk > 0) ? 1u : 0u);
+        umma_commit_if(lead, &empty[s]);
       }
+      if (ok) umma_commit_if(lead, &tfull[tc & 1u]);
     }
     if (!ok) {
       if (lead) flag_error(args.err, MOE_DEVERR_TIMEOUT);
