@@ -23,12 +23,13 @@
 // for the weights.  The epilogue reads the 48 shared columns first and releases
 // them; the next tile's MMAs start then, while the rest is still being read.
 //
-// Row tiles of 128; a tile with at most 96 rows loads its rows in boxes of 32,
-// so that a decode tile moves 4 KB of rows beside 17 KB of weights a stage.
+// Row tiles of 128 (or 32, see Ring); a tile with at most 96 rows loads its rows
+// in boxes of 32, so that a decode tile moves 4 KB of rows beside 17 KB of
+// weights a stage.
 // Rows past an expert's end are computed from whatever is there and never
 // stored (rows of an MMA are independent).  Schedule, roles and bounded waits as
 // in the bf16 GEMMs (ffn_tc.cu): persistent CTAs, warp 0 TMA, warp 1 MMA, warps
-// 2-5 epilogue.
+// 2-5 epilogue, and warps 6-9 for the scales.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -43,21 +44,33 @@ namespace {
 using namespace ptx;
 
 constexpr int kE = 8;
-constexpr int BM = 128;
 constexpr int BK = 128;
-constexpr int kThreads = 320;  // 10 warps: TMA, MMA, 4 epilogue, 4 scales
-constexpr int kStages = 4;
-constexpr int A_BYTES = BM * BK;       // 16 KB of e4m3
+constexpr int kThreads = 320;          // 10 warps: TMA, MMA, 4 epilogue, 4 scales
 constexpr int B_HALF = 128 * BK;       // 16 KB: 128 channels x 128 codes, spread
 constexpr int B_BYTES = 2 * B_HALF;
 constexpr int B_TX = B_BYTES / 2;      // bytes that the spreading loads report: those read, not the padding
-constexpr int SF_BYTES = 3 * 512;      // rows, first and second 128 channels
 constexpr int kTmemCols = 512;
 constexpr int kAccSecond = 208;        // first column of the second accumulator
-constexpr int kScaleCol = 464;         // kStages sets of 12 columns
-static_assert(kScaleCol + 12 * kStages <= kTmemCols, "TMEM columns");
-constexpr int SMEM_BYTES = 1024 + kStages * (A_BYTES + B_BYTES + SF_BYTES) + 256;
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+constexpr int kScaleCol = 464;         // kScaleSets sets of 12 columns
+constexpr int kScaleSets = 4;
+static_assert(kScaleCol + 12 * kScaleSets <= kTmemCols, "TMEM columns");
+constexpr int kGroupSlots = 3;         // groups of scales in shared memory
+
+// BM rows a tile: 128, or 32 where few rows an expert are expected.  The MMA
+// takes 128 rows either way (it has no smaller block-scaled form); with 32 the
+// others are whatever lies behind in shared memory, and the ring holds 6 stages
+// instead of 4, which is what the weights' stream needs in flight.
+template <int BM>
+struct Ring {
+  static constexpr int kStages = BM == 128 ? 4 : 6;
+  static constexpr int A_BYTES = BM * BK;
+  static constexpr int kGroup = BM == 128 ? 4 : 2;  // K blocks whose scales are loaded together
+  static constexpr int GROUP_BYTES = 3 * kGroup * 512;
+  static constexpr int kBars = 2 * kStages + 2 + 1 + kScaleSets + 2 * kGroupSlots + 1;
+  static constexpr int SMEM_BYTES = 1024 + kStages * (A_BYTES + B_BYTES) + kGroupSlots * GROUP_BYTES + kBars * 8 + 16;
+  static_assert(SMEM_BYTES + 256 <= 227 * 1024, "shared memory budget");
+  static_assert((kStages - 1) * A_BYTES + 128 * BK <= kStages * (A_BYTES + B_BYTES), "the MMA's A reads stay inside");
+};
 
 enum Mode { kGateUp = 0, kDownSum = 1, kDownParts = 2 };
 
@@ -89,9 +102,11 @@ struct Sched {
 };
 
 struct Tile {
-  int e, m0, rows, nt, mtile, kb0, kb1, split;
+  int e, m0, rows, nt, kb0, kb1, split;
+  int mtile, in_mtile;  // 128-row tile of the rows' scales, and the first row's place in it
 };
 
+template <int BM>
 __device__ __forceinline__ Tile decode_tile(const Sched& s, const MxArgs& a, int L) {
   int e = 0;
 #pragma unroll
@@ -108,7 +123,8 @@ __device__ __forceinline__ Tile decode_tile(const Sched& s, const MxArgs& a, int
   t.nt = local / s.mt[e];
   const int mi = local - t.nt * s.mt[e];
   t.m0 = s.offs[e] + mi * BM;
-  t.mtile = s.tile0[e] + mi;
+  t.mtile = s.tile0[e] + mi * BM / 128;
+  t.in_mtile = mi * BM % 128;
   const int left = s.offs[e + 1] - t.m0;
   t.rows = left < BM ? left : BM;
   t.kb0 = a.num_kb * t.split / a.splits;
@@ -116,6 +132,7 @@ __device__ __forceinline__ Tile decode_tile(const Sched& s, const MxArgs& a, int
   return t;
 }
 
+template <int BM>
 __device__ __forceinline__ void build_schedule(Sched& sched, const MxArgs& args) {
   bool ok = true;
   int prev = 0;
@@ -131,31 +148,35 @@ __device__ __forceinline__ void build_schedule(Sched& sched, const MxArgs& args)
     sched.mt[k] = (n + BM - 1) / BM;
     sched.tile0[k] = tiles;
     sched.prefix[k] = acc;
-    tiles += sched.mt[k];
+    tiles += (n + 127) / 128;
     acc += sched.mt[k] * args.n_tiles * args.splits;
   }
   sched.prefix[kE] = acc;
   if (!ok) flag_error(args.err, MOE_DEVERR_OFFSETS);
 }
 
-template <int MODE>
+template <int MODE, int BM>
 __global__ void __launch_bounds__(kThreads, 1)
     mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA32,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                     const MxArgs args) {
-  constexpr int S = kStages;
+  using R = Ring<BM>;
+  constexpr int S = R::kStages;
+  constexpr int kGroup = R::kGroup, GROUP_BYTES = R::GROUP_BYTES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sA = smem;
-  uint8_t* sB = smem + S * A_BYTES;
-  uint8_t* sSF = smem + S * (A_BYTES + B_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(sSF + S * SF_BYTES);
+  uint8_t* sB = smem + S * R::A_BYTES;
+  uint8_t* sG = sB + S * B_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sG + kGroupSlots * GROUP_BYTES);
   uint64_t* empty = full + S;
-  uint64_t* tfull = empty + S;   // accumulator 0 / 1 complete
-  uint64_t* tshared = tfull + 2; // the columns both accumulators use have been read
-  uint64_t* sfull = tshared + 1; // the stage's scales are in TMEM
-  uint64_t* drain = sfull + S;
+  uint64_t* tfull = empty + S;        // accumulator 0 / 1 complete
+  uint64_t* tshared = tfull + 2;      // the columns both accumulators use have been read
+  uint64_t* sfull = tshared + 1;      // scale set written
+  uint64_t* gfull = sfull + kScaleSets;  // group of scales landed
+  uint64_t* gfree = gfull + kGroupSlots; // ... and read
+  uint64_t* drain = gfree + kGroupSlots;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Sched sched;
@@ -171,7 +192,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&tfull[0], 1);
     mbar_init(&tfull[1], 1);
     mbar_init(tshared, 128);
-    for (int s = 0; s < S; ++s) mbar_init(&sfull[s], 4);
+    for (int s = 0; s < kScaleSets; ++s) mbar_init(&sfull[s], 4);
+    for (int s = 0; s < kGroupSlots; ++s) {
+      mbar_init(&gfull[s], 1);
+      mbar_init(&gfree[s], 4);
+    }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -188,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
     tc_fence_before();
   }
-  if (warp == 2 && lane == 0) build_schedule(sched, args);
+  if (warp == 2 && lane == 0) build_schedule<BM>(sched, args);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
@@ -201,23 +226,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       const uint64_t keep = policy_evict_last();
       for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
-        const Tile t = decode_tile(sched, args, L);
+        const Tile t = decode_tile<BM>(sched, args, L);
         const int boxes = t.rows > 96 ? 0 : (t.rows + 31) / 32;
-        const uint32_t bytes = (boxes ? (uint32_t)boxes * 32 * BK : A_BYTES) + B_TX + SF_BYTES;
-        const uint8_t* sa = args.a_scales + (int64_t)t.mtile * args.num_kb * 512;
-        const int64_t eb = (int64_t)t.e * args.nb_scales;
-        const uint8_t *sb0, *sb1;
-        int n0, n1;
-        if (MODE == kGateUp) {
-          n0 = n1 = t.nt * 128;
-          sb0 = args.b_scales0 + (eb + t.nt) * args.num_kb * 512;
-          sb1 = args.b_scales1 + (eb + t.nt) * args.num_kb * 512;
-        } else {
-          n0 = t.nt * 256;
-          n1 = n0 + 128;
-          sb0 = args.b_scales0 + (eb + 2 * t.nt) * args.num_kb * 512;
-          sb1 = sb0 + (int64_t)args.num_kb * 512;
-        }
+        const uint32_t bytes = (boxes ? (uint32_t)boxes * 32 * BK : R::A_BYTES) + B_TX;
+        const int n0 = t.nt * (MODE == kGateUp ? 128 : 256);
+        const int n1 = MODE == kGateUp ? n0 : n0 + 128;
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const int s = it % S;
           const uint32_t ph = (it / S) & 1u;
@@ -226,9 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&full[s], bytes);
-          uint8_t* a = sA + s * A_BYTES;
+          uint8_t* a = sA + s * R::A_BYTES;
           uint8_t* b = sB + s * B_BYTES;
-          uint8_t* f = sSF + s * SF_BYTES;
           tma_load_3d_hint(b, &tmB0, &full[s], kb * BK, n0, t.e, keep);
           tma_load_3d_hint(b + B_HALF, MODE == kGateUp ? &tmB1 : &tmB0, &full[s], kb * BK, n1, t.e, keep);
           if (boxes == 0) {
@@ -237,9 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < boxes; ++i)
               tma_load_2d_hint(a + i * 32 * BK, &tmA32, &full[s], kb * BK, t.m0 + 32 * i, keep);
           }
-          bulk_load(f, sa + (int64_t)kb * 512, 512, &full[s], keep);
-          bulk_load(f + 512, sb0 + (int64_t)kb * 512, 512, &full[s], keep);
-          bulk_load(f + 1024, sb1 + (int64_t)kb * 512, 512, &full[s], keep);
         }
       }
       if (!ok) {
@@ -258,25 +267,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t it = 0, tc = 0;
     bool ok = true;
     for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
-      const Tile t = decode_tile(sched, args, L);
+      const Tile t = decode_tile<BM>(sched, args, L);
       const int n_kb = __shfl_sync(0xffffffffu, t.kb1 - t.kb0, 0);
+      // rows of a tile that starts inside a 128-row scale tile: 32 rows a column
+      const uint32_t sf_skip = BM == 128 ? 0u : __shfl_sync(0xffffffffu, (uint32_t)t.in_mtile / 32u, 0);
       // the previous tile's epilogue has read the shared columns (and so has
       // finished the tile before, whose accumulator this one takes)
       if (tc > 0) ok = __all_sync(0xffffffffu, mbar_wait(tshared, (tc - 1) & 1u, abort_flag));
       if (!ok) break;
       const uint32_t d_tmem = tmem_base + ((tc & 1u) ? kAccSecond : 0);
       for (int i = 0; i < n_kb; ++i, ++it) {
-        const uint32_t s = it % S, ph = (it / S) & 1u;
-        ok = __all_sync(0xffffffffu, mbar_wait2(&full[s], ph, &sfull[s], ph, abort_flag));
+        const uint32_t s = it % S, set = it % kScaleSets;
+        ok = __all_sync(0xffffffffu, mbar_wait2(&full[s], (it / S) & 1u, &sfull[set], (it / kScaleSets) & 1u,
+                                                abort_flag));
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ad = sw128_desc(smem_u32(sA + s * A_BYTES), 16, 1024);
+        const uint64_t ad = sw128_desc(smem_u32(sA + s * R::A_BYTES), 16, 1024);
         const uint64_t bd = sw128_desc(smem_u32(sB + s * B_BYTES), 16, 1024);
-        const uint32_t sfa = tmem_base + kScaleCol + s * 12;
+        const uint32_t sfa = tmem_base + kScaleCol + set * 12;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)  // 32 bytes of K further each: 2 in the descriptors' 16-byte units
-          umma_mxf8f6f4_if(lead, d_tmem, ad + 2 * kk, bd + 2 * kk, idesc_mx_e4m3_e2m1(BM, 256, kk), sfa, sfa + 4,
-                           (i > 0 || kk > 0) ? 1u : 0u);
+          umma_mxf8f6f4_if(lead, d_tmem, ad + 2 * kk, bd + 2 * kk, idesc_mx_e4m3_e2m1(128, 256, kk), sfa + sf_skip,
+                           sfa + 4, (i > 0 || kk > 0) ? 1u : 0u);
         umma_commit_if(lead, &empty[s]);
       }
       if (ok) umma_commit_if(lead, &tfull[tc & 1u]);
@@ -293,41 +305,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp >= 6) {
     // ---------------------------------------------------------------- scales
-    // Each stage's scales from shared memory to the stage's 12 TMEM columns: all
-    // four lane quarters hold the same 32 lanes, one warp each.  A stage whose
-    // loads have landed was released by its last MMAs, and its columns with it.
+    // On a path of their own beside the operands' ring: loads of kGroup K blocks
+    // at a time (one lane of the first warp), and each block's 12 columns to its
+    // TMEM set, all four lane quarters holding the same 32 lanes, one warp each.
+    // (Moved by tcgen05.cp from the MMA warp, they stalled the MMAs.)  A set is
+    // free when the MMAs four K blocks back are done.
     const int q = warp & 3;
-    uint32_t it = 0;
+    const bool loader = warp == 6 && lane == 0;
+    uint32_t it = 0, grp = 0, issued = 0;
     bool ok = true;
+    // tile and K block of the next group to load
+    int lL = blockIdx.x, lkb = 0;
+    Tile lt = {};
+    if (lL < total) {
+      lt = decode_tile<BM>(sched, args, lL);
+      lkb = lt.kb0;
+    }
+    const uint64_t keep = policy_evict_last();
+    auto load_groups = [&](uint32_t upto) {  // loader: groups below `upto`, their slots being free
+      while (issued < upto && lL < total) {
+        const uint32_t slot = issued % kGroupSlots;
+        if (issued >= (uint32_t)kGroupSlots &&
+            !mbar_wait(&gfree[slot], (issued / kGroupSlots - 1) & 1u, abort_flag))
+          return false;
+        const int n = min(kGroup, lt.kb1 - lkb);
+        const uint32_t bytes = (uint32_t)n * 512;
+        const int64_t eb = (int64_t)lt.e * args.nb_scales;
+        const int64_t nb0 = eb + (MODE == kGateUp ? lt.nt : 2 * lt.nt);
+        const uint8_t* sa = args.a_scales + ((int64_t)lt.mtile * args.num_kb + lkb) * 512;
+        const uint8_t* sb0 = args.b_scales0 + (nb0 * args.num_kb + lkb) * 512;
+        const uint8_t* sb1 = MODE == kGateUp ? args.b_scales1 + (nb0 * args.num_kb + lkb) * 512
+                                             : sb0 + (int64_t)args.num_kb * 512;
+        uint8_t* g = sG + slot * GROUP_BYTES;
+        mbar_arrive_expect_tx(&gfull[slot], 3 * bytes);
+        bulk_load(g, sa, bytes, &gfull[slot], keep);
+        bulk_load(g + kGroup * 512, sb0, bytes, &gfull[slot], keep);
+        bulk_load(g + 2 * kGroup * 512, sb1, bytes, &gfull[slot], keep);
+        ++issued;
+        lkb += n;
+        if (lkb >= lt.kb1) {
+          lL += gridDim.x;
+          if (lL < total) {
+            lt = decode_tile<BM>(sched, args, lL);
+            lkb = lt.kb0;
+          }
+        }
+      }
+      return true;
+    };
+    if (loader) ok = load_groups(kGroupSlots - 1);
     for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
-      const Tile t = decode_tile(sched, args, L);
-      for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-        const int s = it % S;
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (it / S) & 1u, abort_flag));
+      const Tile t = decode_tile<BM>(sched, args, L);
+      for (int kb = t.kb0; kb < t.kb1 && ok; kb += kGroup, ++grp) {
+        const uint32_t slot = grp % kGroupSlots;
+        bool go = !loader || load_groups(grp + kGroupSlots);
+        go = go && mbar_wait(&gfull[slot], (grp / kGroupSlots) & 1u, abort_flag);
+        ok = __all_sync(0xffffffffu, go);
         if (!ok) break;
-        tc_fence_after();
-        const uint4* f = reinterpret_cast<const uint4*>(sSF + s * SF_BYTES) + lane;
-        const uint4 va = f[0], vb = f[32], vc = f[64];
-        const uint32_t dst = tmem_base + kScaleCol + s * 12 + ((uint32_t)(q * 32) << 16);
-        tmem_st4(dst, va);
-        tmem_st8(dst + 4, vb, vc);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sfull[s]);
+        const uint4* f = reinterpret_cast<const uint4*>(sG + slot * GROUP_BYTES) + lane;
+        const int n = min(kGroup, t.kb1 - kb);
+        for (int j = 0; j < n; ++j, ++it) {
+          const uint32_t set = it % kScaleSets;
+          const uint4 va = f[j * 32], vb = f[kGroup * 32 + j * 32], vc = f[2 * kGroup * 32 + j * 32];
+          if (it >= (uint32_t)kScaleSets) {
+            const uint32_t done = it - kScaleSets;
+            ok = __all_sync(0xffffffffu, mbar_wait(&empty[done % S], (done / S) & 1u, abort_flag));
+            if (!ok) break;
+          }
+          tc_fence_after();
+          const uint32_t dst = tmem_base + kScaleCol + set * 12 + ((uint32_t)(q * 32) << 16);
+          tmem_st4(dst, va);
+          tmem_st8(dst + 4, vb, vc);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull[set]);
+        }
+        if (ok && lane == 0) mbar_arrive(&gfree[slot]);
       }
     }
     if (!ok) {
       if (lane == 0) flag_error(args.err, MOE_DEVERR_TIMEOUT);
       *abort_flag = 1;
     }
+    if (loader) {
+      // drain, as the producer does
+      const uint32_t first = issued > (uint32_t)kGroupSlots ? issued - kGroupSlots : 0u;
+      for (uint32_t j = first; j < issued; ++j)
+        mbar_wait(&gfull[j % kGroupSlots], (j / kGroupSlots) & 1u, nullptr, 100000000ull);
+    }
+    __syncwarp();
   } else {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;
     const int r = q * 32 + lane;
     uint32_t tc = 0;
     for (int L = blockIdx.x; L < total; L += gridDim.x, ++tc) {
-      const Tile t = decode_tile(sched, args, L);
+      const Tile t = decode_tile<BM>(sched, args, L);
       const uint32_t buf = tc & 1u;
       if (!mbar_wait(&tfull[buf], (tc >> 1) & 1u, abort_flag)) {
         if (lane == 0) flag_error(args.err, MOE_DEVERR_TIMEOUT);
@@ -335,6 +409,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
+      if (q * 32 >= t.rows) {  // a warp without rows reads nothing
+        mbar_arrive(tshared);
+        continue;
+      }
       const bool valid = r < t.rows;
       const int row = t.m0 + r;
       const uint32_t tacc = tmem_base + (buf ? kAccSecond : 0) + ((uint32_t)(q * 32) << 16);
@@ -365,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (valid)
           *reinterpret_cast<uint32_t*>(args.h_scales + ((int64_t)t.mtile * (args.ld / 128) + t.nt) * 512 +
-                                       mx_scale_at(r, 0)) = scales;
+                                       mx_scale_at(t.in_mtile + r, 0)) = scales;
       } else {
         int64_t drow = (int64_t)t.split * args.rows_alloc + row;
         bool store = valid;
@@ -477,14 +555,24 @@ __global__ void __launch_bounds__(256) mx4_combine_kernel(const float4* __restri
   out[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
 }
 
+template <int MODE, int BM>
+cudaError_t launch_mx_tiles(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b0, const CUtensorMap& b1,
+                            const MxArgs& args, cudaStream_t s, const Ctx& ctx) {
+  auto kern = mx4_gemm_kernel<MODE, BM>;
+  constexpr int smem = Ring<BM>::SMEM_BYTES;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(ctx.num_sms), dim3(kThreads), smem, s, no_extra_attr(), a, a32, b0, b1, args);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Row tiles of 32 where an expert gets at most 16 rows on the average (Grok-1
+// decode), else of 128.
 template <int MODE>
 cudaError_t launch_mx(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b0, const CUtensorMap& b1,
                       const MxArgs& args, cudaStream_t s, const Ctx& ctx) {
-  auto kern = mx4_gemm_kernel<MODE>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(ctx.num_sms), dim3(kThreads), SMEM_BYTES, s, no_extra_attr(), a, a32, b0, b1, args);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  if (MODE != kDownSum && args.rows_alloc <= 16 * kE) return launch_mx_tiles<MODE, 32>(a, a32, b0, b1, args, s, ctx);
+  return launch_mx_tiles<MODE, 128>(a, a32, b0, b1, args, s, ctx);
 }
 
 // [rows, K] e4m3 codes, box of 128 columns x box_rows rows.
