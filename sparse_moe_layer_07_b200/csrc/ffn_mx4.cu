@@ -58,13 +58,14 @@ constexpr int kGroupSlots = 3;         // groups of scales in shared memory
 
 // BM rows a tile: 128, or 32 where few rows an expert are expected.  The MMA
 // takes 128 rows either way (it has no smaller block-scaled form); with 32 the
-// others are whatever lies behind in shared memory, and the ring holds 6 stages
-// instead of 4, which is what the weights' stream needs in flight.
+// others are whatever lies behind in shared memory, and the room goes to a fifth
+// stage and to scales 16 K blocks ahead: there they come from DRAM, and with 4
+// blocks ahead the MMAs waited for them (gate/up of Grok-1 decode 338 us).
 template <int BM>
 struct Ring {
-  static constexpr int kStages = BM == 128 ? 4 : 6;
+  static constexpr int kStages = BM == 128 ? 4 : 5;
   static constexpr int A_BYTES = BM * BK;
-  static constexpr int kGroup = BM == 128 ? 4 : 2;  // K blocks whose scales are loaded together
+  static constexpr int kGroup = BM == 128 ? 4 : 8;  // K blocks whose scales are loaded together
   static constexpr int GROUP_BYTES = 3 * kGroup * 512;
   static constexpr int kBars = 2 * kStages + 2 + 1 + kScaleSets + 2 * kGroupSlots + 1;
   static constexpr int SMEM_BYTES = 1024 + kStages * (A_BYTES + B_BYTES) + kGroupSlots * GROUP_BYTES + kBars * 8 + 16;
@@ -416,21 +417,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = r < t.rows;
       const int row = t.m0 + r;
       const uint32_t tacc = tmem_base + (buf ? kAccSecond : 0) + ((uint32_t)(q * 32) << 16);
+      // The shared columns first (the first accumulator's last 48, the second's
+      // first 48: two chunks of 32), then the release: the next tile's MMAs wait
+      // for nothing but these two loads.
+      uint32_t early[2][32];
+      const uint32_t tshare = MODE == kGateUp ? tacc + (buf ? 0 : 128) : tacc;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = buf ? i : (MODE == kGateUp ? 3 : 7) - i;
+        tmem_ld32(tshare + c * 32, early[i]);
+      }
+      tmem_wait_ld();
+      tmem_regs_ready(early[0]);
+      tmem_regs_ready(early[1]);
+      tc_fence_before();
+      mbar_arrive(tshared);
       if (MODE == kGateUp) {
         uint32_t scales = 0;
         uint8_t* dst = args.h + (int64_t)row * args.ld + t.nt * 128;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          // the first accumulator's last 48 columns are the shared ones, the second's first 48
-          const int c = buf ? i : 3 - i;
-          uint32_t g[32], u[32];
-          tmem_ld32(tacc + c * 32, g);
-          tmem_ld32(tacc + 128 + c * 32, u);
-          tmem_wait_ld();
-          if (i == 1) {
-            tc_fence_before();
-            mbar_arrive(tshared);
-          }
+        auto finish = [&](int c, const uint32_t (&g)[32], const uint32_t (&u)[32]) {
           float h[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) h[k] = silu_mul_fast(__uint_as_float(g[k]), __uint_as_float(u[k]));
@@ -440,6 +445,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             __stcs(reinterpret_cast<uint4*>(dst + c * 32), make_uint4(codes[0], codes[1], codes[2], codes[3]));
             __stcs(reinterpret_cast<uint4*>(dst + c * 32 + 16), make_uint4(codes[4], codes[5], codes[6], codes[7]));
           }
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = buf ? i : 3 - i;
+          uint32_t other[32];  // gate beside the early up columns, or up beside the early gate columns
+          tmem_ld32(tacc + (buf ? 128 : 0) + c * 32, other);
+          tmem_wait_ld();
+          if (buf)
+            finish(c, early[i], other);
+          else
+            finish(c, other, early[i]);
+        }
+#pragma unroll 1
+        for (int i = 2; i < 4; ++i) {
+          const int c = buf ? i : 3 - i;
+          uint32_t g[32], u[32];
+          tmem_ld32(tacc + c * 32, g);
+          tmem_ld32(tacc + 128 + c * 32, u);
+          tmem_wait_ld();
+          finish(c, g, u);
         }
         if (valid)
           *reinterpret_cast<uint32_t*>(args.h_scales + ((int64_t)t.mtile * (args.ld / 128) + t.nt) * 512 +
@@ -457,16 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float sc = (store && args.row_scale) ? __ldg(args.row_scale + row) : 1.0f;
         float* dst = args.out + (store ? drow : 0) * args.ld + t.nt * 256;
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          const int c = buf ? i : 7 - i;
-          uint32_t v[32];
-          tmem_ld32(tacc + c * 32, v);
-          tmem_wait_ld();
-          if (i == 1) {
-            tc_fence_before();
-            mbar_arrive(tshared);
-          }
+        auto finish = [&](int c, const uint32_t (&v)[32]) {
           if (store) {
             float4* d4 = reinterpret_cast<float4*>(dst + c * 32);
 #pragma unroll
@@ -479,6 +495,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 d4[k] = o;
             }
           }
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) finish(buf ? i : 7 - i, early[i]);
+#pragma unroll 1
+        for (int i = 2; i < 8; ++i) {
+          const int c = buf ? i : 7 - i;
+          uint32_t v[32];
+          tmem_ld32(tacc + c * 32, v);
+          tmem_wait_ld();
+          finish(c, v);
         }
       }
       tc_fence_before();
