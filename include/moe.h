@@ -531,7 +531,7 @@ MOE_API moe_status_t moe_expert_utilization(const int32_t* stats, int32_t E, int
  *   loss[0..2]   = balance_coef * balance + z_coef * z, balance, z
  *   dlogits      = d loss[0] / d logits, the counts held fixed
  * (one sequence of balanced tokens gives balance = 1).  Rows that are not live
- * are not read and get dlogits 0; every row of dlogits is written.  With no
+ * may hold anything and get dlogits 0; every row of dlogits is written.  With no
  * live token loss and dlogits are 0.  A live row whose logits hold a NaN or
  * +inf makes loss and its own dlogits row NaN; -inf logits are experts of
  * probability 0.

@@ -186,7 +186,7 @@ def _ptr(t):
         raise TypeError("expected a torch.Tensor")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()  # an int passes as a c_void_p argument
 
 
 def _dev_ptr(t):
@@ -198,7 +198,7 @@ def _dev_ptr(t):
 def _stream(stream, device=None):
     if stream is None:
         stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _check(status: int, where: str):
@@ -596,6 +596,26 @@ def layer_backward(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ws, gra
     return g
 
 
+def _carve(buf, spec):
+    """Views (name, dtype, 1-D or 2-D or 3-D shape) of consecutive 256-byte aligned parts of a buffer."""
+    flat = buf.view(torch.uint8).view(-1)
+    if flat.numel() % 256:
+        flat = flat[:flat.numel() // 256 * 256]
+    typed, views, o = {}, {}, 0
+    for name, dt, shape in spec:
+        if dt not in typed:
+            typed[dt] = flat.view(dt)
+        strides = [1]
+        for n in shape[:0:-1]:
+            strides.insert(0, strides[0] * n)
+        nbytes = math.prod(shape) * dt.itemsize
+        if o + nbytes > flat.numel():
+            raise ValueError(f"the buffer of {flat.numel()} bytes ends inside {name}")
+        views[name] = typed[dt].as_strided(shape, strides, typed[dt].storage_offset() + o // dt.itemsize)
+        o += _round256(nbytes)
+    return views
+
+
 def checkpoint_size_c8(cfg: Config) -> int:
     return lib.moe_checkpoint_size_c8(cfg.ref)
 
@@ -613,12 +633,7 @@ def checkpoint_views_c8(cfg: Config, ckpt):
             ("perm", i32, (rows,)), ("slot_of", i32, (T, 2)), ("row_scale", f32, (rows,)),
             ("g_codes", torch.int8, (rows, f)), ("u_codes", torch.int8, (rows, f)),
             ("g_scale", torch.bfloat16, (rows, f // 32)), ("u_scale", torch.bfloat16, (rows, f // 32))]
-    flat = ckpt.view(torch.uint8).view(-1)
-    views, o = {}, 0
-    for name, dt, shape in spec:
-        nbytes = math.prod(shape) * dt.itemsize
-        views[name] = flat[o:o + nbytes].view(dt).view(shape)
-        o += _round256(nbytes)
+    views = _carve(ckpt, spec)
     route = views.pop("route")
     views.update(counts_raw=route[:E], counts_kept=route[E:2 * E], offsets=route[2 * E:])
     return views
@@ -867,13 +882,7 @@ def mx4_workspace_views(cfg: Config, ws):
     R = rows // 128 + cfg.E
     spec = [("x_codes", (rows, d)), ("x_scales", (R, d // 128, 512)), ("h_codes", (rows, f)),
             ("h_scales", (R, f // 128, 512))]
-    flat = ws.view(torch.uint8).view(-1)
-    views, o = {}, 0
-    for name, shape in spec:
-        n = math.prod(shape)
-        views[name] = flat[o:o + n].view(shape)
-        o += _round256(n)
-    return views
+    return _carve(ws, [(name, torch.uint8, shape) for name, shape in spec])
 
 
 def expert_ffn_mx4(cfg: Config, x_perm, offsets, qw: MxExperts, row_scale=None, y=None, ws=None, stream=None):

@@ -66,12 +66,13 @@ struct __align__(16) Shared {
   int done;
 };
 
-// Sequence of every token of a chunk, in windows of kWindow sequences.
+// A chunk of tokens and the sequences that they can belong to.
 struct Chunk {
-  int first, last;   // sequences that its tokens can belong to; last < first: none
+  int first, last;   // last < first: none
   int t0;            // first token
   bool live[kTok];   // unmasked, inside the range of all sequences
 };
+constexpr int kScan = 8;  // offsets a thread looks at in the one-round search
 
 // Sequences that end at or before token t, by the whole block: every round
 // tests kNT evenly spaced ones at once (empty sequences are passed over, so this
@@ -91,9 +92,42 @@ __device__ __forceinline__ int block_seq_of(const BalanceArgs& a, int t) {
   return lo;
 }
 
-__device__ __forceinline__ Chunk open_chunk(const BalanceArgs& a, int c) {
+// Sequences that end at or before t0 and t1, in one round for up to kNT * kScan
+// sequences: every thread looks at kScan neighbouring offsets.
+__device__ __forceinline__ int2 block_seqs_of(const BalanceArgs& a, int t0, int t1, Shared& sh) {
+  if (a.n_seq > kNT * kScan) return make_int2(block_seq_of(a, t0), block_seq_of(a, t1));
+  int c0 = 0, c1 = 0;
+#pragma unroll
+  for (int i = 0; i < kScan; ++i) {
+    const int s = i * kNT + (int)threadIdx.x;
+    if (s < a.n_seq) {
+      const int v = bound_of(a, s + 1);
+      c0 += v <= t0;
+      c1 += v <= t1;
+    }
+  }
+  const unsigned both = __reduce_add_sync(~0u, (unsigned)c0 | (unsigned)c1 << 16);  // at most 256 each
+  if ((threadIdx.x & 31) == 0) sh.ired[threadIdx.x >> 5] = (int)both;
+  __syncthreads();
+  c0 = c1 = 0;
+#pragma unroll
+  for (int w = 0; w < kNT / 32; ++w) {
+    c0 += sh.ired[w] & 0xffff;
+    c1 += (int)((unsigned)sh.ired[w] >> 16);
+  }
+  __syncthreads();
+  return make_int2(c0, c1);
+}
+
+__device__ __forceinline__ Chunk open_chunk(const BalanceArgs& a, int c, Shared& sh) {
   Chunk k;
   k.t0 = c * kChunk;
+  uint8_t mask[kTok];
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {  // in flight during the search
+    const int64_t t = (int64_t)k.t0 + j * kNT + threadIdx.x;
+    mask[j] = t < a.T ? (a.mask ? __ldg(a.mask + t) : 1) : 0;
+  }
   const int begin = bound_of(a, 0), end = bound_of(a, a.n_seq);
   int64_t t1 = (int64_t)k.t0 + kChunk;
   if (t1 > end) t1 = end;
@@ -101,14 +135,14 @@ __device__ __forceinline__ Chunk open_chunk(const BalanceArgs& a, int c) {
   k.first = 0;
   k.last = -1;
   if (t0 < t1) {
-    k.first = a.n_seq == 1 ? 0 : block_seq_of(a, t0);
-    k.last = a.n_seq == 1 ? 0 : block_seq_of(a, (int)t1 - 1);
-    if (k.last >= a.n_seq) k.last = a.n_seq - 1;
+    const int2 s = a.n_seq == 1 ? make_int2(0, 0) : block_seqs_of(a, t0, (int)t1 - 1, sh);
+    k.first = s.x < a.n_seq ? s.x : a.n_seq - 1;
+    k.last = s.y < a.n_seq ? s.y : a.n_seq - 1;
   }
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
     const int64_t t = (int64_t)k.t0 + j * kNT + threadIdx.x;
-    k.live[j] = t < a.T && t >= begin && t < end && (!a.mask || __ldg(a.mask + t));
+    k.live[j] = mask[j] && t >= begin && t < end;
   }
   return k;
 }
@@ -138,16 +172,16 @@ __device__ __forceinline__ void open_window(const BalanceArgs& a, const Chunk& k
 }
 
 // Pass 1 over chunk c: counts of every sequence that meets the chunk, into its slot.
-__device__ __forceinline__ void count_chunk(const BalanceArgs& a, int c, const Chunk& k, int (&seq)[kTok], Shared& sh) {
-  int2 e[kTok];
+__device__ __forceinline__ void count_chunk(const BalanceArgs& a, int c, const Chunk& k, int2 (&e)[kTok],
+                                            int (&seq)[kTok], Shared& sh) {
   int live = 0;
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
-    e[j] = make_int2(-1, -1);
     if (k.live[j]) {
-      e[j] = __ldg(reinterpret_cast<const int2*>(a.idx) + k.t0 + j * kNT + threadIdx.x);
       if ((unsigned)e[j].x >= kE || (unsigned)e[j].y >= kE) flag_error(a.err, MOE_DEVERR_EXPERT_INDEX);
       ++live;
+    } else {
+      e[j] = make_int2(-1, -1);
     }
   }
   for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
@@ -193,12 +227,22 @@ __device__ __forceinline__ void count_chunk(const BalanceArgs& a, int c, const C
   }
 }
 
-__device__ __forceinline__ void load_logits(const BalanceArgs& a, const Chunk& k, float (&l)[kTok][kE]) {
+// A chunk's choices and logits, asked for before it is known which tokens are
+// live (a padded row's values are dropped), so that they travel during the search.
+__device__ __forceinline__ void load_choices(const BalanceArgs& a, int c, int2 (&e)[kTok]) {
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
-    if (k.live[j]) {
-      const float4* p = reinterpret_cast<const float4*>(a.logits) + 2 * ((int64_t)k.t0 + j * kNT + threadIdx.x);
-      const float4 u = __ldg(p), v = __ldg(p + 1);
+    const int64_t t = (int64_t)c * kChunk + j * kNT + threadIdx.x;
+    if (t < a.T) e[j] = __ldg(reinterpret_cast<const int2*>(a.idx) + t);
+  }
+}
+__device__ __forceinline__ void load_logits(const BalanceArgs& a, int c, float (&l)[kTok][kE]) {
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    const int64_t t = (int64_t)c * kChunk + j * kNT + threadIdx.x;
+    if (t < a.T) {
+      const float4* p = reinterpret_cast<const float4*>(a.logits) + 2 * t;
+      const float4 u = __ldcs(p), v = __ldcs(p + 1);
       l[j][0] = u.x; l[j][1] = u.y; l[j][2] = u.z; l[j][3] = u.w;
       l[j][4] = v.x; l[j][5] = v.y; l[j][6] = v.z; l[j][7] = v.w;
     }
@@ -393,8 +437,10 @@ __global__ void __launch_bounds__(kNT, 2) balance_count_kernel(const BalanceArgs
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   empty_counts(a, blockIdx.x, gridDim.x);
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
+    int2 e[kTok];
+    load_choices(a, c, e);
     int seq[kTok];
-    count_chunk(a, c, open_chunk(a, c), seq, sh);
+    count_chunk(a, c, open_chunk(a, c, sh), e, seq, sh);
     __syncthreads();
   }
 }
@@ -404,10 +450,10 @@ __global__ void __launch_bounds__(kNT, 2) balance_gradient_kernel(const BalanceA
   pdl_wait();
   int n = -1;
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
-    const Chunk k = open_chunk(a, c);
     float l[kTok][kE];
-    load_logits(a, k, l);
+    load_logits(a, c, l);
     if (n < 0) n = total_live(a, sh);
+    const Chunk k = open_chunk(a, c, sh);
     int seq[kTok];
     gradient_chunk(a, c, k, l, n > 0 ? 1.0f / (float)n : 0.f, false, seq, sh);
     __syncthreads();
@@ -428,12 +474,14 @@ __global__ void __launch_bounds__(kNT, 1) balance_cluster_kernel(const BalanceAr
   __shared__ Shared sh;
   pdl_wait();
   const int c = blockIdx.x;
-  const Chunk k = open_chunk(a, c);
   float l[kTok][kE];
-  load_logits(a, k, l);
+  load_logits(a, c, l);
+  int2 e[kTok];
+  load_choices(a, c, e);
+  const Chunk k = open_chunk(a, c, sh);
   empty_counts(a, blockIdx.x, gridDim.x);
   int seq[kTok];
-  count_chunk(a, c, k, seq, sh);
+  count_chunk(a, c, k, e, seq, sh);
   ptx::cluster_sync();  // the slots and live tokens of all chunks are written
   const int n = total_live(a, sh);
   gradient_chunk(a, c, k, l, n > 0 ? 1.0f / (float)n : 0.f, k.last - k.first < kWindow, seq, sh);

@@ -46,9 +46,14 @@ constexpr int BK = 64;
 // Epilogue warps: 4, one per TMEM lane quarter.  (The layout also allows 8, two
 // per quarter each taking half of the tile's columns; for kDH that measured 14%
 // slower than 4 relative to the forward GEMMs in the same capture.)
-template <int MODE>
+// C8 is 0, or with 8-bit checkpoints the number of kDH's epilogue warps: its
+// epilogue decodes as well, and 4 warps take about 36K clocks a tile, more than
+// the tile's products (8 clocks per unit of d) below d of about 4500: 8 warps
+// are 12% faster at d = 1536 (223 against 255 us, T 2048, f 8192), 4 warps 12%
+// at d = 6144 (6.11 against 6.94 ms, T 8192, f 32768).
+template <int MODE, int C8 = 0>
 struct Warps {
-  static constexpr int kEpi = 4;
+  static constexpr int kEpi = MODE == 0 && C8 ? C8 : 4;
   // weight gradients: one more warp zeroes the rows past an expert's end in its
   // last K block, so the MMA warp does not stall on it
   static constexpr int kZeroWarp = MODE == 2 ? 2 + kEpi : -1;
@@ -182,8 +187,8 @@ __device__ __forceinline__ void unpack8_bf16(const uint4 q, float (&v)[8]) {
   }
 }
 
-template <int MODE, bool C8>
-__global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
+template <int MODE, int C8>
+__global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
     bwd_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                     const __grid_constant__ CUtensorMap tmOut, const BwdArgs args) {
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 32 * Warps<MODE>::kEpi);
+      mbar_init(&tempty[b], 32 * Warps<MODE, C8>::kEpi);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
         mbar_wait(drain, 0, nullptr, 100000000ull);
       }
     }
-  } else if (warp == Warps<MODE>::kZeroWarp) {
+  } else if (warp == Warps<MODE, C8>::kZeroWarp) {
     // ------------------------------------------------ ragged-row zeroing (kWG)
     // The tile's last K block may hold rows past the expert's end (the next
     // expert's rows, or rows past the kept ones): once the stage has landed,
@@ -425,7 +430,7 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3;
     // column chunks of 32 this warp covers: all 8, or one half with 8 epilogue warps
-    constexpr int kSplit = Warps<MODE>::kEpi / 4;
+    constexpr int kSplit = Warps<MODE, C8>::kEpi / 4;
     const int half = kSplit == 1 ? 0 : (warp - 2) / 4;
     const int c_begin = half * (BN / 32) / kSplit, c_end = c_begin + (BN / 32) / kSplit;
     uint32_t tc = 0;
@@ -446,11 +451,14 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
         const bool valid = r < t.rows;
         const int64_t row = t.m0 + r;
         const float w = valid ? __ldg(args.row_scale + row) : 0.f;
-        const int64_t base = row * args.ld + t.n0;
+        constexpr int NC = BN / 32 / kSplit;  // chunks of this warp
+        const int64_t base = row * args.ld + t.n0 + c_begin * 32;
+        const uint32_t tmine = tacc + c_begin * 32;
         float dot = 0.f;
         // codes of a 32-column chunk: 2 x 16 bytes of G and of U, the next chunk's
-        // loaded while this one is computed; the tile's 8 scales of each are one load
-        uint4 qg[2], qu[2], sg4 = {}, su4 = {};
+        // loaded while this one is computed; the chunks' scales of each are one load
+        uint4 qg[2], qu[2];
+        uint32_t sg4[NC / 2] = {}, su4[NC / 2] = {};
         auto load_chunk = [&](int c, uint4 (&a)[2], uint4 (&b)[2]) {
 #pragma unroll
           for (int p = 0; p < 2; ++p) {
@@ -459,20 +467,27 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
           }
         };
         if (valid) {
-          sg4 = __ldg(reinterpret_cast<const uint4*>(args.codes.sg + base / 32));
-          su4 = __ldg(reinterpret_cast<const uint4*>(args.codes.su + base / 32));
+#pragma unroll
+          for (int i = 0; i < NC / 4; ++i) {
+            const uint2 a = __ldg(reinterpret_cast<const uint2*>(args.codes.sg + base / 32) + i);
+            const uint2 b = __ldg(reinterpret_cast<const uint2*>(args.codes.su + base / 32) + i);
+            sg4[2 * i] = a.x;
+            sg4[2 * i + 1] = a.y;
+            su4[2 * i] = b.x;
+            su4[2 * i + 1] = b.y;
+          }
           load_chunk(0, qg, qu);
         }
 #pragma unroll
-        for (int c = 0; c < BN / 32; ++c) {
+        for (int c = 0; c < NC; ++c) {
           uint32_t v[32];
-          tmem_ld32(tacc + c * 32, v);
-          const bool more = c + 1 < BN / 32;
+          tmem_ld32(tmine + c * 32, v);
+          const bool more = c + 1 < NC;
           uint4 ng[2], nu[2];
           if (valid && more) load_chunk(c + 1, ng, nu);
           tmem_wait_ld();
           if (valid) {
-            const uint32_t pg = (&sg4.x)[c >> 1], pu = (&su4.x)[c >> 1];
+            const uint32_t pg = sg4[c >> 1], pu = su4[c >> 1];
             const float sg = __uint_as_float((c & 1) ? pg & 0xffff0000u : pg << 16);
             const float su = __uint_as_float((c & 1) ? pu & 0xffff0000u : pu << 16);
 #pragma unroll
@@ -520,7 +535,7 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
             }
           }
         }
-        if (valid) args.dw_part[row * (int64_t)args.n_tiles + t.nb] = dot;
+        if (valid) args.dw_part[(row * (int64_t)args.n_tiles + t.nb) * kSplit + half] = dot;
       } else if (MODE == kDH) {
         const bool valid = r < t.rows;
         const int64_t row = t.m0 + r;
@@ -687,13 +702,13 @@ __global__ void __launch_bounds__(Warps<MODE>::kThreads, 1)
   }
 }
 
-template <int MODE, bool C8 = false>
+template <int MODE, int C8 = 0>
 cudaError_t launch_bwd(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
                        const CUtensorMap& out, const BwdArgs& args, cudaStream_t s, const Ctx& ctx) {
   auto kern = bwd_gemm_kernel<MODE, C8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  kern<<<ctx.num_sms, Warps<MODE>::kThreads, SMEM_BYTES, s>>>(a0, a1, b0, b1, out, args);
+  kern<<<ctx.num_sms, Warps<MODE, C8>::kThreads, SMEM_BYTES, s>>>(a0, a1, b0, b1, out, args);
   return cudaGetLastError();
 }
 
@@ -724,6 +739,7 @@ bool map_weights(CUtensorMap* m, const void* base, int E, int64_t R, int64_t C) 
 }  // namespace
 
 int bwd_dh_parts_per_tile() { return Warps<kDH>::kEpi / 4; }
+int bwd_dh_c8_parts_per_tile(const moe_config_t& c) { return c.d < 4096 ? 2 : 1; }
 
 cudaError_t launch_bwd_dh(const moe_config_t& c, const void* dout_perm, const int32_t* offsets, const void* wd,
                           const void* G, const void* U, const void* H, const float* row_scale, void* dG, void* dU,
@@ -751,7 +767,6 @@ cudaError_t launch_bwd_dh(const moe_config_t& c, const void* dout_perm, const in
 cudaError_t launch_bwd_dh_c8(const moe_config_t& c, const void* dout_perm, const int32_t* offsets, const void* wd,
                              const Codes8& codes, const float* row_scale, void* dG, void* dU, void* hw, float* dw_part,
                              cudaStream_t s, const Ctx& ctx) {
-  static_assert(Warps<kDH>::kEpi == 4, "one partial per row and tile");
   const int64_t rows = slot_rows(c);
   if (rows == 0) return cudaSuccess;
   CUtensorMap ta, tb;
@@ -766,7 +781,8 @@ cudaError_t launch_bwd_dh_c8(const moe_config_t& c, const void* dout_perm, const
   a.dU = static_cast<__nv_bfloat16*>(dU);
   a.dw_part = dw_part;
   a.ld = c.f;
-  return launch_bwd<kDH, true>(ta, ta, tb, tb, ta, a, s, ctx);
+  if (bwd_dh_c8_parts_per_tile(c) == 2) return launch_bwd<kDH, 8>(ta, ta, tb, tb, ta, a, s, ctx);
+  return launch_bwd<kDH, 4>(ta, ta, tb, tb, ta, a, s, ctx);
 }
 
 cudaError_t launch_bwd_dx(const moe_config_t& c, const void* dG, const void* dU, const int32_t* offsets,
@@ -821,7 +837,7 @@ cudaError_t launch_bwd_wgrad(const moe_config_t& c, const void* a_rows, int64_t 
   a.m_outer = m_outer ? 1 : 0;
   a.ld = N;
   a.M = M;
-  if (bf16_out) return launch_bwd<kWG, true>(ta, ta, tb, tb, to, a, s, ctx);
+  if (bf16_out) return launch_bwd<kWG, 4>(ta, ta, tb, tb, to, a, s, ctx);
   a.out = static_cast<float*>(dW);
   return launch_bwd<kWG>(ta, ta, tb, tb, to, a, s, ctx);
 }

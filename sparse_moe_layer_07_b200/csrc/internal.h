@@ -157,6 +157,7 @@ cudaError_t launch_tc_down_scatter(const moe_config_t& c, const void* h, const i
 // the weight gradients dW[e] = A_e^T B_e over each expert's rows ([E, M, N] fp32).
 // Routing-weight partials the dH kernel writes per row and N tile.
 int bwd_dh_parts_per_tile();
+int bwd_dh_c8_parts_per_tile(const moe_config_t& c);
 cudaError_t launch_bwd_dh(const moe_config_t& c, const void* dout_perm, const int32_t* offsets, const void* wd,
                           const void* G, const void* U, const void* H, const float* row_scale, void* dG, void* dU,
                           float* dw_part, cudaStream_t s, const Ctx& ctx);

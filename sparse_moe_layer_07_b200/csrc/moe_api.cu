@@ -1071,7 +1071,7 @@ Train8Layout train8_layout_of(const moe_config_t& c) {
   L.dout_perm = take(rows * c.d * 2);
   L.dg = take(rows * c.f * 2);
   L.du = take(rows * c.f * 2);
-  L.dw_part = take(rows * (size_t)(c.f / 256) * 4);
+  L.dw_part = take(rows * (size_t)(c.f / 256) * bwd_dh_c8_parts_per_tile(c) * 4);
   L.dlogits = take((size_t)c.T * c.E * 4);
   L.dweight = take(rows * 4);
   L.wr_part = take((size_t)kRouterBwdChunks * c.E * c.d * 4);
@@ -1231,7 +1231,7 @@ moe_status_t moe_layer_backward_c8(const moe_config_t* cfg, const void* x, const
   }
   if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_BWD_ROUTER, stream);
-    e = launch_router_bwd(c, dw_part, (int)(c.f / 256), slot_of, topk_idx, topk_w, w_router, dx32, x,
+    e = launch_router_bwd(c, dw_part, (int)(c.f / 256) * bwd_dh_c8_parts_per_tile(c), slot_of, topk_idx, topk_w, w_router, dx32, x,
                           reinterpret_cast<float*>(w8 + S.dlogits), reinterpret_cast<float*>(w8 + S.dweight), dx,
                           dw_router, dbias, reinterpret_cast<float*>(w8 + S.wr_part), stream, ctx, dlogits, true);
   }
