@@ -11,11 +11,17 @@
 // from the choices and the mask alone, (2) one read of the logits that gives
 // both losses and the gradient.  Every input is read once but the mask.
 //
-// Counts of sequences that cross token chunks: the pairs (chunk c, sequence s)
-// that meet form a staircase, each step of which raises c or s, so c + s names
-// a slot of its own; pass 1 writes the pair's counts there and pass 2 sums a
-// sequence's slots.  Integers, so no order matters; the float sums run in a
-// fixed order (thread, warp, chunk), so results do not depend on scheduling.
+// Three forms, each a chain of dependent steps, which is what bounds them up to
+// about 10^5 tokens (a launch adds 2 to 3 us, a round trip to L2 0.5 us):
+//   one chunk of 1024 tokens: one block, everything in shared memory;
+//   up to 8 chunks: one cluster, a block a chunk that keeps its logits in
+//     registers across the cluster's barrier.  The pairs (chunk c, sequence s)
+//     that meet form a staircase, each step of which raises c or s, so c + s
+//     names a slot of its own for the pair's counts;
+//   more: cleared totals per sequence, a kernel that adds the chunks' counts to
+//     them, a kernel for the rest.
+// Counts are integers, so no order matters; the float sums run in a fixed order
+// (thread, warp, chunk), so results do not depend on scheduling.
 #include <math.h>
 
 #include "common.cuh"
@@ -31,7 +37,7 @@ constexpr int kChunk = 1024;   // tokens of a chunk
 constexpr int kTok = kChunk / kNT;
 constexpr int kWindow = 1024;  // sequences held at once (a chunk meets more only if most are empty)
 constexpr int kSlot = 16;      // int32 of a slot: 8 counts, live tokens, padding to 64 bytes
-constexpr int kCluster = 8;    // most blocks of the one-launch form
+constexpr int kCluster = 8;    // most blocks of the cluster form
 
 struct BalanceArgs {
   const float* logits;         // [T, E]
@@ -45,10 +51,10 @@ struct BalanceArgs {
   int32_t* counts;             // [n_seq, E]
   float* loss;                 // [3]: a balance + b z, balance, z
   float* dlogits;              // [T, E] or NULL
-  int32_t* slots;              // [n_chunks + n_seq][kSlot]
-  int32_t* chunk_live;         // [n_chunks]
+  int32_t* slots;              // cluster: [n_chunks + n_seq][kSlot];  totals: [n_seq][kSlot]
+  int32_t* chunk_live;         // cluster: [n_chunks]
   float2* chunk_sum;           // [n_chunks]: sum of sum_e f p, sum of lse^2
-  int32_t* ticket;             // blocks of pass 2 that are done
+  int32_t* ticket;             // [0]: blocks of pass 2 that are done, [1]: live tokens
   int* err;
 };
 
@@ -60,7 +66,6 @@ __device__ __forceinline__ int bound_of(const BalanceArgs& a, int s) {
 struct __align__(16) Shared {
   int hist[kWindow][kE + 1];  // pass 1: counts and live tokens; pass 2: f (as float bits) in [0, E)
   int bound[kWindow + 1];     // offsets of the window's sequences
-  int4 red[kNT / 32][3];
   float2 fred[kNT / 32];
   int ired[kNT / 32];
   int done;
@@ -171,9 +176,8 @@ __device__ __forceinline__ void open_window(const BalanceArgs& a, const Chunk& k
   }
 }
 
-// Pass 1 over chunk c: counts of every sequence that meets the chunk, into its slot.
-__device__ __forceinline__ void count_chunk(const BalanceArgs& a, int c, const Chunk& k, int2 (&e)[kTok],
-                                            int (&seq)[kTok], Shared& sh) {
+// Drops the choices of tokens that are not live; the chunk's live tokens (in every thread).
+__device__ __forceinline__ int live_choices(const BalanceArgs& a, const Chunk& k, int2 (&e)[kTok], Shared& sh) {
   int live = 0;
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
@@ -184,47 +188,43 @@ __device__ __forceinline__ void count_chunk(const BalanceArgs& a, int c, const C
       e[j] = make_int2(-1, -1);
     }
   }
-  for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
-    const int n = min(k.last - w0 + 1, kWindow);
-    for (int i = threadIdx.x; i < n * (kE + 1); i += kNT) (&sh.hist[0][0])[i] = 0;
-    open_window(a, k, w0, n, seq, sh);  // its barrier also covers the zeros
-    if (n == 1) {
-      // one sequence: ballots instead of atomics on the same few words
-#pragma unroll
-      for (int q = 0; q <= kE; ++q) {
-        int cnt = 0;
-#pragma unroll
-        for (int j = 0; j < kTok; ++j)
-          cnt += q < kE ? __popc(__ballot_sync(~0u, seq[j] == 0 && e[j].x == q)) +
-                              __popc(__ballot_sync(~0u, seq[j] == 0 && e[j].y == q))
-                        : __popc(__ballot_sync(~0u, seq[j] == 0));
-        if ((threadIdx.x & 31) == 0 && cnt) atomicAdd(&sh.hist[0][q], cnt);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kTok; ++j) {
-        if (seq[j] >= 0) {
-          if ((unsigned)e[j].x < kE) atomicAdd(&sh.hist[seq[j]][e[j].x], 1);
-          if ((unsigned)e[j].y < kE) atomicAdd(&sh.hist[seq[j]][e[j].y], 1);
-          atomicAdd(&sh.hist[seq[j]][kE], 1);
-        }
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * (kE + 1); i += kNT) {
-      const int s = i / (kE + 1), q = i - s * (kE + 1);
-      a.slots[((int64_t)c + w0 + s) * kSlot + q] = sh.hist[s][q];
-    }
-    __syncthreads();
-  }
-  const int warp_live = __reduce_add_sync(~0u, live);
-  if ((threadIdx.x & 31) == 0) sh.ired[threadIdx.x >> 5] = warp_live;
+  live = __reduce_add_sync(~0u, live);
+  if ((threadIdx.x & 31) == 0) sh.ired[threadIdx.x >> 5] = live;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int sum = 0;
-    for (int w = 0; w < kNT / 32; ++w) sum += sh.ired[w];
-    a.chunk_live[c] = sum;
+  int sum = 0;
+#pragma unroll
+  for (int w = 0; w < kNT / 32; ++w) sum += sh.ired[w];
+  return sum;  // sh.ired is next written after a barrier of count_window
+}
+
+// Counts and live tokens of the n sequences from w0 on, into sh.hist.
+__device__ __forceinline__ void count_window(const BalanceArgs& a, const Chunk& k, int w0, int n, const int2 (&e)[kTok],
+                                             int (&seq)[kTok], Shared& sh) {
+  for (int i = threadIdx.x; i < n * (kE + 1); i += kNT) (&sh.hist[0][0])[i] = 0;
+  open_window(a, k, w0, n, seq, sh);  // its barrier also covers the zeros
+  if (n == 1) {
+    // one sequence: ballots instead of atomics on the same few words
+#pragma unroll
+    for (int q = 0; q <= kE; ++q) {
+      int cnt = 0;
+#pragma unroll
+      for (int j = 0; j < kTok; ++j)
+        cnt += q < kE ? __popc(__ballot_sync(~0u, seq[j] == 0 && e[j].x == q)) +
+                            __popc(__ballot_sync(~0u, seq[j] == 0 && e[j].y == q))
+                      : __popc(__ballot_sync(~0u, seq[j] == 0));
+      if ((threadIdx.x & 31) == 0 && cnt) atomicAdd(&sh.hist[0][q], cnt);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      if (seq[j] >= 0) {
+        if ((unsigned)e[j].x < kE) atomicAdd(&sh.hist[seq[j]][e[j].x], 1);
+        if ((unsigned)e[j].y < kE) atomicAdd(&sh.hist[seq[j]][e[j].y], 1);
+        atomicAdd(&sh.hist[seq[j]][kE], 1);
+      }
+    }
   }
+  __syncthreads();
 }
 
 // A chunk's choices and logits, asked for before it is known which tokens are
@@ -249,11 +249,8 @@ __device__ __forceinline__ void load_logits(const BalanceArgs& a, int c, float (
   }
 }
 
-// Pass 2 over chunk c: f of its sequences, then the tokens' losses and
-// gradients.  same: seq and sh.bound still hold the chunk's one window.
-__device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, const Chunk& k, const float (&l)[kTok][kE],
-                                               float inv_n, bool same, int (&seq)[kTok], Shared& sh) {
-  float sum_f = 0.f, sum_z = 0.f;
+// dlogits 0 for the chunk's tokens that are not live.
+__device__ __forceinline__ void clear_dead(const BalanceArgs& a, const Chunk& k) {
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
     const int64_t t = (int64_t)k.t0 + j * kNT + threadIdx.x;
@@ -262,115 +259,78 @@ __device__ __forceinline__ void gradient_chunk(const BalanceArgs& a, int c, cons
       p[0] = p[1] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
-    const int n = min(k.last - w0 + 1, kWindow);
-    if (!same) open_window(a, k, w0, n, seq, sh);
-    // the chunk's first and last sequence may run through many chunks: the block
-    // sums their slots, 16 bytes a thread, 128 slots at a time
-    for (int i = 0; i < 2; ++i) {
-      const int s = (i == 0 ? k.first : k.last) - w0;
-      if ((i == 1 && k.last == k.first) || s < 0 || s >= n) continue;
-      const int lo = sh.bound[s], hi = sh.bound[s + 1];
-      const int c0 = lo / kChunk, c1 = lo < hi ? (hi - 1) / kChunk : c0 - 1;
-      const int q = threadIdx.x & 3, g = threadIdx.x >> 2;
-      int4 v = make_int4(0, 0, 0, 0);
-      if (q < 3) {
-        const int4* p = reinterpret_cast<const int4*>(a.slots + ((int64_t)w0 + s) * kSlot) + q;
-#pragma unroll 4
-        for (int cc = c0 + g; cc <= c1; cc += kNT / 4) {
-          const int4 u = __ldcg(p + (int64_t)cc * (kSlot / 4));
-          v.x += u.x;
-          v.y += u.y;
-          v.z += u.z;
-          v.w += u.w;
-        }
-        // the eight groups of a warp, then the warps
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          v.x += __shfl_xor_sync(0x77777777u, v.x, o);
-          v.y += __shfl_xor_sync(0x77777777u, v.y, o);
-          v.z += __shfl_xor_sync(0x77777777u, v.z, o);
-          v.w += __shfl_xor_sync(0x77777777u, v.w, o);
-        }
-        if ((threadIdx.x & 31) < 3) sh.red[threadIdx.x >> 5][q] = v;
-      }
-      __syncthreads();
-      if (threadIdx.x <= kE) {
-        int sum = 0;
-        for (int w = 0; w < kNT / 32; ++w) sum += reinterpret_cast<const int*>(&sh.red[w][0])[threadIdx.x];
-        sh.hist[s][threadIdx.x] = sum;
-      }
-      __syncthreads();
+}
+
+// sh.hist of the window, now the sequences' totals, to f (as float bits); the
+// chunk that holds a sequence's first token writes its counts.
+__device__ __forceinline__ void counts_to_f(const BalanceArgs& a, int c, int w0, int n, Shared& sh) {
+  for (int i = threadIdx.x; i < n; i += kNT) {
+    if (sh.bound[i] < sh.bound[i + 1] && sh.bound[i] / kChunk == c) {
+      int4* o = reinterpret_cast<int4*>(a.counts + ((int64_t)w0 + i) * kE);
+      o[0] = make_int4(sh.hist[i][0], sh.hist[i][1], sh.hist[i][2], sh.hist[i][3]);
+      o[1] = make_int4(sh.hist[i][4], sh.hist[i][5], sh.hist[i][6], sh.hist[i][7]);
     }
-    // the others lie in this chunk alone: one slot each (an empty one has none)
-    for (int i = threadIdx.x; i < n * (kE + 1); i += kNT) {
-      const int s = i / (kE + 1), q = i - s * (kE + 1);
-      if (w0 + s != k.first && w0 + s != k.last)
-        sh.hist[s][q] = sh.bound[s] < sh.bound[s + 1] ? __ldcg(a.slots + ((int64_t)c + w0 + s) * kSlot + q) : 0;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kNT) {
-      // the chunk that holds a sequence's first token writes its counts
-      const bool mine = sh.bound[i] < sh.bound[i + 1] && sh.bound[i] / kChunk == c;
-      if (mine) {
-        int4* o = reinterpret_cast<int4*>(a.counts + ((int64_t)w0 + i) * kE);
-        o[0] = make_int4(sh.hist[i][0], sh.hist[i][1], sh.hist[i][2], sh.hist[i][3]);
-        o[1] = make_int4(sh.hist[i][4], sh.hist[i][5], sh.hist[i][6], sh.hist[i][7]);
-      }
-      const int live = sh.hist[i][kE];
-      const float half = live > 0 ? 0.5f / (float)live : 0.f;
+    const int live = sh.hist[i][kE];
+    const float half = live > 0 ? 0.5f / (float)live : 0.f;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) sh.hist[i][e] = __float_as_int((float)sh.hist[i][e] * half);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      if (seq[j] < 0) continue;
-      float top = l[j][0];
-#pragma unroll
-      for (int e = 1; e < kE; ++e) top = fmaxf(top, l[j][e]);
-      float p[kE], f[kE], total = 0.f, dot = 0.f;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        p[e] = expf(l[j][e] - top);
-        total += p[e];
-        f[e] = __int_as_float(sh.hist[seq[j]][e]);
-      }
-      const float inv = 1.0f / total;
-      const float lse = top + logf(total);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        p[e] *= inv;
-        dot = fmaf(f[e], p[e], dot);
-      }
-      sum_f += dot;
-      sum_z = fmaf(lse, lse, sum_z);
-      if (a.dlogits) {
-        const float ka = a.a * (float)kE * inv_n, kb = 2.0f * a.b * inv_n * lse;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) p[e] *= fmaf(ka, f[e] - dot, kb);
-        float4* o = reinterpret_cast<float4*>(a.dlogits) + 2 * ((int64_t)k.t0 + j * kNT + threadIdx.x);
-        o[0] = make_float4(p[0], p[1], p[2], p[3]);
-        o[1] = make_float4(p[4], p[5], p[6], p[7]);
-      }
-    }
-    __syncthreads();
+    for (int e = 0; e < kE; ++e) sh.hist[i][e] = __float_as_int((float)sh.hist[i][e] * half);
   }
+  __syncthreads();
+}
+
+// The window's tokens: gradients, and their part of the two sums.
+__device__ __forceinline__ void window_tokens(const BalanceArgs& a, const Chunk& k, const float (&l)[kTok][kE],
+                                              const int (&seq)[kTok], float inv_n, float2& sum, const Shared& sh) {
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    if (seq[j] < 0) continue;
+    float top = l[j][0];
+#pragma unroll
+    for (int e = 1; e < kE; ++e) top = fmaxf(top, l[j][e]);
+    float p[kE], f[kE], total = 0.f, dot = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      p[e] = expf(l[j][e] - top);
+      total += p[e];
+      f[e] = __int_as_float(sh.hist[seq[j]][e]);
+    }
+    const float inv = 1.0f / total;
+    const float lse = top + logf(total);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) {
+      p[e] *= inv;
+      dot = fmaf(f[e], p[e], dot);
+    }
+    sum.x += dot;
+    sum.y = fmaf(lse, lse, sum.y);
+    if (a.dlogits) {
+      const float ka = a.a * (float)kE * inv_n, kb = 2.0f * a.b * inv_n * lse;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) p[e] *= fmaf(ka, f[e] - dot, kb);
+      float4* o = reinterpret_cast<float4*>(a.dlogits) + 2 * ((int64_t)k.t0 + j * kNT + threadIdx.x);
+      o[0] = make_float4(p[0], p[1], p[2], p[3]);
+      o[1] = make_float4(p[4], p[5], p[6], p[7]);
+    }
+  }
+}
+
+// The block's sum, in thread 0.
+__device__ __forceinline__ float2 block_sum(float2 s, Shared& sh) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    sum_f += __shfl_xor_sync(~0u, sum_f, o);
-    sum_z += __shfl_xor_sync(~0u, sum_z, o);
+    s.x += __shfl_xor_sync(~0u, s.x, o);
+    s.y += __shfl_xor_sync(~0u, s.y, o);
   }
-  if ((threadIdx.x & 31) == 0) sh.fred[threadIdx.x >> 5] = make_float2(sum_f, sum_z);
+  if ((threadIdx.x & 31) == 0) sh.fred[threadIdx.x >> 5] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    float2 s = sh.fred[0];
+    s = sh.fred[0];
     for (int w = 1; w < kNT / 32; ++w) {
       s.x += sh.fred[w].x;
       s.y += sh.fred[w].y;
     }
-    a.chunk_sum[c] = s;
   }
+  return s;
 }
 
 // Zero counts of the empty sequences and the check of the offsets, shared out over `parts` blocks.
@@ -387,17 +347,12 @@ __device__ __forceinline__ void empty_counts(const BalanceArgs& a, int part, int
   }
 }
 
-// N, the live tokens of all chunks, by all threads of a block.
-__device__ __forceinline__ int total_live(const BalanceArgs& a, Shared& sh) {
-  int v = 0;
-  for (int c = threadIdx.x; c < a.n_chunks; c += kNT) v += __ldcg(a.chunk_live + c);
-  v = __reduce_add_sync(~0u, v);
-  if ((threadIdx.x & 31) == 0) sh.ired[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int n = 0;
-  for (int w = 0; w < kNT / 32; ++w) n += sh.ired[w];
-  __syncthreads();
-  return n;
+__device__ __forceinline__ void store_loss(const BalanceArgs& a, double f, double z, int n) {
+  const double inv = n > 0 ? 1.0 / (double)n : 0.0;
+  const double balance = (double)kE * f * inv, zl = z * inv;
+  a.loss[0] = (float)((double)a.a * balance + (double)a.b * zl);
+  a.loss[1] = (float)balance;
+  a.loss[2] = (float)zl;
 }
 
 // The losses from the chunks' sums, in double and in a fixed order, by one block.
@@ -408,39 +363,125 @@ __device__ __forceinline__ void write_loss(const BalanceArgs& a, int n, Shared& 
     f += (double)v.x;
     z += (double)v.y;
   }
-  if (a.n_chunks > 1) {
-    double2* red = reinterpret_cast<double2*>(&sh.hist[0][0]);
-    red[threadIdx.x] = make_double2(f, z);
-    __syncthreads();
-    for (int w = kNT / 2; w > 0; w >>= 1) {
-      if ((int)threadIdx.x < w) {
-        red[threadIdx.x].x += red[threadIdx.x + w].x;
-        red[threadIdx.x].y += red[threadIdx.x + w].y;
-      }
-      __syncthreads();
-    }
-    f = red[0].x;
-    z = red[0].y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    f += __shfl_xor_sync(~0u, f, o);
+    z += __shfl_xor_sync(~0u, z, o);
   }
+  double2* red = reinterpret_cast<double2*>(&sh.hist[0][0]);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_double2(f, z);
+  __syncthreads();
   if (threadIdx.x == 0) {
-    const double inv = n > 0 ? 1.0 / (double)n : 0.0;
-    const double balance = (double)kE * f * inv, zl = z * inv;
-    a.loss[0] = (float)((double)a.a * balance + (double)a.b * zl);
-    a.loss[1] = (float)balance;
-    a.loss[2] = (float)zl;
+    for (int w = 1; w < kNT / 32; ++w) {
+      f += red[w].x;
+      z += red[w].y;
+    }
+    store_loss(a, f, z, n);
   }
+}
+
+// One chunk: counts, f, gradients and losses in one block.
+__global__ void __launch_bounds__(kNT, 1) balance_single_kernel(const BalanceArgs a) {
+  __shared__ Shared sh;
+  pdl_wait();
+  float l[kTok][kE];
+  int2 e[kTok];
+  load_logits(a, 0, l);
+  load_choices(a, 0, e);
+  const Chunk k = open_chunk(a, 0, sh);
+  empty_counts(a, 0, 1);
+  clear_dead(a, k);
+  const int n = live_choices(a, k, e, sh);
+  const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
+  float2 sum = make_float2(0.f, 0.f);
+  for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
+    const int m = min(k.last - w0 + 1, kWindow);
+    int seq[kTok];
+    count_window(a, k, w0, m, e, seq, sh);
+    counts_to_f(a, 0, w0, m, sh);
+    window_tokens(a, k, l, seq, inv_n, sum, sh);
+    __syncthreads();
+  }
+  sum = block_sum(sum, sh);
+  if (threadIdx.x == 0) store_loss(a, (double)sum.x, (double)sum.y, n);
+}
+
+__global__ void __launch_bounds__(kNT, 1) balance_cluster_kernel(const BalanceArgs a) {
+  __shared__ Shared sh;
+  pdl_wait();
+  const int c = blockIdx.x;
+  float l[kTok][kE];
+  int2 e[kTok];
+  load_logits(a, c, l);
+  load_choices(a, c, e);
+  const Chunk k = open_chunk(a, c, sh);
+  empty_counts(a, c, gridDim.x);
+  const int mine = live_choices(a, k, e, sh);
+  int seq[kTok];
+  for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
+    const int m = min(k.last - w0 + 1, kWindow);
+    count_window(a, k, w0, m, e, seq, sh);
+    for (int i = threadIdx.x; i < m * (kE + 1); i += kNT) {
+      const int s = i / (kE + 1), q = i - s * (kE + 1);
+      a.slots[((int64_t)c + w0 + s) * kSlot + q] = sh.hist[s][q];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.chunk_live[c] = mine;
+  ptx::cluster_sync();  // the slots and live tokens of all chunks are written
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i)
+    if (i < a.n_chunks) n += __ldcg(a.chunk_live + i);
+  const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
+  clear_dead(a, k);
+  float2 sum = make_float2(0.f, 0.f);
+  const bool same = k.last - k.first < kWindow;  // seq and sh.bound still hold the only window
+  for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
+    const int m = min(k.last - w0 + 1, kWindow);
+    if (!same) open_window(a, k, w0, m, seq, sh);
+    // a sequence's slots: one for each chunk that it meets
+    for (int i = threadIdx.x; i < m * (kE + 1); i += kNT) {
+      const int s = i / (kE + 1), q = i - s * (kE + 1);
+      const int lo = sh.bound[s], hi = sh.bound[s + 1];
+      const int c0 = lo / kChunk, c1 = lo < hi ? (hi - 1) / kChunk : -1;
+      int v = 0;
+#pragma unroll
+      for (int j = 0; j < kCluster; ++j)
+        if (j >= c0 && j <= c1 && j < a.n_chunks) v += __ldcg(a.slots + ((int64_t)j + w0 + s) * kSlot + q);
+      sh.hist[s][q] = v;
+    }
+    __syncthreads();
+    counts_to_f(a, c, w0, m, sh);
+    window_tokens(a, k, l, seq, inv_n, sum, sh);
+    __syncthreads();
+  }
+  sum = block_sum(sum, sh);
+  if (threadIdx.x == 0) a.chunk_sum[c] = sum;
+  ptx::cluster_sync();  // the chunks' sums are written
+  if (c == 0) write_loss(a, n, sh);
 }
 
 __global__ void __launch_bounds__(kNT, 2) balance_count_kernel(const BalanceArgs a) {
   __shared__ Shared sh;
   pdl_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0;
   empty_counts(a, blockIdx.x, gridDim.x);
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
     int2 e[kTok];
     load_choices(a, c, e);
-    int seq[kTok];
-    count_chunk(a, c, open_chunk(a, c, sh), e, seq, sh);
+    const Chunk k = open_chunk(a, c, sh);
+    const int live = live_choices(a, k, e, sh);
+    if (threadIdx.x == 0) atomicAdd(a.ticket + 1, live);
+    for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
+      const int m = min(k.last - w0 + 1, kWindow);
+      int seq[kTok];
+      count_window(a, k, w0, m, e, seq, sh);
+      for (int i = threadIdx.x; i < m * (kE + 1); i += kNT) {
+        const int s = i / (kE + 1), q = i - s * (kE + 1), v = sh.hist[s][q];
+        if (v) atomicAdd(a.slots + ((int64_t)w0 + s) * kSlot + q, v);
+      }
+      __syncthreads();
+    }
     __syncthreads();
   }
 }
@@ -448,14 +489,35 @@ __global__ void __launch_bounds__(kNT, 2) balance_count_kernel(const BalanceArgs
 __global__ void __launch_bounds__(kNT, 2) balance_gradient_kernel(const BalanceArgs a) {
   __shared__ Shared sh;
   pdl_wait();
-  int n = -1;
+  const int n = __ldcg(a.ticket + 1);
+  const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
     float l[kTok][kE];
     load_logits(a, c, l);
-    if (n < 0) n = total_live(a, sh);
     const Chunk k = open_chunk(a, c, sh);
-    int seq[kTok];
-    gradient_chunk(a, c, k, l, n > 0 ? 1.0f / (float)n : 0.f, false, seq, sh);
+    clear_dead(a, k);
+    float2 sum = make_float2(0.f, 0.f);
+    for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
+      const int m = min(k.last - w0 + 1, kWindow);
+      for (int i = threadIdx.x; i < m * 3; i += kNT) {
+        const int s = i / 3, q = i - s * 3;
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(a.slots + ((int64_t)w0 + s) * kSlot) + q);
+        int* h = &sh.hist[s][4 * q];
+        h[0] = v.x;
+        if (q < 2) {
+          h[1] = v.y;
+          h[2] = v.z;
+          h[3] = v.w;
+        }
+      }
+      int seq[kTok];
+      open_window(a, k, w0, m, seq, sh);  // its barrier also covers the totals
+      counts_to_f(a, c, w0, m, sh);
+      window_tokens(a, k, l, seq, inv_n, sum, sh);
+      __syncthreads();
+    }
+    sum = block_sum(sum, sh);
+    if (threadIdx.x == 0) a.chunk_sum[c] = sum;
     __syncthreads();
   }
   // the block that finishes last adds up the chunks' sums
@@ -466,27 +528,6 @@ __global__ void __launch_bounds__(kNT, 2) balance_gradient_kernel(const BalanceA
   }
   __syncthreads();
   if (sh.done) write_loss(a, n, sh);
-}
-
-// Both passes in one launch, for at most kCluster chunks: one cluster, a block
-// a chunk, which keeps its logits in registers across the cluster's barrier.
-__global__ void __launch_bounds__(kNT, 1) balance_cluster_kernel(const BalanceArgs a) {
-  __shared__ Shared sh;
-  pdl_wait();
-  const int c = blockIdx.x;
-  float l[kTok][kE];
-  load_logits(a, c, l);
-  int2 e[kTok];
-  load_choices(a, c, e);
-  const Chunk k = open_chunk(a, c, sh);
-  empty_counts(a, blockIdx.x, gridDim.x);
-  int seq[kTok];
-  count_chunk(a, c, k, e, seq, sh);
-  ptx::cluster_sync();  // the slots and live tokens of all chunks are written
-  const int n = total_live(a, sh);
-  gradient_chunk(a, c, k, l, n > 0 ? 1.0f / (float)n : 0.f, k.last - k.first < kWindow, seq, sh);
-  ptx::cluster_sync();  // and their sums
-  if (c == 0) write_loss(a, n, sh);
 }
 
 }  // namespace
@@ -512,24 +553,29 @@ cudaError_t launch_balance(const moe_config_t& c, const float* logits, const int
   a.counts = counts;
   a.loss = loss;
   a.dlogits = dlogits;
-  a.slots = static_cast<int32_t*>(ws);
+  a.ticket = static_cast<int32_t*>(ws);  // 64 bytes
+  a.slots = a.ticket + 16;
   a.chunk_sum = reinterpret_cast<float2*>(a.slots + ((int64_t)a.n_chunks + n_seq) * kSlot);
   a.chunk_live = reinterpret_cast<int32_t*>(a.chunk_sum + a.n_chunks);
-  a.ticket = a.chunk_live + a.n_chunks;
   a.err = ctx.err;
-  if (a.n_chunks <= kCluster) {
+  cudaError_t e;
+  if (a.n_chunks == 1) {
+    e = launch_pdl(balance_single_kernel, dim3(1), dim3(kNT), 0, s, no_extra_attr(), a);
+  } else if (a.n_chunks <= kCluster) {
     cudaLaunchAttribute cl = {};
     cl.id = cudaLaunchAttributeClusterDimension;
     cl.val.clusterDim.x = (unsigned)a.n_chunks;
     cl.val.clusterDim.y = cl.val.clusterDim.z = 1;
-    const cudaError_t e = launch_pdl(balance_cluster_kernel, dim3(a.n_chunks), dim3(kNT), 0, s, cl, a);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    e = launch_pdl(balance_cluster_kernel, dim3(a.n_chunks), dim3(kNT), 0, s, cl, a);
+  } else {
+    e = cudaMemsetAsync(ws, 0, (size_t)(16 + (int64_t)n_seq * kSlot) * 4, s);
+    if (e != cudaSuccess) return e;
+    const int cap = ctx.num_sms * 2;
+    const int grid = a.n_chunks < cap ? a.n_chunks : cap;
+    e = launch_pdl(balance_count_kernel, dim3(grid), dim3(kNT), 0, s, no_extra_attr(), a);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(balance_gradient_kernel, dim3(grid), dim3(kNT), 0, s, no_extra_attr(), a);
   }
-  const int cap = ctx.num_sms * 2;
-  const int grid = a.n_chunks < cap ? a.n_chunks : cap;
-  cudaError_t e = launch_pdl(balance_count_kernel, dim3(grid), dim3(kNT), 0, s, no_extra_attr(), a);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(balance_gradient_kernel, dim3(grid), dim3(kNT), 0, s, no_extra_attr(), a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
