@@ -545,8 +545,8 @@ MOE_API moe_status_t moe_expert_utilization(const int32_t* stats, int32_t E, int
  * leave [0, T] set MOE_DEVERR_OFFSETS (the outputs are then unspecified); an
  * index outside [0, E) sets MOE_DEVERR_EXPERT_INDEX and is not counted.
  * Sums have a fixed order: results do not depend on scheduling.  T == 0 writes
- * zeros.  ws: moe_balance_loss_workspace_size bytes of scratch, used by one
- * call at a time. */
+ * zeros.  ws: moe_balance_loss_workspace_size bytes of scratch (0 up to 1024
+ * tokens: ws may then be NULL), used by one call at a time. */
 #define MOE_BALANCE_MAX_SEQS (1 << 24)
 MOE_API size_t moe_balance_loss_workspace_size(const moe_config_t* cfg, int32_t n_seq);
 MOE_API moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logits, const int32_t* topk_idx,

@@ -196,9 +196,11 @@ def _dev_ptr(t):
 
 
 def _stream(stream, device=None):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if device is not None and device.index is not None:
+        return torch._C._cuda_getCurrentRawStream(device.index)  # 2 us less than through a Stream object
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _check(status: int, where: str):
@@ -230,7 +232,7 @@ def _expect_layer(cfg, x=None, w_router=None, w_gate=None, w_up=None, w_down=Non
 
 
 def _empty(shape, dtype, like):
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    return like.new_empty(shape, dtype=dtype)
 
 
 _HERE = contextlib.nullcontext()
@@ -720,23 +722,26 @@ def balance_loss(cfg: Config, logits, topk_idx, token_mask=None, seq_offsets=Non
         n_seq = seq_offsets.numel() - 1
         if seq_offsets.dtype != torch.int32 or n_seq < 1:
             raise ValueError("seq_offsets must be int32 with at least two entries")
-    o = dict(out or {})
-    o.setdefault("loss", _empty((3,), torch.float32, logits))
-    o.setdefault("counts", _empty((n_seq, cfg.E), torch.int32, logits))
-    if want_grad:
-        o.setdefault("dlogits", _empty((cfg.T, cfg.E), torch.float32, logits))
-    else:
+    o = dict(out) if out else {}
+    if "loss" not in o:
+        o["loss"] = _empty((3,), torch.float32, logits)
+    if "counts" not in o:
+        o["counts"] = _empty((n_seq, cfg.E), torch.int32, logits)
+    if not want_grad:
         o["dlogits"] = None
+    elif "dlogits" not in o:
+        o["dlogits"] = _empty((cfg.T, cfg.E), torch.float32, logits)
     _expect("loss", o["loss"], 3, torch.float32)
     _expect("counts", o["counts"], n_seq * cfg.E, torch.int32)
     _expect("dlogits", o["dlogits"], cfg.T * cfg.E, torch.float32)
     if ws is None:
-        ws = _empty((max(balance_loss_workspace_size(cfg, n_seq), 1),), torch.uint8, logits)
+        need = balance_loss_workspace_size(cfg, n_seq)
+        ws = _empty((need,), torch.uint8, logits) if need else None
     with _same_device(logits, topk_idx, token_mask, seq_offsets, ws, *o.values()):
         _check(lib.moe_balance_loss(cfg.ref, _dev_ptr(logits), _dev_ptr(topk_idx), _dev_ptr(token_mask),
                                     _dev_ptr(seq_offsets), n_seq, float(balance_coef), float(z_coef),
                                     _dev_ptr(o["counts"]), _dev_ptr(o["loss"]), _dev_ptr(o["dlogits"]), _dev_ptr(ws),
-                                    ws.numel() * ws.element_size(), _stream(stream, logits.device)),
+                                    0 if ws is None else _nbytes(ws), _stream(stream, logits.device)),
                "moe_balance_loss")
     return o
 

@@ -14,7 +14,7 @@
 // Three forms, each a chain of dependent steps, which is what bounds them up to
 // about 10^5 tokens (a launch adds 2 to 3 us, a round trip to L2 0.5 us):
 //   one chunk of 1024 tokens: one block, everything in shared memory;
-//   up to 8 chunks: one cluster, a block a chunk that keeps its logits in
+//   up to 16 chunks: one cluster, a block a chunk that keeps its logits in
 //     registers across the cluster's barrier.  The pairs (chunk c, sequence s)
 //     that meet form a staircase, each step of which raises c or s, so c + s
 //     names a slot of its own for the pair's counts;
@@ -23,6 +23,8 @@
 // Counts are integers, so no order matters; the float sums run in a fixed order
 // (thread, warp, chunk), so results do not depend on scheduling.
 #include <math.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -37,7 +39,7 @@ constexpr int kChunk = 1024;   // tokens of a chunk
 constexpr int kTok = kChunk / kNT;
 constexpr int kWindow = 1024;  // sequences held at once (a chunk meets more only if most are empty)
 constexpr int kSlot = 16;      // int32 of a slot: 8 counts, live tokens, padding to 64 bytes
-constexpr int kCluster = 8;    // most blocks of the cluster form
+constexpr int kCluster = 16;   // most blocks of the cluster form
 
 struct BalanceArgs {
   const float* logits;         // [T, E]
@@ -59,14 +61,16 @@ struct BalanceArgs {
 };
 
 __device__ __forceinline__ int bound_of(const BalanceArgs& a, int s) {
-  const int64_t v = a.seq ? (int64_t)__ldg(a.seq + s) : (s == 0 ? 0 : a.T);
-  return (int)(v < 0 ? 0 : (v > a.T ? a.T : v));
+  const int T = (int)a.T;  // at most 2^24
+  const int v = a.seq ? __ldg(a.seq + s) : (s == 0 ? 0 : T);
+  return min(max(v, 0), T);
 }
 
 struct __align__(16) Shared {
   int hist[kWindow][kE + 1];  // pass 1: counts and live tokens; pass 2: f (as float bits) in [0, E)
   int bound[kWindow + 1];     // offsets of the window's sequences
   float2 fred[kNT / 32];
+  unsigned found[kNT / 32];
   int ired[kNT / 32];
   int done;
 };
@@ -102,37 +106,25 @@ __device__ __forceinline__ int block_seq_of(const BalanceArgs& a, int t) {
 __device__ __forceinline__ int2 block_seqs_of(const BalanceArgs& a, int t0, int t1, Shared& sh) {
   if (a.n_seq > kNT * kScan) return make_int2(block_seq_of(a, t0), block_seq_of(a, t1));
   int c0 = 0, c1 = 0;
-#pragma unroll
-  for (int i = 0; i < kScan; ++i) {
-    const int s = i * kNT + (int)threadIdx.x;
-    if (s < a.n_seq) {
-      const int v = bound_of(a, s + 1);
-      c0 += v <= t0;
-      c1 += v <= t1;
-    }
+  for (int s = threadIdx.x; s < a.n_seq; s += kNT) {
+    const int v = bound_of(a, s + 1);
+    c0 += v <= t0;
+    c1 += v <= t1;
   }
-  const unsigned both = __reduce_add_sync(~0u, (unsigned)c0 | (unsigned)c1 << 16);  // at most 256 each
-  if ((threadIdx.x & 31) == 0) sh.ired[threadIdx.x >> 5] = (int)both;
+  // at most 4096 in all: both in one word.  sh.found is next written a chunk
+  // later, behind other barriers
+  const unsigned both = __reduce_add_sync(~0u, (unsigned)c0 | (unsigned)c1 << 16);
+  if ((threadIdx.x & 31) == 0) sh.found[threadIdx.x >> 5] = both;
   __syncthreads();
-  c0 = c1 = 0;
+  unsigned sum = 0;
 #pragma unroll
-  for (int w = 0; w < kNT / 32; ++w) {
-    c0 += sh.ired[w] & 0xffff;
-    c1 += (int)((unsigned)sh.ired[w] >> 16);
-  }
-  __syncthreads();
-  return make_int2(c0, c1);
+  for (int w = 0; w < kNT / 32; ++w) sum += sh.found[w];
+  return make_int2((int)(sum & 0xffffu), (int)(sum >> 16));
 }
 
-__device__ __forceinline__ Chunk open_chunk(const BalanceArgs& a, int c, Shared& sh) {
+__device__ __forceinline__ Chunk open_chunk(const BalanceArgs& a, int c, const uint8_t (&mask)[kTok], Shared& sh) {
   Chunk k;
   k.t0 = c * kChunk;
-  uint8_t mask[kTok];
-#pragma unroll
-  for (int j = 0; j < kTok; ++j) {  // in flight during the search
-    const int64_t t = (int64_t)k.t0 + j * kNT + threadIdx.x;
-    mask[j] = t < a.T ? (a.mask ? __ldg(a.mask + t) : 1) : 0;
-  }
   const int begin = bound_of(a, 0), end = bound_of(a, a.n_seq);
   int64_t t1 = (int64_t)k.t0 + kChunk;
   if (t1 > end) t1 = end;
@@ -202,33 +194,45 @@ __device__ __forceinline__ void count_window(const BalanceArgs& a, const Chunk& 
                                              int (&seq)[kTok], Shared& sh) {
   for (int i = threadIdx.x; i < n * (kE + 1); i += kNT) (&sh.hist[0][0])[i] = 0;
   open_window(a, k, w0, n, seq, sh);  // its barrier also covers the zeros
-  if (n == 1) {
-    // one sequence: ballots instead of atomics on the same few words
 #pragma unroll
-    for (int q = 0; q <= kE; ++q) {
-      int cnt = 0;
-#pragma unroll
-      for (int j = 0; j < kTok; ++j)
-        cnt += q < kE ? __popc(__ballot_sync(~0u, seq[j] == 0 && e[j].x == q)) +
-                            __popc(__ballot_sync(~0u, seq[j] == 0 && e[j].y == q))
-                      : __popc(__ballot_sync(~0u, seq[j] == 0));
-      if ((threadIdx.x & 31) == 0 && cnt) atomicAdd(&sh.hist[0][q], cnt);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
+  for (int j = 0; j < kTok; ++j) {
+    // 32 neighbouring tokens mostly lie in one sequence: then the warp adds up
+    // eight one-byte counts in two words (64 at most in a byte) and nine lanes add
+    // them to the sequence's, where all lanes would queue at the same words
+    const unsigned live = __ballot_sync(~0u, seq[j] >= 0);
+    if (live == 0) continue;
+    const int s0 = __shfl_sync(~0u, seq[j], __ffs(live) - 1);
+    if (__all_sync(~0u, seq[j] < 0 || seq[j] == s0)) {
+      unsigned long long v = 0;
       if (seq[j] >= 0) {
-        if ((unsigned)e[j].x < kE) atomicAdd(&sh.hist[seq[j]][e[j].x], 1);
-        if ((unsigned)e[j].y < kE) atomicAdd(&sh.hist[seq[j]][e[j].y], 1);
-        atomicAdd(&sh.hist[seq[j]][kE], 1);
+        if ((unsigned)e[j].x < kE) v += 1ull << (8 * e[j].x);
+        if ((unsigned)e[j].y < kE) v += 1ull << (8 * e[j].y);
       }
+      const unsigned lo = __reduce_add_sync(~0u, (unsigned)v), hi = __reduce_add_sync(~0u, (unsigned)(v >> 32));
+      const int lane = threadIdx.x & 31;
+      if (lane <= kE) {
+        const int mine = lane == kE ? __popc(live) : (int)(((lane < 4 ? lo : hi) >> (8 * (lane & 3))) & 0xffu);
+        if (mine) atomicAdd(&sh.hist[s0][lane], mine);
+      }
+    } else if (seq[j] >= 0) {
+      if ((unsigned)e[j].x < kE) atomicAdd(&sh.hist[seq[j]][e[j].x], 1);
+      if ((unsigned)e[j].y < kE) atomicAdd(&sh.hist[seq[j]][e[j].y], 1);
+      atomicAdd(&sh.hist[seq[j]][kE], 1);
     }
   }
   __syncthreads();
 }
 
-// A chunk's choices and logits, asked for before it is known which tokens are
-// live (a padded row's values are dropped), so that they travel during the search.
+// A chunk's masks, choices and logits, asked for before it is known which tokens
+// are live (a padded row's values are dropped), so that they travel during the
+// search, or while the block works on the chunk before.
+__device__ __forceinline__ void load_masks(const BalanceArgs& a, int c, uint8_t (&mask)[kTok]) {
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    const int64_t t = (int64_t)c * kChunk + j * kNT + threadIdx.x;
+    mask[j] = t < a.T ? (a.mask ? __ldg(a.mask + t) : 1) : 0;
+  }
+}
 __device__ __forceinline__ void load_choices(const BalanceArgs& a, int c, int2 (&e)[kTok]) {
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
@@ -290,12 +294,12 @@ __device__ __forceinline__ void window_tokens(const BalanceArgs& a, const Chunk&
     float p[kE], f[kE], total = 0.f, dot = 0.f;
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
-      p[e] = expf(l[j][e] - top);
+      p[e] = __expf(l[j][e] - top);  // a few ulp, as the logarithm and quotient below
       total += p[e];
       f[e] = __int_as_float(sh.hist[seq[j]][e]);
     }
-    const float inv = 1.0f / total;
-    const float lse = top + logf(total);
+    const float inv = __fdividef(1.0f, total);
+    const float lse = top + __logf(total);
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
       p[e] *= inv;
@@ -386,9 +390,11 @@ __global__ void __launch_bounds__(kNT, 1) balance_single_kernel(const BalanceArg
   pdl_wait();
   float l[kTok][kE];
   int2 e[kTok];
+  uint8_t mask[kTok];
+  load_masks(a, 0, mask);
   load_logits(a, 0, l);
   load_choices(a, 0, e);
-  const Chunk k = open_chunk(a, 0, sh);
+  const Chunk k = open_chunk(a, 0, mask, sh);
   empty_counts(a, 0, 1);
   clear_dead(a, k);
   const int n = live_choices(a, k, e, sh);
@@ -412,9 +418,11 @@ __global__ void __launch_bounds__(kNT, 1) balance_cluster_kernel(const BalanceAr
   const int c = blockIdx.x;
   float l[kTok][kE];
   int2 e[kTok];
+  uint8_t mask[kTok];
+  load_masks(a, c, mask);
   load_logits(a, c, l);
   load_choices(a, c, e);
-  const Chunk k = open_chunk(a, c, sh);
+  const Chunk k = open_chunk(a, c, mask, sh);
   empty_counts(a, c, gridDim.x);
   const int mine = live_choices(a, k, e, sh);
   int seq[kTok];
@@ -466,10 +474,19 @@ __global__ void __launch_bounds__(kNT, 2) balance_count_kernel(const BalanceArgs
   __shared__ Shared sh;
   pdl_wait();
   empty_counts(a, blockIdx.x, gridDim.x);
+  uint8_t mask[kTok];
+  int2 next[kTok];
+  load_masks(a, blockIdx.x, mask);
+  load_choices(a, blockIdx.x, next);
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
+    const Chunk k = open_chunk(a, c, mask, sh);
     int2 e[kTok];
-    load_choices(a, c, e);
-    const Chunk k = open_chunk(a, c, sh);
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) e[j] = next[j];
+    if (c + (int)gridDim.x < a.n_chunks) {
+      load_masks(a, c + gridDim.x, mask);
+      load_choices(a, c + gridDim.x, next);
+    }
     const int live = live_choices(a, k, e, sh);
     if (threadIdx.x == 0) atomicAdd(a.ticket + 1, live);
     for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
@@ -482,7 +499,7 @@ __global__ void __launch_bounds__(kNT, 2) balance_count_kernel(const BalanceArgs
       }
       __syncthreads();
     }
-    __syncthreads();
+    if (k.last < k.first) __syncthreads();  // no window's barriers before sh.ired is written again
   }
 }
 
@@ -491,10 +508,21 @@ __global__ void __launch_bounds__(kNT, 2) balance_gradient_kernel(const BalanceA
   pdl_wait();
   const int n = __ldcg(a.ticket + 1);
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
+  uint8_t mask[kTok];
+  float next[kTok][kE];
+  load_masks(a, blockIdx.x, mask);
+  load_logits(a, blockIdx.x, next);
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
+    const Chunk k = open_chunk(a, c, mask, sh);
     float l[kTok][kE];
-    load_logits(a, c, l);
-    const Chunk k = open_chunk(a, c, sh);
+#pragma unroll
+    for (int j = 0; j < kTok; ++j)
+#pragma unroll
+      for (int e = 0; e < kE; ++e) l[j][e] = next[j][e];
+    if (c + (int)gridDim.x < a.n_chunks) {
+      load_masks(a, c + gridDim.x, mask);
+      load_logits(a, c + gridDim.x, next);
+    }
     clear_dead(a, k);
     float2 sum = make_float2(0.f, 0.f);
     for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
@@ -514,11 +542,11 @@ __global__ void __launch_bounds__(kNT, 2) balance_gradient_kernel(const BalanceA
       open_window(a, k, w0, m, seq, sh);  // its barrier also covers the totals
       counts_to_f(a, c, w0, m, sh);
       window_tokens(a, k, l, seq, inv_n, sum, sh);
-      __syncthreads();
+      if (w0 + kWindow <= k.last) __syncthreads();
     }
-    sum = block_sum(sum, sh);
+    sum = block_sum(sum, sh);  // its barrier ends the use of sh.hist
     if (threadIdx.x == 0) a.chunk_sum[c] = sum;
-    __syncthreads();
+    if (k.last < k.first) __syncthreads();  // no window's barriers before sh.fred is written again
   }
   // the block that finishes last adds up the chunks' sums
   if (threadIdx.x == 0) {
@@ -530,10 +558,37 @@ __global__ void __launch_bounds__(kNT, 2) balance_gradient_kernel(const BalanceA
   if (sh.done) write_loss(a, n, sh);
 }
 
+// Blocks that one cluster can have on this device: kCluster where 16 are
+// accepted (a form beyond the portable 8), asked once per device.
+int cluster_limit(const Ctx& ctx) {
+  static std::atomic<int> cached[64];
+  const int slot = ctx.dev >= 0 && ctx.dev < 64 ? ctx.dev : 0;
+  int n = cached[slot].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  n = 8;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kNT);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int fit = 0;
+  if (cudaFuncSetAttribute(balance_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+      cudaOccupancyMaxActiveClusters(&fit, balance_cluster_kernel, &cfg) == cudaSuccess && fit > 0)
+    n = kCluster;
+  (void)cudaGetLastError();
+  cached[slot].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 }  // namespace
 
 int64_t balance_slot_bytes(int64_t T, int64_t n_seq) {
-  const int64_t chunks = T > 0 ? (T + kChunk - 1) / kChunk : 1;
+  const int64_t chunks = (T + kChunk - 1) / kChunk;
+  if (chunks <= 1) return 0;  // all in shared memory
   return (chunks + n_seq) * kSlot * 4 + chunks * 16 + 64;
 }
 
@@ -561,7 +616,11 @@ cudaError_t launch_balance(const moe_config_t& c, const float* logits, const int
   cudaError_t e;
   if (a.n_chunks == 1) {
     e = launch_pdl(balance_single_kernel, dim3(1), dim3(kNT), 0, s, no_extra_attr(), a);
-  } else if (a.n_chunks <= kCluster) {
+  } else if (a.n_chunks <= cluster_limit(ctx)) {
+    if (a.n_chunks > 8) {
+      e = cudaFuncSetAttribute(balance_cluster_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+    }
     cudaLaunchAttribute cl = {};
     cl.id = cudaLaunchAttributeClusterDimension;
     cl.val.clusterDim.x = (unsigned)a.n_chunks;
@@ -604,7 +663,8 @@ moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logits, cons
   if (cfg->T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
   if (bad16(logits) || bad16(topk_idx) || bad16(dlogits) || (reinterpret_cast<uintptr_t>(seq_offsets) & 3u))
     return MOE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < moe_balance_loss_workspace_size(cfg, n_seq)) return MOE_ERR_WORKSPACE;
+  const size_t need = moe_balance_loss_workspace_size(cfg, n_seq);
+  if (ws_bytes < need || (need > 0 && !ws)) return MOE_ERR_WORKSPACE;
   if (bad16(ws)) return MOE_ERR_INVALID_ARG;
   Ctx ctx;
   if ((st = current_ctx(ctx)) != MOE_OK) return st;

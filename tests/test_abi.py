@@ -317,11 +317,12 @@ def test_peer_entry_points_check_arguments_before_any_cuda_call():
 
 def test_balance_loss_arguments_checked_before_launch(moe):
     P = ctypes.c_void_p
-    c = _cfg(moe, T=64)
+    c = _cfg(moe, T=2000)
     p, odd = P(256), P(260)  # never dereferenced
     n = moe.balance_loss_workspace_size(c, 3)
     assert n > 0 and moe.balance_loss_workspace_size(c, 0) == 0
     assert moe.balance_loss_workspace_size(c, (1 << 24) + 1) == 0
+    assert moe.balance_loss_workspace_size(_cfg(moe, T=1024), 3) == 0  # needs none
     assert moe.balance_loss_workspace_size(_cfg(moe, E=4), 1) == 0
 
     def call(cfg=c, lg=p, idx=p, mask=None, seq=p, n_seq=3, a=0.1, b=0.1, counts=p, loss=p, dl=p, ws=p, size=n):
