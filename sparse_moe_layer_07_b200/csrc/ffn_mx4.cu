@@ -32,6 +32,9 @@
 // 2-5 epilogue, and warps 6-9 for the scales.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <math.h>
+
+#include <initializer_list>
 
 #include "common.cuh"
 #include "internal.h"
@@ -78,7 +81,8 @@ enum Mode { kGateUp = 0, kDownSum = 1, kDownParts = 2 };
 struct MxArgs {
   const int32_t* offsets;    // [E + 1]
   int64_t rows_alloc;
-  int n_tiles;               // gate/up: f / 128;  down: d / 256
+  int n_tiles;               // gate/up: f / 128;  down: d / bn
+  int bn;                    // columns of a tile: gate/up 128 (and 128 up), down 256, 192 or 128
   int num_kb;                // K / 128
   int splits;                // K splits (kDownParts; 1 otherwise)
   const uint8_t* a_scales;   // [row tiles][K / 128][512]
@@ -163,6 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const MxArgs args) {
   using R = Ring<BM>;
   constexpr int S = R::kStages;
+  // columns of a tile (a variable only where the width is chosen)
+  const int bn = MODE == kGateUp ? 128 : (MODE == kDownParts ? 256 : args.bn);
   constexpr int kGroup = R::kGroup, GROUP_BYTES = R::GROUP_BYTES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -229,9 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
         const Tile t = decode_tile<BM>(sched, args, L);
         const int boxes = t.rows > 96 ? 0 : (t.rows + 31) / 32;
-        const uint32_t bytes = (boxes ? (uint32_t)boxes * 32 * BK : R::A_BYTES) + B_TX;
-        const int n0 = t.nt * (MODE == kGateUp ? 128 : 256);
-        const int n1 = MODE == kGateUp ? n0 : n0 + 128;
+        // boxes of 128 channels; a tile of 192 columns takes three of 64 (64 for
+        // all made the down pass 17 to 24% slower)
+        const int box_n = bn % 128 == 0 ? 128 : 64;
+        const uint32_t bytes = (boxes ? (uint32_t)boxes * 32 * BK : R::A_BYTES) +
+                               (MODE == kGateUp ? B_TX : (uint32_t)bn * BK / 2);
+        const int n0 = t.nt * bn;
         for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
           const int s = it % S;
           const uint32_t ph = (it / S) & 1u;
@@ -242,8 +251,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&full[s], bytes);
           uint8_t* a = sA + s * R::A_BYTES;
           uint8_t* b = sB + s * B_BYTES;
-          tma_load_3d_hint(b, &tmB0, &full[s], kb * BK, n0, t.e, keep);
-          tma_load_3d_hint(b + B_HALF, MODE == kGateUp ? &tmB1 : &tmB0, &full[s], kb * BK, n1, t.e, keep);
+          if (MODE == kGateUp) {
+            tma_load_3d_hint(b, &tmB0, &full[s], kb * BK, n0, t.e, keep);
+            tma_load_3d_hint(b + B_HALF, &tmB1, &full[s], kb * BK, n0, t.e, keep);
+          } else {
+            tma_load_3d_hint(b, &tmB0, &full[s], kb * BK, n0, t.e, keep);
+            if (bn > box_n) tma_load_3d_hint(b + box_n * BK, &tmB0, &full[s], kb * BK, n0 + box_n, t.e, keep);
+            if (bn > 2 * box_n) tma_load_3d_hint(b + 2 * box_n * BK, &tmB0, &full[s], kb * BK, n0 + 2 * box_n, t.e, keep);
+          }
           if (boxes == 0) {
             tma_load_2d_hint(a, &tmA, &full[s], kb * BK, t.m0, keep);
           } else {
@@ -272,6 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_kb = __shfl_sync(0xffffffffu, t.kb1 - t.kb0, 0);
       // rows of a tile that starts inside a 128-row scale tile: 32 rows a column
       const uint32_t sf_skip = BM == 128 ? 0u : __shfl_sync(0xffffffffu, (uint32_t)t.in_mtile / 32u, 0);
+      // a tile of 192 columns may start in the middle of a 128-channel scale block
+      const uint32_t sfb_skip = MODE == kGateUp ? 0u : __shfl_sync(0xffffffffu, (uint32_t)(t.nt * bn % 128) / 32u, 0);
+      const uint32_t idesc = MODE == kGateUp ? idesc_mx_e4m3_e2m1(128, 256, 0) : idesc_mx_e4m3_e2m1(128, bn, 0);
       // the previous tile's epilogue has read the shared columns (and so has
       // finished the tile before, whose accumulator this one takes)
       if (tc > 0) ok = __all_sync(0xffffffffu, mbar_wait(tshared, (tc - 1) & 1u, abort_flag));
@@ -288,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t sfa = tmem_base + kScaleCol + set * 12;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)  // 32 bytes of K further each: 2 in the descriptors' 16-byte units
-          umma_mxf8f6f4_if(lead, d_tmem, ad + 2 * kk, bd + 2 * kk, idesc_mx_e4m3_e2m1(128, 256, kk), sfa + sf_skip,
-                           sfa + 4, (i > 0 || kk > 0) ? 1u : 0u);
+          umma_mxf8f6f4_if(lead, d_tmem, ad + 2 * kk, bd + 2 * kk, idesc | idesc_mx_scale_byte(kk), sfa + sf_skip,
+                           sfa + 4 + sfb_skip, (i > 0 || kk > 0) ? 1u : 0u);
         umma_commit_if(lead, &empty[s]);
       }
       if (ok) umma_commit_if(lead, &tfull[tc & 1u]);
@@ -332,11 +350,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = min(kGroup, lt.kb1 - lkb);
         const uint32_t bytes = (uint32_t)n * 512;
         const int64_t eb = (int64_t)lt.e * args.nb_scales;
-        const int64_t nb0 = eb + (MODE == kGateUp ? lt.nt : 2 * lt.nt);
+        const int64_t nb0 = eb + (MODE == kGateUp ? lt.nt : lt.nt * bn / 128);
+        // a down tile of 128 columns has one block of scales, taken twice
+        const int64_t second = MODE != kGateUp && bn > 128 ? (int64_t)args.num_kb * 512 : 0;
         const uint8_t* sa = args.a_scales + ((int64_t)lt.mtile * args.num_kb + lkb) * 512;
         const uint8_t* sb0 = args.b_scales0 + (nb0 * args.num_kb + lkb) * 512;
         const uint8_t* sb1 = MODE == kGateUp ? args.b_scales1 + (nb0 * args.num_kb + lkb) * 512
-                                             : sb0 + (int64_t)args.num_kb * 512;
+                                             : sb0 + second;
         uint8_t* g = sG + slot * GROUP_BYTES;
         mbar_arrive_expect_tx(&gfull[slot], 3 * bytes);
         bulk_load(g, sa, bytes, &gfull[slot], keep);
@@ -420,11 +440,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The shared columns first (the first accumulator's last 48, the second's
       // first 48: two chunks of 32), then the release: the next tile's MMAs wait
       // for nothing but these two loads.
+      const int last = bn / 32 - 1;
       uint32_t early[2][32];
       const uint32_t tshare = MODE == kGateUp ? tacc + (buf ? 0 : 128) : tacc;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int c = buf ? i : (MODE == kGateUp ? 3 : 7) - i;
+        const int c = buf ? i : last - i;
         tmem_ld32(tshare + c * 32, early[i]);
       }
       tmem_wait_ld();
@@ -481,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           drow = tok;
         }
         const float sc = (store && args.row_scale) ? __ldg(args.row_scale + row) : 1.0f;
-        float* dst = args.out + (store ? drow : 0) * args.ld + t.nt * 256;
+        float* dst = args.out + (store ? drow : 0) * args.ld + t.nt * bn;
         auto finish = [&](int c, const uint32_t (&v)[32]) {
           if (store) {
             float4* d4 = reinterpret_cast<float4*>(dst + c * 32);
@@ -497,10 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
 #pragma unroll
-        for (int i = 0; i < 2; ++i) finish(buf ? i : 7 - i, early[i]);
+        for (int i = 0; i < 2; ++i) finish(buf ? i : last - i, early[i]);
 #pragma unroll 1
-        for (int i = 2; i < 8; ++i) {
-          const int c = buf ? i : 7 - i;
+        for (int i = 2; i <= last; ++i) {
+          const int c = buf ? i : last - i;
           uint32_t v[32];
           tmem_ld32(tacc + c * 32, v);
           tmem_wait_ld();
@@ -609,11 +630,11 @@ bool map_rows8(CUtensorMap* m, const void* base, int64_t rows, int64_t K, uint32
   return encode_tmap_dtype(m, base, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
-// [E, N, K / 2] packed e2m1 codes, box of 128 codes x 128 channels, spread to 16 bytes per 16 codes.
-bool map_codes4(CUtensorMap* m, const void* base, int E, int64_t N, int64_t K) {
+// [E, N, K / 2] packed e2m1 codes, box of 128 codes x `channels`, spread to 16 bytes per 16 codes.
+bool map_codes4(CUtensorMap* m, const void* base, int E, int64_t N, int64_t K, uint32_t channels) {
   const uint64_t dims[3] = {(uint64_t)K, (uint64_t)N, (uint64_t)E};
   const uint64_t str[2] = {(uint64_t)K / 2, (uint64_t)N * K / 2};
-  const uint32_t box[3] = {BK, 128, 1};
+  const uint32_t box[3] = {BK, channels, 1};
   return encode_tmap_dtype(m, base, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B);
 }
@@ -626,6 +647,28 @@ MxArgs base_args(const moe_config_t& c, const int32_t* offsets, const Ctx& ctx) 
   a.n_tok = c.T;
   a.err = ctx.err;
   return a;
+}
+
+// Columns of a down tile where K is not split: the width whose waves of tiles
+// take least time, a wave costing its columns (an MMA's time goes with them)
+// and 32 more for what a K block costs beside.  With 6 x 36 tiles of 256 columns
+// (d 1536, T 2048, cf 1.25) the second wave is half empty; 8 x 36 of 192 fill it.
+int down_columns(const moe_config_t& c, int num_sms) {
+  int64_t rows = slot_rows(c);
+  const double kept = ceil(c.capacity_factor * (double)rows / c.E) * c.E;
+  if (kept < (double)rows) rows = (int64_t)kept;
+  const int64_t row_tiles = rows / 128 + c.E / 2;  // half of the experts' last tiles
+  int best = 256;
+  int64_t best_cost = 0;
+  for (const int bn : {256, 192, 128}) {
+    if (c.d % bn != 0) continue;
+    const int64_t waves = (c.d / bn * row_tiles + num_sms - 1) / num_sms, cost = waves * (bn + 32);
+    if (best_cost == 0 || cost < best_cost) {
+      best = bn;
+      best_cost = cost;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -660,10 +703,11 @@ cudaError_t launch_mx4_gate_up(const moe_config_t& c, const uint8_t* x8, const u
   if (rows == 0) return cudaSuccess;
   CUtensorMap ta, ta32, tg, tu;
   if (!map_rows8(&ta, x8, rows, c.d, 128) || !map_rows8(&ta32, x8, rows, c.d, 32) ||
-      !map_codes4(&tg, gate.codes, c.E, c.f, c.d) || !map_codes4(&tu, up.codes, c.E, c.f, c.d))
+      !map_codes4(&tg, gate.codes, c.E, c.f, c.d, 128) || !map_codes4(&tu, up.codes, c.E, c.f, c.d, 128))
     return cudaErrorInvalidValue;
   MxArgs a = base_args(c, offsets, ctx);
   a.n_tiles = (int)(c.f / 128);
+  a.bn = 128;
   a.num_kb = (int)(c.d / BK);
   a.a_scales = x_scales;
   a.b_scales0 = gate.scales;
@@ -681,11 +725,12 @@ cudaError_t launch_mx4_down(const moe_config_t& c, const uint8_t* h8, const uint
   const int64_t rows = slot_rows(c);
   if (rows == 0) return cudaSuccess;
   CUtensorMap ta, ta32, td;
-  if (!map_rows8(&ta, h8, rows, c.f, 128) || !map_rows8(&ta32, h8, rows, c.f, 32) ||
-      !map_codes4(&td, down.codes, c.E, c.d, c.f))
-    return cudaErrorInvalidValue;
   MxArgs a = base_args(c, offsets, ctx);
-  a.n_tiles = (int)(c.d / 256);
+  a.bn = perm ? down_columns(c, ctx.num_sms) : 256;
+  if (!map_rows8(&ta, h8, rows, c.f, 128) || !map_rows8(&ta32, h8, rows, c.f, 32) ||
+      !map_codes4(&td, down.codes, c.E, c.d, c.f, a.bn % 128 == 0 ? 128 : 64))
+    return cudaErrorInvalidValue;
+  a.n_tiles = (int)(c.d / a.bn);
   a.num_kb = (int)(c.f / BK);
   a.splits = splits;
   a.a_scales = h_scales;

@@ -99,9 +99,10 @@ __global__ void __launch_bounds__(256) dequantize_mx4_kernel(const uint8_t* __re
 
 // Grouped rows to e4m3: row r < offsets[8] of the codes is src row r, or
 // src[perm[r]] when perm is given.  A thread takes 8 values (16 bytes), four
-// neighbours one 32-block; work items of 256 columns over all rows, so that a
-// few rows still spread over the SMs.  The scale of row r goes to the 512-byte
-// block of its tile (row tiles of 128 start anew at each expert).
+// neighbours one 32-block, a warp 256 columns of a row at a time with four such
+// pieces in flight; blockIdx.y shares the columns out, so that a few rows still
+// spread over the SMs.  The scale of row r goes to the 512-byte block of its
+// tile (row tiles of 128 start anew at each expert).
 __global__ void __launch_bounds__(256) quantize_rows_mx8_kernel(const __nv_bfloat16* __restrict__ src,
                                                                const int32_t* __restrict__ perm, int64_t n_src,
                                                                const int32_t* __restrict__ offsets, int64_t max_rows,
@@ -111,13 +112,16 @@ __global__ void __launch_bounds__(256) quantize_rows_mx8_kernel(const __nv_bfloa
   pdl_wait();
   if (threadIdx.x == 0) {
     bool ok = true;
-    int tile = 0;
+    int tile = 0, prev = 0, v[9];
+#pragma unroll
+    for (int k = 0; k <= 8; ++k) v[k] = offsets[k];
+#pragma unroll
     for (int k = 0; k <= 8; ++k) {
-      const int v = offsets[k];
-      s_off[k] = v;
-      if (v < (k ? s_off[k - 1] : 0) || (int64_t)v > max_rows) ok = false;
-      if (k && ok) tile += (v - s_off[k - 1] + 127) / 128;
+      if (v[k] < prev || (int64_t)v[k] > max_rows) ok = false;
+      if (k && ok) tile += (v[k] - prev + 127) / 128;
+      s_off[k] = v[k];
       s_tile[k] = tile;
+      prev = v[k];
     }
     if (!ok) {
       s_off[8] = 0;
@@ -126,12 +130,11 @@ __global__ void __launch_bounds__(256) quantize_rows_mx8_kernel(const __nv_bfloa
   }
   __syncthreads();
   const int lane = threadIdx.x & 31;
-  const int per_row = (int)(K / 256);
-  const int64_t n_items = (int64_t)s_off[8] * per_row;
-  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < n_items; i += warps) {
-    const int64_t r = i / per_row;
-    const int c = (int)(i - r * per_row);
+  const int pieces = (int)(K / 256);
+  const int per = (pieces + (int)gridDim.y - 1) / (int)gridDim.y;
+  const int c_begin = (int)blockIdx.y * per, c_end = min(c_begin + per, pieces);
+  const int rows = s_off[8], warps = (int)gridDim.x * 8;
+  for (int r = (int)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
     int64_t sr = r;
     if (perm) {
       sr = __ldg(perm + r);
@@ -144,25 +147,44 @@ __global__ void __launch_bounds__(256) quantize_rows_mx8_kernel(const __nv_bfloa
 #pragma unroll
     for (int k = 1; k < 8; ++k)
       if (r >= s_off[k]) e = k;
-    float v[8];
-    load8(src + sr * K + c * 256 + lane * 8, v);
-    uint32_t m = 0;
+    const int in_expert = r - s_off[e];
+    const uint4* from = reinterpret_cast<const uint4*>(src + sr * K) + lane;
+    uint2* to = reinterpret_cast<uint2*>(codes + (int64_t)r * K) + lane;
+    uint8_t* sc = scales + (int64_t)(s_tile[e] + in_expert / 128) * (K / 128) * 512;
+    for (int c0 = c_begin; c0 < c_end; c0 += 4) {
+      uint4 q[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const int x = mx_exponent<8, kMxTopE4m3>(m);
-    const float inv = mx_inverse(x);
-    uint2 q = make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16,
-                         e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16);
-    const bool bad = m >= 0x7f800000u;
-    if (bad) q = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-    reinterpret_cast<uint2*>(codes + r * K + c * 256)[lane] = q;
-    if ((lane & 3) == 0) {
-      const int in_tile = (int)(r - s_off[e]) & 127;
-      const int64_t tile = s_tile[e] + (int)(r - s_off[e]) / 128;
-      const int kblock = c * 8 + (lane >> 2);
-      scales[(tile * (K / 128) + kblock / 4) * 512 + mx_scale_at(in_tile, kblock)] = bad ? 255 : (uint8_t)(x + 127);
+      for (int i = 0; i < 4; ++i)
+        if (c0 + i < c_end) q[i] = __ldg(from + (c0 + i) * 32);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + i;
+        if (c >= c_end) break;
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+        float v[8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] = __uint_as_float(w[k] << 16);
+          v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+          m = max(m, max(w[k] << 16 & 0x7fffffffu, w[k] & 0x7fff0000u));
+        }
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int x = mx_exponent<8, kMxTopE4m3>(m);
+        const float inv = mx_inverse(x);
+        uint2 o = make_uint2(e4m3x2(v[0] * inv, v[1] * inv) | e4m3x2(v[2] * inv, v[3] * inv) << 16,
+                             e4m3x2(v[4] * inv, v[5] * inv) | e4m3x2(v[6] * inv, v[7] * inv) << 16);
+        const bool bad = m >= 0x7f800000u;
+        if (bad) o = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+        to[c * 32] = o;
+        // the warp's 8 blocks are two words of four scales: lanes 0 and 16 write one each
+        uint32_t byte = bad ? 255u : (uint32_t)(x + 127);
+        byte |= __shfl_down_sync(0xffffffffu, byte, 4) << 8;
+        byte |= __shfl_down_sync(0xffffffffu, byte, 8) << 16;
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(sc + (c * 2 + lane / 16) * 512 + mx_scale_at(in_expert, 0)) = byte;
+      }
     }
   }
 }
@@ -187,9 +209,13 @@ cudaError_t launch_quantize_rows_mx8(const void* src, const int32_t* perm, int64
                                      int64_t max_rows, int64_t K, uint8_t* codes, uint8_t* scales, cudaStream_t s,
                                      const Ctx& ctx) {
   if (max_rows == 0) return cudaSuccess;
-  const int64_t want = (max_rows * (K / 256) + 7) / 8, cap = (int64_t)ctx.num_sms * 8;
+  const int64_t want = (max_rows + 7) / 8, cap = (int64_t)ctx.num_sms * 8;
+  const unsigned gx = (unsigned)(want < cap ? want : cap);
+  // columns in pieces of 256, shared out until there are two blocks an SM
+  int64_t gy = 1;
+  while (gy * 2 <= K / 256 && gx * gy < 2 * ctx.num_sms) gy *= 2;
   const cudaError_t e =
-      launch_pdl(quantize_rows_mx8_kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, s, no_extra_attr(),
+      launch_pdl(quantize_rows_mx8_kernel, dim3(gx, (unsigned)gy), dim3(256), 0, s, no_extra_attr(),
                  static_cast<const __nv_bfloat16*>(src), perm, n_src, offsets, max_rows, K, codes, scales, ctx.err);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -455,6 +455,9 @@ __host__ __device__ constexpr uint32_t idesc_mx_e4m3_e2m1(int M, int N, int sf) 
          | ((uint32_t)sf << 29);                    // A: scale byte
 }
 
+// The bits that choose scale byte `sf` on both sides.
+__host__ __device__ constexpr uint32_t idesc_mx_scale_byte(int sf) { return (uint32_t)sf << 4 | (uint32_t)sf << 29; }
+
 // Instruction descriptor, kind::f16 with bf16 A/B and fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_major, bool b_mn_major) {
   return (1u << 4)                                  // D format: f32

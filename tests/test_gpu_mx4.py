@@ -82,6 +82,9 @@ CASES = {
     "ragged": dict(T=700, d=512, f=384, capacity_factor=1.25),
     "full_tiles": dict(T=512, d=256, f=256, capacity_factor=4.0, logit_bias=(60.0, 50.0, 0, 0, 0, 0, 0, 0)),
     "wide": dict(T=300, d=1536, f=256, capacity_factor=4.0),
+    # the layer's down tiles have 128 columns up to here, then 192, then 256
+    "columns_192": dict(T=600, d=1536, f=256, capacity_factor=4.0),
+    "columns_256": dict(T=8192, d=256, f=128, capacity_factor=4.0),
     "long": dict(T=40, d=256, f=8192, capacity_factor=4.0),
 }
 
