@@ -10,6 +10,7 @@
 //   down    : Y[r, n] = row_scale[r] * sum_k h^ d^, 256 columns; added into the
 //             tokens' fp32 sums (two terms a token: the order does not matter),
 //             or stored as K-split partials where there are few rows.
+// Few rows (decode): the weights on the MMA's other side, see Ring.
 //
 // The weights stay 4 bits until the tensor core: TMA reads packed codes and
 // spreads 16 of them over 16 bytes of shared memory (8 bytes of padding), the
@@ -59,11 +60,15 @@ constexpr int kScaleSets = 4;
 static_assert(kScaleCol + 12 * kScaleSets <= kTmemCols, "TMEM columns");
 constexpr int kGroupSlots = 3;         // groups of scales in shared memory
 
-// BM rows a tile: 128, or 32 where few rows an expert are expected.  The MMA
-// takes 128 rows either way (it has no smaller block-scaled form); with 32 the
-// others are whatever lies behind in shared memory, and the room goes to a fifth
-// stage and to scales 16 K blocks ahead: there they come from DRAM, and with 4
-// blocks ahead the MMAs waited for them (gate/up of Grok-1 decode 338 us).
+// BM rows a tile: 128, or 32 where few rows an expert are expected.  The
+// block-scaled MMA takes 128 rows on its A side at least, so tiles of 32 put the
+// weights there (two MMAs of 128 channels x 32 rows for 256 channels) and the rows
+// on the B side: an MMA then costs its 4 KB of weights, and the accumulators are
+// 64 columns, lane = channel, column = row.  With the rows on the A side, padded
+// to 128, the tensor core was busy for 60% of the time and gate/up of Grok-1
+// decode took 307 us (259 with the MMAs' width cut).  The room of the rows goes to
+// a fifth stage and to scales 16 K blocks ahead: they come from DRAM here, and
+// with 4 blocks ahead the MMAs waited for them (338 us).
 template <int BM>
 struct Ring {
   static constexpr int kStages = BM == 128 ? 4 : 5;
@@ -73,7 +78,6 @@ struct Ring {
   static constexpr int kBars = 2 * kStages + 2 + 1 + kScaleSets + 2 * kGroupSlots + 1;
   static constexpr int SMEM_BYTES = 1024 + kStages * (A_BYTES + B_BYTES) + kGroupSlots * GROUP_BYTES + kBars * 8 + 16;
   static_assert(SMEM_BYTES + 256 <= 227 * 1024, "shared memory budget");
-  static_assert((kStages - 1) * A_BYTES + 128 * BK <= kStages * (A_BYTES + B_BYTES), "the MMA's A reads stay inside");
 };
 
 enum Mode { kGateUp = 0, kDownSum = 1, kDownParts = 2 };
@@ -285,11 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
       const Tile t = decode_tile<BM>(sched, args, L);
       const int n_kb = __shfl_sync(0xffffffffu, t.kb1 - t.kb0, 0);
-      // rows of a tile that starts inside a 128-row scale tile: 32 rows a column
-      const uint32_t sf_skip = BM == 128 ? 0u : __shfl_sync(0xffffffffu, (uint32_t)t.in_mtile / 32u, 0);
-      // a tile of 192 columns may start in the middle of a 128-channel scale block
-      const uint32_t sfb_skip = MODE == kGateUp ? 0u : __shfl_sync(0xffffffffu, (uint32_t)(t.nt * bn % 128) / 32u, 0);
-      const uint32_t idesc = MODE == kGateUp ? idesc_mx_e4m3_e2m1(128, 256, 0) : idesc_mx_e4m3_e2m1(128, bn, 0);
+      const uint32_t idesc = BM == 32 ? idesc_mx_e2m1_e4m3(128, 32)
+                                      : idesc_mx_e4m3_e2m1(128, MODE == kGateUp ? 256 : bn, 0);
       // the previous tile's epilogue has read the shared columns (and so has
       // finished the tile before, whose accumulator this one takes)
       if (tc > 0) ok = __all_sync(0xffffffffu, mbar_wait(tshared, (tc - 1) & 1u, abort_flag));
@@ -305,9 +306,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t bd = sw128_desc(smem_u32(sB + s * B_BYTES), 16, 1024);
         const uint32_t sfa = tmem_base + kScaleCol + set * 12;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 bytes of K further each: 2 in the descriptors' 16-byte units
-          umma_mxf8f6f4_if(lead, d_tmem, ad + 2 * kk, bd + 2 * kk, idesc | idesc_mx_scale_byte(kk), sfa + sf_skip,
-                           sfa + 4 + sfb_skip, (i > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of K further each: 2 in the descriptors' 16-byte units
+          const uint32_t id = idesc | idesc_mx_scale_byte(kk), acc = (i > 0 || kk > 0) ? 1u : 0u;
+          if (BM == 128) {
+            umma_mxf8f6f4_if(lead, d_tmem, ad + 2 * kk, bd + 2 * kk, id, sfa, sfa + 4, acc);
+          } else {
+            umma_mxf8f6f4_if(lead, d_tmem, bd + 2 * kk, ad + 2 * kk, id, sfa + 4, sfa, acc);
+            umma_mxf8f6f4_if(lead, d_tmem + 32, bd + 2 * kk + B_HALF / 16, ad + 2 * kk, id, sfa + 8, sfa, acc);
+          }
+        }
         umma_commit_if(lead, &empty[s]);
       }
       if (ok) umma_commit_if(lead, &tfull[tc & 1u]);
@@ -387,7 +394,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = min(kGroup, t.kb1 - kb);
         for (int j = 0; j < n; ++j, ++it) {
           const uint32_t set = it % kScaleSets;
-          const uint4 va = f[j * 32], vb = f[kGroup * 32 + j * 32], vc = f[2 * kGroup * 32 + j * 32];
+          uint4 va = f[j * 32], vb = f[kGroup * 32 + j * 32], vc = f[2 * kGroup * 32 + j * 32];
+          // A tile that starts inside a 128-row block of scales (32 rows, or channels,
+          // to a word): its first word goes to the first column, since the MMA takes
+          // scales from columns at multiples of 4 (another column faulted).
+          if (BM == 32) {
+            const uint32_t rows32 = t.in_mtile / 32;
+            va.x = rows32 == 0 ? va.x : (rows32 == 1 ? va.y : (rows32 == 2 ? va.z : va.w));
+          } else if (MODE == kDownSum && (t.nt * bn) % 128 != 0) {  // 192 columns from the middle of a block
+            vb.x = vb.z;
+            vb.y = vb.w;
+            vb.z = vc.x;
+            vb.w = vc.y;
+            vc.x = vc.z;
+            vc.y = vc.w;
+          }
           if (it >= (uint32_t)kScaleSets) {
             const uint32_t done = it - kScaleSets;
             ok = __all_sync(0xffffffffu, mbar_wait(&empty[done % S], (done / S) & 1u, abort_flag));
@@ -430,6 +451,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
+      if (BM == 32) {
+        // lane = channel, column = row
+        uint32_t v[2][32];
+        const uint32_t tacc = tmem_base + (buf ? kAccSecond : 0) + ((uint32_t)(q * 32) << 16);
+        tmem_ld32(tacc, v[0]);
+        tmem_ld32(tacc + 32, v[1]);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(tshared);
+        if (MODE == kGateUp) {
+          uint8_t* dst = args.h + (int64_t)t.m0 * args.ld + t.nt * 128 + r;
+          uint8_t* sc = args.h_scales + ((int64_t)t.mtile * (args.ld / 128) + t.nt) * 512;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= t.rows) break;
+            // the warp's 32 channels are the block
+            const float h = silu_mul_fast(__uint_as_float(v[0][j]), __uint_as_float(v[1][j]));
+            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
+            const int x = mx_exponent<8, kMxTopE4m3>(m);
+            const bool bad = m >= 0x7f800000u;
+            dst[j * args.ld] = bad ? 0x7f : (uint8_t)e4m3x2(h * mx_inverse(x), 0.f);
+            if (lane == 0) sc[mx_scale_at(t.in_mtile + j, q)] = bad ? 255 : (uint8_t)(x + 127);
+          }
+        } else {
+          const float mine = lane < t.rows && args.row_scale ? __ldg(args.row_scale + t.m0 + lane) : 1.0f;
+          float* dst = args.out + ((int64_t)t.split * args.rows_alloc + t.m0) * args.ld + t.nt * 256 + r;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= t.rows) break;
+            const float s1 = __shfl_sync(0xffffffffu, mine, j);
+            dst[j * args.ld] = s1 * __uint_as_float(v[0][j]);
+            dst[j * args.ld + 128] = s1 * __uint_as_float(v[1][j]);
+          }
+        }
+        continue;
+      }
       if (q * 32 >= t.rows) {  // a warp without rows reads nothing
         mbar_arrive(tshared);
         continue;

@@ -350,6 +350,16 @@ __device__ __forceinline__ void umma_mxf8f6f4_if(uint32_t lead, uint32_t d_tmem,
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(lead)
       : "memory");
 }
+__device__ __forceinline__ void umma_bf16_if(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
 __device__ __forceinline__ void umma_commit_if(uint32_t lead, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -453,6 +463,11 @@ __host__ __device__ constexpr uint32_t idesc_mx_e4m3_e2m1(int M, int N, int sf) 
          | (1u << 23)                               // scales: e8m0
          | ((uint32_t)(M >> 4) << 24)               // M / 16
          | ((uint32_t)sf << 29);                    // A: scale byte
+}
+
+// The same with e2m1 A and e4m3 B.
+__host__ __device__ constexpr uint32_t idesc_mx_e2m1_e4m3(int M, int N) {
+  return (5u << 7) | (0u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
 
 // The bits that choose scale byte `sf` on both sides.

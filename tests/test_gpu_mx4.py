@@ -76,6 +76,7 @@ CASES = {
     "one_token": dict(T=1, d=256, f=128, capacity_factor=4.0),
     "few": dict(T=7, d=512, f=384, capacity_factor=4.0),
     "decode": dict(T=32, d=256, f=1024, capacity_factor=4.0),
+    "decode_two": dict(T=60, d=256, f=256, capacity_factor=4.0, logit_bias=(60.0, 50.0, 0, 0, 0, 0, 0, 0)),
     "decode_skew": dict(T=200, d=256, f=256, capacity_factor=4.0, logit_bias=(60.0, 50.0, 0, 0, 0, 0, 0, 0)),
     "last_streaming": dict(T=256, d=256, f=640, capacity_factor=1.25),
     "first_tiled": dict(T=257, d=256, f=256, capacity_factor=4.0),
