@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
   if (warp == 0 && lane == 1) {
     prefetch_tmap(&tmA0);
     prefetch_tmap(&tmB0);
-    if (MODE == kDX) {
+    if (MODE == kDX || (MODE == kDH && C8)) {
       prefetch_tmap(&tmA1);
       prefetch_tmap(&tmB1);
     }
@@ -455,6 +455,29 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
         const int64_t base = row * args.ld + t.n0 + c_begin * 32;
         const uint32_t tmine = tacc + c_begin * 32;
         float dot = 0.f;
+        // The three results go out 32 rows x 32 columns at a time by TMA from shared
+        // memory (rows of 64 bytes, 64-byte swizzle), two buffers a warp: stored by
+        // the threads, each 16 bytes of its own row, they kept the load/store unit at
+        // 32 lines an instruction and the tile at 38K clocks.  A warp whose rows pass
+        // the expert's end stores its valid rows itself.
+        const bool whole = (q + 1) * 32 <= t.rows && t.rows > 64;
+        uint8_t* stage0 = sOut + (warp - 2) * (OUT_BYTES / Warps<MODE, C8>::kEpi);
+        int turn = 0;
+        auto put = [&](const CUtensorMap* map, const uint4 (&v)[4], int x) {
+          uint8_t* st = stage0 + (turn & 1) * 2048;
+          ++turn;
+          if (lane == 0) bulk_wait_group_read<1>();  // the store that last read this buffer is done with it
+          __syncwarp();
+          uint4* line = reinterpret_cast<uint4*>(st + lane * 64);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) line[j ^ ((lane >> 1) & 3)] = v[j];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(map, st, x, t.m0 + q * 32);
+            bulk_commit_group();
+          }
+        };
         // codes of a 32-column chunk: 2 x 16 bytes of G and of U, the next chunk's
         // loaded while this one is computed; the chunks' scales of each are one load
         uint4 qg[2], qu[2];
@@ -486,13 +509,13 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
           uint4 ng[2], nu[2];
           if (valid && more) load_chunk(c + 1, ng, nu);
           tmem_wait_ld();
+          uint4 kg[4], ku[4], kh[4];
           if (valid) {
             const uint32_t pg = sg4[c >> 1], pu = su4[c >> 1];
             const float sg = __uint_as_float((c & 1) ? pg & 0xffff0000u : pg << 16);
             const float su = __uint_as_float((c & 1) ? pu & 0xffff0000u : pu << 16);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
-              const int64_t o = base + c * 32 + p * 8;
               uint32_t og[4], ou[4], oh[4];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
@@ -522,9 +545,23 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
                 oh[2 * i] = pack_bf16x2(hw[0], hw[1]);
                 oh[2 * i + 1] = pack_bf16x2(hw[2], hw[3]);
               }
-              __stcs(reinterpret_cast<uint4*>(args.dG + o), make_uint4(og[0], og[1], og[2], og[3]));
-              __stcs(reinterpret_cast<uint4*>(args.dU + o), make_uint4(ou[0], ou[1], ou[2], ou[3]));
-              __stcs(reinterpret_cast<uint4*>(args.hw + o), make_uint4(oh[0], oh[1], oh[2], oh[3]));
+              kg[p] = make_uint4(og[0], og[1], og[2], og[3]);
+              ku[p] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+              kh[p] = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+            }
+          }
+          const int x = t.n0 + (c_begin + c) * 32;
+          if (whole) {
+            put(&tmA1, kg, x);
+            put(&tmB1, ku, x);
+            put(&tmOut, kh, x);
+          } else if (valid) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              const int64_t o = base + c * 32 + p * 8;
+              __stcs(reinterpret_cast<uint4*>(args.dG + o), kg[p]);
+              __stcs(reinterpret_cast<uint4*>(args.dU + o), ku[p]);
+              __stcs(reinterpret_cast<uint4*>(args.hw + o), kh[p]);
             }
           }
           if (more) {
@@ -694,7 +731,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
   }
 
   // tile stores still in flight must finish before the CTA (and its shared memory) goes
-  if (MODE == kWG && warp >= 2 && lane == 0) bulk_wait_group_all();
+  if ((MODE == kWG || (MODE == kDH && C8)) && warp >= 2 && lane == 0) bulk_wait_group_all();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -726,6 +763,14 @@ bool map_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, uint
   const uint64_t str[1] = {(uint64_t)cols * 2};
   const uint32_t box[2] = {64, box_rows};
   return encode_tmap(m, base, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// [rows, cols] bf16 results stored 32 x 32 at a time, rows of 64 bytes in shared memory
+bool map_out(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
+  const uint64_t dims[2] = {(uint64_t)cols, (uint64_t)rows};
+  const uint64_t str[1] = {(uint64_t)cols * 2};
+  const uint32_t box[2] = {32, 32};
+  return encode_tmap(m, base, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // [E, R, C] weights, box of 64 columns x 64 rows of one expert
@@ -769,8 +814,10 @@ cudaError_t launch_bwd_dh_c8(const moe_config_t& c, const void* dout_perm, const
                              cudaStream_t s, const Ctx& ctx) {
   const int64_t rows = slot_rows(c);
   if (rows == 0) return cudaSuccess;
-  CUtensorMap ta, tb;
-  if (!map_rows(&ta, dout_perm, rows, c.d, 128) || !map_weights(&tb, wd, c.E, c.f, c.d)) return cudaErrorInvalidValue;
+  CUtensorMap ta, tb, tg, tu, th;
+  if (!map_rows(&ta, dout_perm, rows, c.d, 128) || !map_weights(&tb, wd, c.E, c.f, c.d) || !map_out(&tg, dG, rows, c.f) ||
+      !map_out(&tu, dU, rows, c.f) || !map_out(&th, hw, rows, c.f))
+    return cudaErrorInvalidValue;
   BwdArgs a = base_args(c, offsets, ctx);
   a.n_tiles = (int)(c.f / BN);
   a.num_kb = (int)(c.d / BK);
@@ -781,8 +828,8 @@ cudaError_t launch_bwd_dh_c8(const moe_config_t& c, const void* dout_perm, const
   a.dU = static_cast<__nv_bfloat16*>(dU);
   a.dw_part = dw_part;
   a.ld = c.f;
-  if (bwd_dh_c8_parts_per_tile(c) == 2) return launch_bwd<kDH, 8>(ta, ta, tb, tb, ta, a, s, ctx);
-  return launch_bwd<kDH, 4>(ta, ta, tb, tb, ta, a, s, ctx);
+  if (bwd_dh_c8_parts_per_tile(c) == 2) return launch_bwd<kDH, 8>(ta, tg, tb, tu, th, a, s, ctx);
+  return launch_bwd<kDH, 4>(ta, tg, tb, tu, th, a, s, ctx);
 }
 
 cudaError_t launch_bwd_dx(const moe_config_t& c, const void* dG, const void* dU, const int32_t* offsets,
