@@ -438,6 +438,38 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
       const Tile t = decode_tile<MODE>(sched, args, L);
       const uint32_t buf = tc & 1u;
       const uint32_t tph = (tc >> 1) & 1u;
+      // tile row of this thread; M = 64 accumulators hold row 16 q + i in lane i (< 16) of quarter q
+      const int r = (MODE != kWG && t.rows <= 64) ? (lane < 16 ? q * 16 + lane : BM) : q * 32 + lane;
+      // kDH, C8: codes of a 32-column chunk, 2 x 16 bytes of G and of U.  The
+      // first chunk's and the scales do not wait for the products; the next
+      // chunk's are loaded while one is computed.
+      constexpr int NC = BN / 32 / kSplit;  // chunks of this warp
+      const bool valid = r < t.rows;
+      const int64_t row = t.m0 + r;
+      const int64_t base = row * args.ld + t.n0 + c_begin * 32;
+      float w = 0.f;
+      uint4 qg[2], qu[2];
+      uint32_t sg4[NC / 2] = {}, su4[NC / 2] = {};
+      auto load_chunk = [&](int c, uint4 (&a)[2], uint4 (&b)[2]) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          a[p] = __ldcs(reinterpret_cast<const uint4*>(args.codes.g + base + c * 32) + p);
+          b[p] = __ldcs(reinterpret_cast<const uint4*>(args.codes.u + base + c * 32) + p);
+        }
+      };
+      if (MODE == kDH && C8 && valid) {
+        w = __ldg(args.row_scale + row);
+#pragma unroll
+        for (int i = 0; i < NC / 4; ++i) {
+          const uint2 a = __ldg(reinterpret_cast<const uint2*>(args.codes.sg + base / 32) + i);
+          const uint2 b = __ldg(reinterpret_cast<const uint2*>(args.codes.su + base / 32) + i);
+          sg4[2 * i] = a.x;
+          sg4[2 * i + 1] = a.y;
+          su4[2 * i] = b.x;
+          su4[2 * i + 1] = b.y;
+        }
+        load_chunk(0, qg, qu);
+      }
       if (!mbar_wait(&tfull[buf], tph, abort_flag)) {
         if (lane == 0) flag_error(args.err, MOE_DEVERR_TIMEOUT);
         *abort_flag = 1;
@@ -445,14 +477,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
       }
       tc_fence_after();
       const uint32_t tacc = tmem_base + buf * kAccStride + ((uint32_t)(q * 32) << 16);
-      // tile row of this thread; M = 64 accumulators hold row 16 q + i in lane i (< 16) of quarter q
-      const int r = (MODE != kWG && t.rows <= 64) ? (lane < 16 ? q * 16 + lane : BM) : q * 32 + lane;
       if (MODE == kDH && C8) {
-        const bool valid = r < t.rows;
-        const int64_t row = t.m0 + r;
-        const float w = valid ? __ldg(args.row_scale + row) : 0.f;
-        constexpr int NC = BN / 32 / kSplit;  // chunks of this warp
-        const int64_t base = row * args.ld + t.n0 + c_begin * 32;
         const uint32_t tmine = tacc + c_begin * 32;
         float dot = 0.f;
         // The three results go out 32 rows x 32 columns at a time by TMA from shared
@@ -478,29 +503,6 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
             bulk_commit_group();
           }
         };
-        // codes of a 32-column chunk: 2 x 16 bytes of G and of U, the next chunk's
-        // loaded while this one is computed; the chunks' scales of each are one load
-        uint4 qg[2], qu[2];
-        uint32_t sg4[NC / 2] = {}, su4[NC / 2] = {};
-        auto load_chunk = [&](int c, uint4 (&a)[2], uint4 (&b)[2]) {
-#pragma unroll
-          for (int p = 0; p < 2; ++p) {
-            a[p] = __ldcs(reinterpret_cast<const uint4*>(args.codes.g + base + c * 32) + p);
-            b[p] = __ldcs(reinterpret_cast<const uint4*>(args.codes.u + base + c * 32) + p);
-          }
-        };
-        if (valid) {
-#pragma unroll
-          for (int i = 0; i < NC / 4; ++i) {
-            const uint2 a = __ldg(reinterpret_cast<const uint2*>(args.codes.sg + base / 32) + i);
-            const uint2 b = __ldg(reinterpret_cast<const uint2*>(args.codes.su + base / 32) + i);
-            sg4[2 * i] = a.x;
-            sg4[2 * i + 1] = a.y;
-            su4[2 * i] = b.x;
-            su4[2 * i + 1] = b.y;
-          }
-          load_chunk(0, qg, qu);
-        }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           uint32_t v[32];
