@@ -81,7 +81,8 @@ enum Mode { kDH = 0, kDX = 1, kWG = 2 };
 struct BwdArgs {
   const int32_t* offsets;  // [E + 1]
   int64_t rows_alloc;      // rows of the grouped buffers
-  int n_tiles;             // N / BN
+  int n_tiles;             // N / BN (kDX: d / bn)
+  int bn;                  // kDX: columns of a tile, 256 or 192
   int m_tiles;             // kWG: M / BM
   int num_kb;              // kDH: d / BK;  kDX: 2 f / BK
   int half_kb;             // kDX: f / BK (first half dG x W_gate, second dU x W_up)
@@ -145,7 +146,7 @@ __device__ __forceinline__ Tile decode_tile(const Sched& s, const BwdArgs& a, in
     t.m0 = s.offs[e] + mi * BM;
     const int left = s.offs[e + 1] - t.m0;
     t.rows = left < BM ? left : BM;
-    t.n0 = nb * BN;
+    t.n0 = nb * (MODE == kDX ? a.bn : BN);
     t.nb = nb;
     t.nkb = MODE == kDH ? a.num_kb : 2 * a.half_kb;
   }
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&full[s], STAGE);
+          mbar_arrive_expect_tx(&full[s], MODE == kDX ? A_BYTES + args.bn * BK * 2 : STAGE);
           uint8_t* a = sA + s * A_BYTES;
           uint8_t* b = sB + s * B_BYTES;
           if (MODE == kDH) {
@@ -278,7 +279,8 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
             tma_load_2d_hint(a, first ? &tmA0 : &tmA1, &full[s], k0, t.m0, keep);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              tma_load_3d_hint(b + c * CHUNK, first ? &tmB0 : &tmB1, &full[s], k0, t.n0 + 64 * c, t.e, keep);
+              if (64 * c < args.bn)
+                tma_load_3d_hint(b + c * CHUNK, first ? &tmB0 : &tmB1, &full[s], k0, t.n0 + 64 * c, t.e, keep);
           } else {
             const int r0 = t.row0 + kb * BK;
             tma_load_3d_hint(a, &tmA0, &full[s], 0, r0, t.m0 / 64, keep);
@@ -301,8 +303,9 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
     // 25-35% below the MMA rate.
     if (lane == 0) {
       constexpr bool kMN = MODE == kWG;
-      constexpr uint32_t IDESC = idesc_bf16_f32(BM, BN, kMN, kMN);
-      constexpr uint32_t IDESC_M64 = idesc_bf16_f32(64, BN, kMN, kMN);
+      const int bn = MODE == kDX ? args.bn : BN;
+      const uint32_t IDESC = idesc_bf16_f32(BM, bn, kMN, kMN);
+      const uint32_t IDESC_M64 = idesc_bf16_f32(64, bn, kMN, kMN);
       uint32_t it = 0, tc = 0, zphase = 0;  // zphase: parity bit per stage of `zeroed`
       bool ok = true, issued = false;
       for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
@@ -656,7 +659,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
         }
         float* dst = args.out + (int64_t)(tok < 0 ? 0 : tok) * args.ld + t.n0;
 #pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
+        for (int c = 0; c < args.bn / 32; ++c) {
           uint32_t v[32];
           tmem_ld32(tacc + c * 32, v);
           tmem_wait_ld();
@@ -845,7 +848,8 @@ cudaError_t launch_bwd_dx(const moe_config_t& c, const void* dG, const void* dU,
       !map_weights(&tb0, wg, c.E, c.d, c.f) || !map_weights(&tb1, wu, c.E, c.d, c.f))
     return cudaErrorInvalidValue;
   BwdArgs a = base_args(c, offsets, ctx);
-  a.n_tiles = (int)(c.d / BN);
+  a.bn = tile_columns(c, c.d, {256, 192}, ctx.num_sms);
+  a.n_tiles = (int)(c.d / a.bn);
   a.half_kb = (int)(c.f / BK);
   a.num_kb = 2 * a.half_kb;
   a.perm = perm;

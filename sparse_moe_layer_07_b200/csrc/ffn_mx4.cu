@@ -33,9 +33,6 @@
 // 2-5 epilogue, and warps 6-9 for the scales.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <math.h>
-
-#include <initializer_list>
 
 #include "common.cuh"
 #include "internal.h"
@@ -706,28 +703,6 @@ MxArgs base_args(const moe_config_t& c, const int32_t* offsets, const Ctx& ctx) 
   return a;
 }
 
-// Columns of a down tile where K is not split: the width whose waves of tiles
-// take least time, a wave costing its columns (an MMA's time goes with them)
-// and 32 more for what a K block costs beside.  With 6 x 36 tiles of 256 columns
-// (d 1536, T 2048, cf 1.25) the second wave is half empty; 8 x 36 of 192 fill it.
-int down_columns(const moe_config_t& c, int num_sms) {
-  int64_t rows = slot_rows(c);
-  const double kept = ceil(c.capacity_factor * (double)rows / c.E) * c.E;
-  if (kept < (double)rows) rows = (int64_t)kept;
-  const int64_t row_tiles = rows / 128 + c.E / 2;  // half of the experts' last tiles
-  int best = 256;
-  int64_t best_cost = 0;
-  for (const int bn : {256, 192, 128}) {
-    if (c.d % bn != 0) continue;
-    const int64_t waves = (c.d / bn * row_tiles + num_sms - 1) / num_sms, cost = waves * (bn + 32);
-    if (best_cost == 0 || cost < best_cost) {
-      best = bn;
-      best_cost = cost;
-    }
-  }
-  return best;
-}
-
 }  // namespace
 
 int64_t mx_row_tiles(const moe_config_t& c) { return slot_rows(c) / 128 + c.E; }
@@ -783,7 +758,7 @@ cudaError_t launch_mx4_down(const moe_config_t& c, const uint8_t* h8, const uint
   if (rows == 0) return cudaSuccess;
   CUtensorMap ta, ta32, td;
   MxArgs a = base_args(c, offsets, ctx);
-  a.bn = perm ? down_columns(c, ctx.num_sms) : 256;
+  a.bn = perm ? tile_columns(c, c.d, {256, 192, 128}, ctx.num_sms) : 256;
   if (!map_rows8(&ta, h8, rows, c.f, 128) || !map_rows8(&ta32, h8, rows, c.f, 32) ||
       !map_codes4(&td, down.codes, c.E, c.d, c.f, a.bn % 128 == 0 ? 128 : 64))
     return cudaErrorInvalidValue;

@@ -31,6 +31,7 @@
 // released before the CTA exits.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <math.h>
 
 #include <atomic>
 
@@ -59,7 +60,7 @@ struct Cfg {
   static constexpr int kChunks = MMA_N / 64;
   static constexpr int B_BYTES = kChunks * CHUNK_BYTES;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int kStages = MMA_N == 256 ? 4 : 6;
+  static constexpr int kStages = MMA_N == 256 ? 4 : (MMA_N == 192 ? 5 : 6);
   static constexpr int BN_OUT = MODE == kGateUp ? MMA_N / 2 : MMA_N;  // output columns per tile
   static constexpr int kBarBytes = 256;
   static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + kBarBytes;
@@ -769,6 +770,24 @@ std::atomic<int> g_tile_mode{MOE_TILES_AUTO};
 
 int set_tile_mode(int mode) { return g_tile_mode.exchange(mode); }
 
+int tile_columns(const moe_config_t& c, int64_t n, std::initializer_list<int> widths, int num_sms) {
+  int64_t rows = slot_rows(c);
+  const double kept = ceil(c.capacity_factor * (double)rows / c.E) * c.E;
+  if (kept < (double)rows) rows = (int64_t)kept;
+  const int64_t row_tiles = rows / BM + c.E / 2;  // half of the experts' last tiles
+  int best = *widths.begin();
+  int64_t best_cost = 0;
+  for (const int w : widths) {
+    if (n % w != 0) continue;
+    const int64_t waves = (n / w * row_tiles + num_sms - 1) / num_sms, cost = waves * (w + 32);
+    if (best_cost == 0 || cost < best_cost) {
+      best = w;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
 // Automatic choice: single-CTA tiles.  Timed back to back in one process on a
 // power-capped B200, the pair kernels were 7% slower than the single-CTA ones
 // at the Grok-1 prefill shape (T 8192, d 6144, f 32768: gate/up 11.83 vs 11.03
@@ -885,7 +904,10 @@ cudaError_t launch_tc_down_scatter(const moe_config_t& c, const void* h, const i
   args.save_g = nullptr;
   args.save_u = nullptr;
   args.err = ctx.err;
-  args.n_tiles = (int)(c.d / 256);
+  // 192 columns where they fill the waves better (the same sums: an element's K
+  // order does not depend on its tile)
+  const bool narrow = !use_pair_tiles(c) && n_peers == 0 && tile_columns(c, c.d, {256, 192}, ctx.num_sms) == 192;
+  args.n_tiles = (int)(c.d / (narrow ? 192 : 256));
   if (n_peers > 0) {
     if (n_peers > MOE_EP_MAX_WORLD || !peer_out || peer_tokens <= 0) return cudaErrorInvalidValue;
     args.n_peers = n_peers;
@@ -893,6 +915,7 @@ cudaError_t launch_tc_down_scatter(const moe_config_t& c, const void* h, const i
     for (int p = 0; p < n_peers; ++p) args.peer_out[p] = peer_out[p];
   }
   if (use_pair_tiles(c)) return launch_pair<kDown, true>(ta, tw, tw, args, s, ctx);
+  if (narrow) return launch_grouped<kDown, 192, true>(ta, tw, tw, args, s, ctx);
   return launch_grouped<kDown, 256, true>(ta, tw, tw, args, s, ctx);
 }
 

@@ -7,6 +7,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <initializer_list>
 #include <utility>
 
 #include "moe.h"
@@ -143,6 +144,12 @@ cudaError_t launch_tc_down(const moe_config_t& c, const void* h, const int32_t* 
 // or CTA pairs (2-SM MMAs) per 256-row tile.  set_tile_mode returns the previous mode.
 int set_tile_mode(int mode);
 bool use_pair_tiles(const moe_config_t& c);
+
+// Columns of an N tile, of `widths` (those that divide n), by the time that the
+// waves of tiles take: a wave costs its columns (an MMA's time goes with them) and
+// 32 more for what a K block costs beside.  With 6 x 36 tiles of 256 columns (d
+// 1536, T 2048, cf 1.25) the second wave is half empty, and 8 x 36 of 192 fill it.
+int tile_columns(const moe_config_t& c, int64_t n, std::initializer_list<int> widths, int num_sms);
 
 // Down with the combine fused: adds row_scale * (H W_down) into a zeroed fp32
 // out32 [T, d] by token (perm) instead of writing Y.  With n_peers > 0 the
