@@ -69,15 +69,11 @@ __global__ void __launch_bounds__(256) bwd_gather_kernel(const uint4* __restrict
 // gradients, lanes 0-7 write the token's dlogits row, and the warp streams
 // dx[t] = round(dx32[t] + dl_0 W_r[i_0] + dl_1 W_r[i_1]) (slot 0 first), four
 // columns per lane and 16-byte vector, four vectors in flight per lane.
-// kAux: dl_aux (the gradient of a loss on the logits themselves, over all
-// experts) is added to the token's dlogits, and dx takes all eight rows of W_r
-// (in expert order): W_r comes from L1, eight loads where two were.
-template <bool kAux>
 __global__ void __launch_bounds__(256) router_bwd_token_kernel(
     const float* __restrict__ dw_part, int n_parts, const int32_t* __restrict__ slot_of,
     const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w, const __nv_bfloat16* __restrict__ wr,
     const float* __restrict__ dx32, int64_t T, int64_t d, int64_t max_slot, float* __restrict__ dlogits,
-    float* __restrict__ dweight, __nv_bfloat16* __restrict__ dx, const float* __restrict__ dl_aux, int* err) {
+    float* __restrict__ dweight, __nv_bfloat16* __restrict__ dx, int* err) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int nq = (int)(d / 4);  // 4-column groups of a row (d is a multiple of 128)
@@ -107,37 +103,11 @@ __global__ void __launch_bounds__(256) router_bwd_token_kernel(
     const float mean = w0 * dw0 + w1 * dw1;
     const float dl0 = w0 * (dw0 - mean);
     const float dl1 = w1 * (dw1 - mean);
-    float dl = 0.f;  // lane e < 8: the gradient of logit e
     if (lane < kE) {
-      if (e0 == lane) dl += dl0;
-      if (e1 == lane) dl += dl1;
-      if (kAux) dl += __ldg(dl_aux + t * kE + lane);
-      dlogits[t * kE + lane] = dl;
-    }
-    if (kAux) {
-      float g[kE];
-#pragma unroll
-      for (int k = 0; k < kE; ++k) g[k] = __shfl_sync(0xffffffffu, dl, k);
-      const float4* a4 = reinterpret_cast<const float4*>(dx32 + t * d);
-      uint2* o2 = reinterpret_cast<uint2*>(dx + t * d);
-      for (int i = lane; i < nq; i += 32) {
-        const float4 a = __ldcs(a4 + i);
-        uint2 r[kE];
-#pragma unroll
-        for (int k = 0; k < kE; ++k) r[k] = __ldg(reinterpret_cast<const uint2*>(wr + (int64_t)k * d) + i);
-        float v0 = a.x, v1 = a.y, v2 = a.z, v3 = a.w;
-#pragma unroll
-        for (int k = 0; k < kE; ++k) {
-          const float2 p = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[k].x));
-          const float2 q = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r[k].y));
-          v0 = fmaf(g[k], p.x, v0);
-          v1 = fmaf(g[k], p.y, v1);
-          v2 = fmaf(g[k], q.x, v2);
-          v3 = fmaf(g[k], q.y, v3);
-        }
-        o2[i] = make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
-      }
-      continue;
+      float v = 0.f;
+      if (e0 == lane) v += dl0;
+      if (e1 == lane) v += dl1;
+      dlogits[t * kE + lane] = v;
     }
     const float4* a4 = reinterpret_cast<const float4*>(dx32 + t * d);
     const uint2* p2 = reinterpret_cast<const uint2*>(wr + (int64_t)e0 * d);
@@ -172,6 +142,93 @@ __global__ void __launch_bounds__(256) router_bwd_token_kernel(
           o2[g] = make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
         }
       }
+    }
+  }
+}
+
+// The same where a loss on the logits themselves adds its gradient dl_aux over
+// all experts: dx takes all eight rows of W_r (in expert order).  One warp per
+// two tokens, which share the loads of W_r (from L1); eight lanes add up the
+// partials of each of the four routing-weight gradients (in a fixed order).
+__global__ void __launch_bounds__(64) router_bwd_token_aux_kernel(
+    const float* __restrict__ dw_part, int n_parts, const int32_t* __restrict__ slot_of,
+    const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w, const __nv_bfloat16* __restrict__ wr,
+    const float* __restrict__ dx32, int64_t T, int64_t d, int64_t max_slot, float* __restrict__ dlogits,
+    float* __restrict__ dweight, __nv_bfloat16* __restrict__ dx, const float* __restrict__ dl_aux, int* err) {
+  const int lane = threadIdx.x & 31, group = lane >> 3, part = lane & 7;
+  const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  const int nq = (int)(d / 4);
+  for (int64_t t0 = 2 * ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)); t0 < T; t0 += 2 * warps) {
+    // group 2 k + j: choice j of token t0 + k
+    const int64_t a = 2 * t0 + group;
+    const bool have = a < 2 * T;
+    int e = 0;
+    float w = 0.f, dw = 0.f;
+    if (have) {
+      int sl = slot_of[a];
+      e = topk_idx[a];
+      w = topk_w[a];
+      if (sl >= max_slot || sl < -1) {
+        flag_error(err, MOE_DEVERR_SLOT_INDEX);
+        sl = -1;
+      }
+      if (e < 0 || e >= kE) {
+        flag_error(err, MOE_DEVERR_EXPERT_INDEX);
+        e = 0;
+        w = 0.f;
+      }
+      if (sl >= 0) {
+#pragma unroll 4
+        for (int p = part; p < n_parts; p += 8) dw += __ldg(dw_part + (int64_t)sl * n_parts + p);
+      }
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) dw += __shfl_xor_sync(0xffffffffu, dw, o);
+    if (have && part == 0) dweight[a] = dw;
+    const float w2 = __shfl_xor_sync(0xffffffffu, w, 8), dw2 = __shfl_xor_sync(0xffffffffu, dw, 8);
+    const bool first = (group & 1) == 0;  // the mean in the order of the choices, on both sides
+    const float mean = first ? w * dw + w2 * dw2 : w2 * dw2 + w * dw;
+    const float dl_mine = w * (dw - mean);
+    // lane e of a token's first eight: the gradient of logit e
+    float dl = 0.f;
+    const int src = lane & 16;  // first lane of this token's groups
+    const int i0 = __shfl_sync(0xffffffffu, e, src), i1 = __shfl_sync(0xffffffffu, e, src + 8);
+    const float d0 = __shfl_sync(0xffffffffu, dl_mine, src), d1 = __shfl_sync(0xffffffffu, dl_mine, src + 8);
+    const int64_t t = t0 + (lane >> 4);
+    if (t < T && (lane & 15) < kE) {
+      if (i0 == part) dl += d0;
+      if (i1 == part) dl += d1;
+      dl += __ldg(dl_aux + t * kE + part);
+      dlogits[t * kE + part] = dl;
+    }
+    float g[2][kE];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int q = 0; q < kE; ++q) g[k][q] = __shfl_sync(0xffffffffu, dl, 16 * k + q);
+    const bool two = t0 + 1 < T;
+    const float4* a4 = reinterpret_cast<const float4*>(dx32 + t0 * d);
+    uint2* o2 = reinterpret_cast<uint2*>(dx + t0 * d);
+#pragma unroll 2
+    for (int i = lane; i < nq; i += 32) {
+      float4 v[2];
+      v[0] = __ldcs(a4 + i);
+      v[1] = two ? __ldcs(a4 + nq + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < kE; ++q) {
+        const uint2 r = __ldg(reinterpret_cast<const uint2*>(wr + (int64_t)q * d) + i);
+        const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
+        const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          v[k].x = fmaf(g[k][q], lo.x, v[k].x);
+          v[k].y = fmaf(g[k][q], lo.y, v[k].y);
+          v[k].z = fmaf(g[k][q], hi.x, v[k].z);
+          v[k].w = fmaf(g[k][q], hi.y, v[k].w);
+        }
+      }
+      o2[i] = make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[0].z, v[0].w));
+      if (two) o2[nq + i] = make_uint2(pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[1].z, v[1].w));
     }
   }
 }
@@ -297,10 +354,14 @@ cudaError_t launch_router_bwd(const moe_config_t& c, const float* dw_part, int n
                               void* dbias, float* wr_part, cudaStream_t s, const Ctx& ctx, const float* dl_aux,
                               bool bf16_out) {
   if (c.T == 0) return cudaSuccess;
-  auto token_kernel = dl_aux ? router_bwd_token_kernel<true> : router_bwd_token_kernel<false>;
-  token_kernel<<<capped((c.T + 7) / 8, ctx), 256, 0, s>>>(
-      dw_part, n_parts, slot_of, topk_idx, topk_w, static_cast<const __nv_bfloat16*>(w_router), dx32, c.T, c.d,
-      slot_rows(c), dlogits, dweight, static_cast<__nv_bfloat16*>(dx), dl_aux, ctx.err);
+  if (dl_aux)
+    router_bwd_token_aux_kernel<<<capped((c.T + 3) / 4, ctx, 32), 64, 0, s>>>(  // two warps: more blocks to spread
+        dw_part, n_parts, slot_of, topk_idx, topk_w, static_cast<const __nv_bfloat16*>(w_router), dx32, c.T, c.d,
+        slot_rows(c), dlogits, dweight, static_cast<__nv_bfloat16*>(dx), dl_aux, ctx.err);
+  else
+    router_bwd_token_kernel<<<capped((c.T + 7) / 8, ctx), 256, 0, s>>>(
+        dw_part, n_parts, slot_of, topk_idx, topk_w, static_cast<const __nv_bfloat16*>(w_router), dx32, c.T, c.d,
+        slot_rows(c), dlogits, dweight, static_cast<__nv_bfloat16*>(dx), ctx.err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   dim3 grid((unsigned)((c.d / 8 + 255) / 256), (unsigned)kRouterBwdChunks);

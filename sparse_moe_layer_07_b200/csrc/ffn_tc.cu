@@ -64,6 +64,9 @@ struct Cfg {
   static constexpr int BN_OUT = MODE == kGateUp ? MMA_N / 2 : MMA_N;  // output columns per tile
   static constexpr int kBarBytes = 256;
   static constexpr int SMEM_BYTES = 1024 + kStages * STAGE_BYTES + kBarBytes;
+  // gate/up with 8-bit checkpoints: per epilogue warp, two buffers of 32 rows x 32
+  // columns of H (2 KB) and of the codes of G and U (1 KB each)
+  static constexpr int kOutBytes = 4 * 2 * 4096;
   static constexpr uint32_t IDESC = idesc_bf16_f32(BM, MMA_N, false, true);
   // an expert's last row block with at most 64 rows runs M = 64 MMAs (half the
   // work; measured, an M = 64 MMA takes as many clocks as an M = 128 one)
@@ -163,11 +166,16 @@ __device__ __forceinline__ int source_token(const TcArgs& args, int row, int n_r
 // not stored.  n_rows = kept rows.
 // kCodes (gate/up, tiles of 128 columns): the pre-activations are also kept as
 // 8-bit codes.  A thread holds 32 columns of one row at a time, which is a
-// block's worth, so amax needs no exchange between threads; the codes cost two
-// 16-byte stores a chunk and matrix where bf16 copies cost four.
+// block's worth, so amax needs no exchange between threads.  A warp whose 32 rows
+// are all valid (`whole`) puts H and the codes into `stage` and stores them by
+// TMA: the threads' own stores, each 16 bytes of its row, touch 32 lines an
+// instruction, and with three matrices to write they held the kernel back (187
+// against 175 us at T 2048, d 1536, f 8192; 10.1 against 9.3 ms at Grok size).
 template <int MODE, bool kScatter, bool kCodes = false>
 __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, int row0, int r, bool valid, int n0,
-                                              int n_cols, int u_off, uint32_t tacc) {
+                                              int n_cols, int u_off, uint32_t tacc, bool whole = false,
+                                              uint8_t* stage = nullptr, const CUtensorMap* tmH = nullptr,
+                                              const CUtensorMap* tmG = nullptr, const CUtensorMap* tmU = nullptr) {
   if (MODE == kGateUp) {
     __nv_bfloat16* H = static_cast<__nv_bfloat16*>(args.out);
     __nv_bfloat16* dst_row = H + (int64_t)(row0 + r) * args.ld_out + n0;
@@ -196,7 +204,39 @@ __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, in
       for (int i = 0; i < 16; ++i)
         p[i] = pack_bf16x2(silu_mul_fast(__uint_as_float(g[2 * i]), __uint_as_float(u[2 * i])),
                            silu_mul_fast(__uint_as_float(g[2 * i + 1]), __uint_as_float(u[2 * i + 1])));
-      if (valid) {
+      if (kCodes && whole) {
+        const int lane = threadIdx.x & 31;
+        uint8_t* st = stage + (c & 1) * 4096;
+        uint32_t cg[8], cu[8];
+        scales_g[c >> 1] |= (uint32_t)code32(g, cg) << (16 * (c & 1));
+        scales_u[c >> 1] |= (uint32_t)code32(u, cu) << (16 * (c & 1));
+        if (lane == 0) bulk_wait_group_read<1>();  // the stores that last read this buffer are done with it
+        __syncwarp();
+        uint4* hl = reinterpret_cast<uint4*>(st + lane * 64);  // 64-byte swizzle
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hl[i ^ ((lane >> 1) & 3)] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
+        uint4* gl = reinterpret_cast<uint4*>(st + 2048 + lane * 32);
+        uint4* ul = reinterpret_cast<uint4*>(st + 3072 + lane * 32);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          gl[i] = make_uint4(cg[4 * i], cg[4 * i + 1], cg[4 * i + 2], cg[4 * i + 3]);
+          ul[i] = make_uint4(cu[4 * i], cu[4 * i + 1], cu[4 * i + 2], cu[4 * i + 3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const int y = row0 + r;  // lane 0 holds the warp's first row
+          tma_store_2d(tmH, st, n0 + c * 32, y);
+          tma_store_2d(tmG, st + 2048, n0 + c * 32, y);
+          tma_store_2d(tmU, st + 3072, n0 + c * 32, y);
+          bulk_commit_group();
+        }
+        if (c == 3) {
+          const int64_t so = ((int64_t)(row0 + r) * args.ld_out + n0) / 32;
+          *reinterpret_cast<uint2*>(args.scale_g + so) = make_uint2(scales_g[0], scales_g[1]);
+          *reinterpret_cast<uint2*>(args.scale_u + so) = make_uint2(scales_u[0], scales_u[1]);
+        }
+      } else if (valid) {
         // streaming stores: H is read back by the next launch, not by this one, so
         // its lines should not push the operand tiles out of L2 (1-2% faster)
         uint4* d4 = reinterpret_cast<uint4*>(dst_row + c * 32);
@@ -293,7 +333,9 @@ __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, in
 template <int MODE, int MMA_N, bool FUSED>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                           const __grid_constant__ CUtensorMap tmB1, const TcArgs args) {
+                           const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmH,
+                           const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,
+                           const TcArgs args) {
   using C = Cfg<MODE, MMA_N>;
   constexpr bool kScatter = FUSED && MODE == kDown;
   constexpr bool kCodes = FUSED && MODE == kGateUp;
@@ -303,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   uint8_t* sA = smem;
   uint8_t* sB = smem + S * A_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * C::STAGE_BYTES);
+  uint8_t* sOut = smem + S * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sOut + (kCodes ? C::kOutBytes : 0));
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
   uint64_t* tempty = tfull + 2;
@@ -450,12 +493,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = t.rows <= 64 ? (lane < 16 ? q * 16 + lane : BM) : q * 32 + lane;
       const bool valid = r < t.rows;
       const uint32_t tacc = tmem_base + buf * kAccStride + ((uint32_t)(q * 32) << 16);
-      epilogue_rows<MODE, kScatter, kCodes>(args, sched.offs[kE], t.m0, r, valid, t.n0, C::BN_OUT, C::BN_OUT, tacc);
+      epilogue_rows<MODE, kScatter, kCodes>(args, sched.offs[kE], t.m0, r, valid, t.n0, C::BN_OUT, C::BN_OUT, tacc,
+                                            t.rows > 64 && (q + 1) * 32 <= t.rows, sOut + (warp - 2) * 8192, &tmH,
+                                            &tmG, &tmU);
       tc_fence_before();
       mbar_arrive(&tempty[buf]);
     }
   }
 
+  // tile stores still in flight must finish before the CTA's shared memory goes
+  if (kCodes && warp >= 2 && lane == 0) bulk_wait_group_all();
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -751,14 +798,18 @@ cudaError_t launch_pair(const CUtensorMap& a, const CUtensorMap& b0, const CUten
   return cudaGetLastError();
 }
 
+// maps: H and the codes of G and U (gate/up with 8-bit checkpoints).
 template <int MODE, int MMA_N, bool FUSED = false>
 cudaError_t launch_grouped(const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1, const TcArgs& args,
-                           cudaStream_t s, const Ctx& ctx) {
+                           cudaStream_t s, const Ctx& ctx, const CUtensorMap* maps = nullptr) {
   using C = Cfg<MODE, MMA_N>;
   auto kern = grouped_gemm_tc_kernel<MODE, MMA_N, FUSED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  constexpr int smem = C::SMEM_BYTES + (FUSED && MODE == kGateUp ? C::kOutBytes : 0);
+  static_assert(smem + 256 <= 227 * 1024, "shared memory budget");
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3(ctx.num_sms), dim3(kThreads), C::SMEM_BYTES, s, no_extra_attr(), a, b0, b1, args);
+  e = launch_pdl(kern, dim3(ctx.num_sms), dim3(kThreads), smem, s, no_extra_attr(), a, b0, b1, maps ? maps[0] : a,
+                 maps ? maps[1] : a, maps ? maps[2] : a, args);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -835,7 +886,17 @@ cudaError_t launch_tc_gate_up(const moe_config_t& c, const void* x_perm, const i
     args.code_u = codes->u;
     args.scale_g = codes->sg;
     args.scale_u = codes->su;
-    return launch_grouped<kGateUp, 256, true>(ta, tg, tu, args, s, ctx);
+    CUtensorMap out[3];
+    const uint64_t o_dims[2] = {(uint64_t)c.f, (uint64_t)rows};
+    const uint64_t h_str[1] = {(uint64_t)c.f * 2}, c_str[1] = {(uint64_t)c.f};
+    const uint32_t o_box[2] = {32, 32};
+    if (!encode_tmap(&out[0], h, 2, o_dims, h_str, o_box, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_tmap_dtype(&out[1], codes->g, 2, o_dims, c_str, o_box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_DATA_TYPE_UINT8) ||
+        !encode_tmap_dtype(&out[2], codes->u, 2, o_dims, c_str, o_box, CU_TENSOR_MAP_SWIZZLE_NONE,
+                           CU_TENSOR_MAP_DATA_TYPE_UINT8))
+      return cudaErrorInvalidValue;
+    return launch_grouped<kGateUp, 256, true>(ta, tg, tu, args, s, ctx, out);
   }
   if (use_pair_tiles(c)) return launch_pair<kGateUp, false>(ta, tg, tu, args, s, ctx);
   return launch_grouped<kGateUp, 256>(ta, tg, tu, args, s, ctx);
