@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(256) router_bwd_token_kernel(
 // all experts: dx takes all eight rows of W_r (in expert order).  One warp per
 // two tokens, which share the loads of W_r (from L1); eight lanes add up the
 // partials of each of the four routing-weight gradients (in a fixed order).
-__global__ void __launch_bounds__(64) router_bwd_token_aux_kernel(
+__global__ void __launch_bounds__(256) router_bwd_token_aux_kernel(
     const float* __restrict__ dw_part, int n_parts, const int32_t* __restrict__ slot_of,
     const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w, const __nv_bfloat16* __restrict__ wr,
     const float* __restrict__ dx32, int64_t T, int64_t d, int64_t max_slot, float* __restrict__ dlogits,
@@ -355,7 +355,7 @@ cudaError_t launch_router_bwd(const moe_config_t& c, const float* dw_part, int n
                               bool bf16_out) {
   if (c.T == 0) return cudaSuccess;
   if (dl_aux)
-    router_bwd_token_aux_kernel<<<capped((c.T + 3) / 4, ctx, 32), 64, 0, s>>>(  // two warps: more blocks to spread
+    router_bwd_token_aux_kernel<<<capped((c.T + 15) / 16, ctx), 256, 0, s>>>(
         dw_part, n_parts, slot_of, topk_idx, topk_w, static_cast<const __nv_bfloat16*>(w_router), dx32, c.T, c.d,
         slot_rows(c), dlogits, dweight, static_cast<__nv_bfloat16*>(dx), dl_aux, ctx.err);
   else
