@@ -11,6 +11,7 @@ this package fails if the library has not been built
 """
 from __future__ import annotations
 
+import collections.abc
 import contextlib
 import ctypes
 import math
@@ -598,24 +599,31 @@ def layer_backward(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ws, gra
     return g
 
 
-def _carve(buf, spec):
-    """Views (name, dtype, 1-D or 2-D or 3-D shape) of consecutive 256-byte aligned parts of a buffer."""
-    flat = buf.view(torch.uint8).view(-1)
-    if flat.numel() % 256:
-        flat = flat[:flat.numel() // 256 * 256]
-    typed, views, o = {}, {}, 0
-    for name, dt, shape in spec:
-        if dt not in typed:
-            typed[dt] = flat.view(dt)
-        strides = [1]
-        for n in shape[:0:-1]:
-            strides.insert(0, strides[0] * n)
-        nbytes = math.prod(shape) * dt.itemsize
-        if o + nbytes > flat.numel():
-            raise ValueError(f"the buffer of {flat.numel()} bytes ends inside {name}")
-        views[name] = typed[dt].as_strided(shape, strides, typed[dt].storage_offset() + o // dt.itemsize)
-        o += _round256(nbytes)
-    return views
+class _Views(collections.abc.Mapping):
+    """Named views of consecutive 256-byte aligned parts (name, dtype, shape) of a buffer, made when asked for."""
+
+    def __init__(self, buf, spec):
+        self._flat = buf.view(torch.uint8).view(-1)
+        self._at, self._made, o = {}, {}, 0
+        for name, dt, shape in spec:
+            nbytes = math.prod(shape) * dt.itemsize
+            self._at[name] = (o, nbytes, dt, shape)
+            o += _round256(nbytes)
+        if o > self._flat.numel():
+            raise ValueError(f"the buffer holds {self._flat.numel()} bytes, its parts take {o}")
+
+    def __getitem__(self, name):
+        v = self._made.get(name)
+        if v is None:
+            o, nbytes, dt, shape = self._at[name]
+            v = self._made[name] = self._flat[o:o + nbytes].view(dt).view(shape)
+        return v
+
+    def __iter__(self):
+        return iter(self._at)
+
+    def __len__(self):
+        return len(self._at)
 
 
 def checkpoint_size_c8(cfg: Config) -> int:
@@ -628,17 +636,15 @@ def workspace_size_train_c8(cfg: Config) -> int:
 
 def checkpoint_views_c8(cfg: Config, ckpt):
     """Named views into a checkpoint of layer_forward_train_c8 (layout stated in include/moe.h): the routing
-    (topk_idx and logits are what balance_loss takes) and the 8-bit codes with their scales."""
+    (topk_idx and logits are what balance_loss takes; route holds counts_raw [E], counts_kept [E] and offsets
+    [E + 1]) and the 8-bit codes with their scales."""
     T, E, f, rows = cfg.T, cfg.E, cfg.f, cfg.T * cfg.top_k
     i32, f32 = torch.int32, torch.float32
-    spec = [("topk_idx", i32, (T, 2)), ("topk_w", f32, (T, 2)), ("logits", f32, (T, E)), ("route", i32, (3 * E + 1,)),
-            ("perm", i32, (rows,)), ("slot_of", i32, (T, 2)), ("row_scale", f32, (rows,)),
-            ("g_codes", torch.int8, (rows, f)), ("u_codes", torch.int8, (rows, f)),
-            ("g_scale", torch.bfloat16, (rows, f // 32)), ("u_scale", torch.bfloat16, (rows, f // 32))]
-    views = _carve(ckpt, spec)
-    route = views.pop("route")
-    views.update(counts_raw=route[:E], counts_kept=route[E:2 * E], offsets=route[2 * E:])
-    return views
+    return _Views(ckpt, [("topk_idx", i32, (T, 2)), ("topk_w", f32, (T, 2)), ("logits", f32, (T, E)),
+                         ("route", i32, (3 * E + 1,)), ("perm", i32, (rows,)), ("slot_of", i32, (T, 2)),
+                         ("row_scale", f32, (rows,)), ("g_codes", torch.int8, (rows, f)),
+                         ("u_codes", torch.int8, (rows, f)), ("g_scale", torch.bfloat16, (rows, f // 32)),
+                         ("u_scale", torch.bfloat16, (rows, f // 32))])
 
 
 def _nbytes(t):
@@ -887,7 +893,7 @@ def mx4_workspace_views(cfg: Config, ws):
     R = rows // 128 + cfg.E
     spec = [("x_codes", (rows, d)), ("x_scales", (R, d // 128, 512)), ("h_codes", (rows, f)),
             ("h_scales", (R, f // 128, 512))]
-    return _carve(ws, [(name, torch.uint8, shape) for name, shape in spec])
+    return _Views(ws, [(name, torch.uint8, shape) for name, shape in spec])
 
 
 def expert_ffn_mx4(cfg: Config, x_perm, offsets, qw: MxExperts, row_scale=None, y=None, ws=None, stream=None):

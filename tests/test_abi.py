@@ -394,7 +394,9 @@ def test_checkpoint_views_cover_the_checkpoint(moe):
         last = v["u_scale"]
         end = last.data_ptr() - ck.data_ptr() + last.numel() * 2
         assert ck.numel() - 256 < end <= ck.numel()
-        assert v["offsets"].numel() == 9 and v["logits"].dtype == torch.float32
+        assert v["route"].numel() == 25 and v["logits"].dtype == torch.float32 and len(dict(v.items())) == 11
+        with pytest.raises(ValueError, match="its parts take"):
+            moe.checkpoint_views_c8(c, ck[:-256])
     x = torch.zeros((37, 256), dtype=torch.bfloat16)
     w = torch.zeros((8, 256, 512), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="dlogits must"):

@@ -83,6 +83,8 @@ def step(request):
     torch.cuda.synchronize()
     v = moe.checkpoint_views_c8(s.cfg, s.ck)
     s.kept = {k: (t.float() if t.dtype == torch.bfloat16 else t).cpu().numpy() for k, t in v.items()}
+    route = s.kept.pop("route")
+    s.kept.update(counts_raw=route[:8], counts_kept=route[8:16], offsets=route[16:])
     return s
 
 
@@ -248,7 +250,7 @@ def test_blocks_with_overflow_and_zero_rows():
     out = s.forward()
     torch.cuda.synchronize()
     v = moe.checkpoint_views_c8(s.cfg, s.ck)
-    n = int(v["offsets"][8])
+    n = int(v["route"][24])
     tok = v["perm"][:n]
     for q in ("g", "u"):
         scale, codes = v[q + "_scale"][:n].float(), v[q + "_codes"][:n]
