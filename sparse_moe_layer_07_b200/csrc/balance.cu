@@ -354,7 +354,8 @@ __device__ __forceinline__ void empty_counts(const BalanceArgs& a, int part, int
 __device__ __forceinline__ void store_loss(const BalanceArgs& a, double f, double z, int n) {
   const double inv = n > 0 ? 1.0 / (double)n : 0.0;
   const double balance = (double)kE * f * inv, zl = z * inv;
-  a.loss[0] = (float)((double)a.a * balance + (double)a.b * zl);
+  // a term without weight stays out, an infinite one too
+  a.loss[0] = (float)((a.a != 0.f ? (double)a.a * balance : 0.0) + (a.b != 0.f ? (double)a.b * zl : 0.0));
   a.loss[1] = (float)balance;
   a.loss[2] = (float)zl;
 }

@@ -24,7 +24,7 @@
 // for the weights.  The epilogue reads the 48 shared columns first and releases
 // them; the next tile's MMAs start then, while the rest is still being read.
 //
-// Row tiles of 128 (or 32, see Ring); a tile with at most 96 rows loads its rows
+// Row tiles of 128 (or 32 or 64, see Ring); a tile with at most 96 rows loads its rows
 // in boxes of 32, so that a decode tile moves 4 KB of rows beside 17 KB of
 // weights a stage.
 // Rows past an expert's end are computed from whatever is there and never
@@ -57,22 +57,24 @@ constexpr int kScaleSets = 4;
 static_assert(kScaleCol + 12 * kScaleSets <= kTmemCols, "TMEM columns");
 constexpr int kGroupSlots = 3;         // groups of scales in shared memory
 
-// BM rows a tile: 128, or 32 where few rows an expert are expected.  The
-// block-scaled MMA takes 128 rows on its A side at least, so tiles of 32 put the
-// weights there (two MMAs of 128 channels x 32 rows for 256 channels) and the rows
+// BM rows a tile: 128, or 32 or 64 where few rows an expert are expected.  The
+// block-scaled MMA takes 128 rows on its A side at least, so these put the
+// weights there (two MMAs of 128 channels x BM rows for 256 channels) and the rows
 // on the B side: an MMA then costs its 4 KB of weights, and the accumulators are
-// 64 columns, lane = channel, column = row.  With the rows on the A side, padded
+// 2 BM columns, lane = channel, column = row.  With the rows on the A side, padded
 // to 128, the tensor core was busy for 60% of the time and gate/up of Grok-1
-// decode took 307 us (259 with the MMAs' width cut).  The room of the rows goes to
-// a fifth stage and to scales 16 K blocks ahead: they come from DRAM here, and
-// with 4 blocks ahead the MMAs waited for them (338 us).
+// decode (T 32) took 307 us, where it takes 257 so (1.71 GB of weights and scales:
+// 6.67 TB/s).  The room of the rows goes to a fifth stage (4: 5 to 6% slower at 64
+// rows) and to scales further ahead: they come from DRAM here, and with 4 K blocks
+// ahead the MMAs waited for them (338 us).
 template <int BM>
 struct Ring {
-  static constexpr int kStages = BM == 128 ? 4 : 5;
+  static constexpr bool kSwap = BM < 128;           // weights on the A side
+  static constexpr int kStages = kSwap ? 5 : 4;
   static constexpr int A_BYTES = BM * BK;
-  static constexpr int kGroup = BM == 128 ? 4 : 8;  // K blocks whose scales are loaded together
+  static constexpr int kGroup = BM == 32 ? 8 : (BM == 64 ? 5 : 4);  // K blocks whose scales are loaded together
   static constexpr int GROUP_BYTES = 3 * kGroup * 512;
-  static constexpr int kBars = 2 * kStages + 2 + 1 + kScaleSets + 2 * kGroupSlots + 1;
+  static constexpr int kBars = 2 * kStages + 2 + 2 + kScaleSets + 2 * kGroupSlots + 1;
   static constexpr int SMEM_BYTES = 1024 + kStages * (A_BYTES + B_BYTES) + kGroupSlots * GROUP_BYTES + kBars * 8 + 16;
   static_assert(SMEM_BYTES + 256 <= 227 * 1024, "shared memory budget");
 };
@@ -180,8 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sG + kGroupSlots * GROUP_BYTES);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;        // accumulator 0 / 1 complete
-  uint64_t* tshared = tfull + 2;      // the columns both accumulators use have been read
-  uint64_t* sfull = tshared + 1;      // scale set written
+  uint64_t* tshared = tfull + 2;      // [0]: the columns both accumulators use have been read
+                                      // (swapped: accumulator 0 / 1 has been read)
+  uint64_t* sfull = tshared + 2;      // scale set written
   uint64_t* gfull = sfull + kScaleSets;  // group of scales landed
   uint64_t* gfree = gfull + kGroupSlots; // ... and read
   uint64_t* drain = gfree + kGroupSlots;
@@ -199,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&tfull[0], 1);
     mbar_init(&tfull[1], 1);
-    mbar_init(tshared, 128);
+    mbar_init(&tshared[0], 128);
+    mbar_init(&tshared[1], 128);
     for (int s = 0; s < kScaleSets; ++s) mbar_init(&sfull[s], 4);
     for (int s = 0; s < kGroupSlots; ++s) {
       mbar_init(&gfull[s], 1);
@@ -286,12 +290,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
       const Tile t = decode_tile<BM>(sched, args, L);
       const int n_kb = __shfl_sync(0xffffffffu, t.kb1 - t.kb0, 0);
-      const uint32_t idesc = BM == 32 ? idesc_mx_e2m1_e4m3(128, 32)
+      const uint32_t idesc = R::kSwap ? idesc_mx_e2m1_e4m3(128, BM)
                                       : idesc_mx_e4m3_e2m1(128, MODE == kGateUp ? 256 : bn, 0);
-      // the previous tile's epilogue has read the shared columns (and so has
-      // finished the tile before, whose accumulator this one takes)
-      if (tc > 0) ok = __all_sync(0xffffffffu, mbar_wait(tshared, (tc - 1) & 1u, abort_flag));
+      if (R::kSwap) {
+        // two accumulators apart from each other: this one's last tile has been read
+        ok = __all_sync(0xffffffffu, mbar_wait(&tshared[tc & 1u], ((tc >> 1) & 1u) ^ 1u, abort_flag));
+      } else if (tc > 0) {
+        // the previous tile's epilogue has read the shared columns (and so has
+        // finished the tile before, whose accumulator this one takes)
+        ok = __all_sync(0xffffffffu, mbar_wait(&tshared[0], (tc - 1) & 1u, abort_flag));
+      }
       if (!ok) break;
+      tc_fence_after();
       const uint32_t d_tmem = tmem_base + ((tc & 1u) ? kAccSecond : 0);
       for (int i = 0; i < n_kb; ++i, ++it) {
         const uint32_t s = it % S, set = it % kScaleSets;
@@ -305,11 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of K further each: 2 in the descriptors' 16-byte units
           const uint32_t id = idesc | idesc_mx_scale_byte(kk), acc = (i > 0 || kk > 0) ? 1u : 0u;
-          if (BM == 128) {
+          if (!R::kSwap) {
             umma_mxf8f6f4_if(lead, d_tmem, ad + 2 * kk, bd + 2 * kk, id, sfa, sfa + 4, acc);
           } else {
             umma_mxf8f6f4_if(lead, d_tmem, bd + 2 * kk, ad + 2 * kk, id, sfa + 4, sfa, acc);
-            umma_mxf8f6f4_if(lead, d_tmem + 32, bd + 2 * kk + B_HALF / 16, ad + 2 * kk, id, sfa + 8, sfa, acc);
+            umma_mxf8f6f4_if(lead, d_tmem + BM, bd + 2 * kk + B_HALF / 16, ad + 2 * kk, id, sfa + 8, sfa, acc);
           }
         }
         umma_commit_if(lead, &empty[s]);
@@ -398,6 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (BM == 32) {
             const uint32_t rows32 = t.in_mtile / 32;
             va.x = rows32 == 0 ? va.x : (rows32 == 1 ? va.y : (rows32 == 2 ? va.z : va.w));
+          } else if (BM == 64) {
+            va.x = t.in_mtile == 0 ? va.x : va.z;
+            va.y = t.in_mtile == 0 ? va.y : va.w;
           } else if (MODE == kDownSum && (t.nt * bn) % 128 != 0) {  // 192 columns from the middle of a block
             vb.x = vb.z;
             vb.y = vb.w;
@@ -448,44 +461,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      if (BM == 32) {
-        // lane = channel, column = row
-        uint32_t v[2][32];
+      if (R::kSwap) {
+        // lane = channel, column = row, 32 rows at a time
         const uint32_t tacc = tmem_base + (buf ? kAccSecond : 0) + ((uint32_t)(q * 32) << 16);
-        tmem_ld32(tacc, v[0]);
-        tmem_ld32(tacc + 32, v[1]);
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(tshared);
-        if (MODE == kGateUp) {
-          uint8_t* dst = args.h + (int64_t)t.m0 * args.ld + t.nt * 128 + r;
-          uint8_t* sc = args.h_scales + ((int64_t)t.mtile * (args.ld / 128) + t.nt) * 512;
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= t.rows) break;
-            // the warp's 32 channels are the block
-            const float h = silu_mul_fast(__uint_as_float(v[0][j]), __uint_as_float(v[1][j]));
-            const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
-            const int x = mx_exponent<8, kMxTopE4m3>(m);
-            const bool bad = m >= 0x7f800000u;
-            dst[j * args.ld] = bad ? 0x7f : (uint8_t)e4m3x2(h * mx_inverse(x), 0.f);
-            if (lane == 0) sc[mx_scale_at(t.in_mtile + j, q)] = bad ? 255 : (uint8_t)(x + 127);
+#pragma unroll 1
+        for (int j0 = 0; j0 < BM; j0 += 32) {
+          uint32_t v[2][32];
+          tmem_ld32(tacc + j0, v[0]);
+          tmem_ld32(tacc + BM + j0, v[1]);
+          tmem_wait_ld();
+          if (j0 + 32 >= BM) {
+            tc_fence_before();
+            mbar_arrive(&tshared[buf]);
           }
-        } else {
-          const float mine = lane < t.rows && args.row_scale ? __ldg(args.row_scale + t.m0 + lane) : 1.0f;
-          float* dst = args.out + ((int64_t)t.split * args.rows_alloc + t.m0) * args.ld + t.nt * 256 + r;
+          const int n = t.rows - j0;  // rows of this batch, all above 31 alike
+          if (n <= 0) continue;
+          if (MODE == kGateUp) {
+            uint8_t* dst = args.h + (int64_t)(t.m0 + j0) * args.ld + t.nt * 128 + r;
+            uint8_t* sc = args.h_scales + ((int64_t)t.mtile * (args.ld / 128) + t.nt) * 512;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= t.rows) break;
-            const float s1 = __shfl_sync(0xffffffffu, mine, j);
-            dst[j * args.ld] = s1 * __uint_as_float(v[0][j]);
-            dst[j * args.ld + 128] = s1 * __uint_as_float(v[1][j]);
+            for (int j = 0; j < 32; ++j) {
+              if (j >= n) break;
+              // the warp's 32 channels are the block
+              const float h = silu_mul_fast(__uint_as_float(v[0][j]), __uint_as_float(v[1][j]));
+              const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(h) & 0x7fffffffu);
+              const int x = mx_exponent<8, kMxTopE4m3>(m);
+              const bool bad = m >= 0x7f800000u;
+              dst[j * args.ld] = bad ? 0x7f : (uint8_t)e4m3x2(h * mx_inverse(x), 0.f);
+              if (lane == 0) sc[mx_scale_at(t.in_mtile + j0 + j, q)] = bad ? 255 : (uint8_t)(x + 127);
+            }
+          } else {
+            const float mine = lane < n && args.row_scale ? __ldg(args.row_scale + t.m0 + j0 + lane) : 1.0f;
+            float* dst = args.out + ((int64_t)t.split * args.rows_alloc + t.m0 + j0) * args.ld + t.nt * 256 + r;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (j >= n) break;
+              const float s1 = __shfl_sync(0xffffffffu, mine, j);
+              dst[j * args.ld] = s1 * __uint_as_float(v[0][j]);
+              dst[j * args.ld + 128] = s1 * __uint_as_float(v[1][j]);
+            }
           }
         }
         continue;
       }
       if (q * 32 >= t.rows) {  // a warp without rows reads nothing
-        mbar_arrive(tshared);
+        mbar_arrive(&tshared[0]);
         continue;
       }
       const bool valid = r < t.rows;
@@ -506,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_regs_ready(early[0]);
       tmem_regs_ready(early[1]);
       tc_fence_before();
-      mbar_arrive(tshared);
+      mbar_arrive(&tshared[0]);
       if (MODE == kGateUp) {
         uint32_t scales = 0;
         uint8_t* dst = args.h + (int64_t)row * args.ld + t.nt * 128;
@@ -667,12 +687,17 @@ cudaError_t launch_mx_tiles(const CUtensorMap& a, const CUtensorMap& a32, const 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Row tiles of 32 where an expert gets at most 16 rows on the average (Grok-1
-// decode), else of 128.
+// Row tiles that hold an expert's rows at once: 32 where it gets up to 24 on the
+// average, 64 up to 48, else 128.  Gate/up, d 6144, f 32768: T 96 263 us with
+// tiles of 32 against 323 with 128; T 128 337 with 32 (a second tile reads the
+// weights again), 282 with 64, 328 with 128; T 192 415, 293, 331.
 template <int MODE>
 cudaError_t launch_mx(const CUtensorMap& a, const CUtensorMap& a32, const CUtensorMap& b0, const CUtensorMap& b1,
                       const MxArgs& args, cudaStream_t s, const Ctx& ctx) {
-  if (MODE != kDownSum && args.rows_alloc <= 16 * kE) return launch_mx_tiles<MODE, 32>(a, a32, b0, b1, args, s, ctx);
+  if constexpr (MODE != kDownSum) {
+    if (args.rows_alloc <= 24 * kE) return launch_mx_tiles<MODE, 32>(a, a32, b0, b1, args, s, ctx);
+    if (args.rows_alloc <= 48 * kE) return launch_mx_tiles<MODE, 64>(a, a32, b0, b1, args, s, ctx);
+  }
   return launch_mx_tiles<MODE, 128>(a, a32, b0, b1, args, s, ctx);
 }
 

@@ -124,6 +124,14 @@ def test_infinite_and_extreme_logits():
     assert torch.isfinite(got["dlogits"][rest.cuda()]).all()
 
 
+def test_a_loss_without_weight_does_not_spoil_the_sum():
+    _, lg, idx = _inputs(50, 3)
+    lg[4] = 1e20  # lse^2 passes fp32
+    idx[4] = (0, 1)
+    got = _call(lg, idx, b=0.0)
+    assert torch.isinf(got["loss"][2]) and torch.isfinite(got["loss"][:2]).all() and torch.isfinite(got["dlogits"]).all()
+
+
 def test_same_expert_twice_counts_twice():
     _, lg, idx = _inputs(70, 4)
     idx[:, 1] = idx[:, 0]

@@ -77,7 +77,11 @@ CASES = {
     "few": dict(T=7, d=512, f=384, capacity_factor=4.0),
     "decode": dict(T=32, d=256, f=1024, capacity_factor=4.0),
     "decode_two": dict(T=60, d=256, f=256, capacity_factor=4.0, logit_bias=(60.0, 50.0, 0, 0, 0, 0, 0, 0)),
-    "decode_skew": dict(T=200, d=256, f=256, capacity_factor=4.0, logit_bias=(60.0, 50.0, 0, 0, 0, 0, 0, 0)),
+    "decode_skew": dict(T=230, d=256, f=256, capacity_factor=4.0, logit_bias=(60.0, 50.0, 0, 0, 0, 0, 0, 0)),
+    "tiles_of_32": dict(T=96, d=256, f=384, capacity_factor=4.0),
+    "tiles_of_64": dict(T=130, d=512, f=256, capacity_factor=4.0),
+    # 190 rows on each of two experts: three tiles of 64, the last at the middle of a 128-row block of scales
+    "tiles_of_64_skew": dict(T=190, d=256, f=256, capacity_factor=4.0, logit_bias=(60.0, 50.0, 0, 0, 0, 0, 0, 0)),
     "last_streaming": dict(T=256, d=256, f=640, capacity_factor=1.25),
     "first_tiled": dict(T=257, d=256, f=256, capacity_factor=4.0),
     "ragged": dict(T=700, d=512, f=384, capacity_factor=1.25),
