@@ -512,12 +512,13 @@ __global__ void __launch_bounds__(kNT, 3) balance_gradient_kernel(const BalanceA
   pdl_wait();
   const int n = __ldcg(a.ticket + 1);
   const float inv_n = n > 0 ? 1.0f / (float)n : 0.f;
+  uint8_t mask[kTok];
+  load_masks(a, blockIdx.x, mask);
   for (int c = blockIdx.x; c < a.n_chunks; c += gridDim.x) {
-    uint8_t mask[kTok];
-    float l[kTok][kE];
-    load_masks(a, c, mask);
-    load_logits(a, c, l);
     const Chunk k = open_chunk(a, c, mask, sh);
+    float l[kTok][kE];  // after the search: across it they cost a block's registers or spill
+    load_logits(a, c, l);
+    if (c + (int)gridDim.x < a.n_chunks) load_masks(a, c + gridDim.x, mask);
     clear_dead(a, k);
     float2 sum = make_float2(0.f, 0.f);
     for (int w0 = k.first; w0 <= k.last; w0 += kWindow) {
