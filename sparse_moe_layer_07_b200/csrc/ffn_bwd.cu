@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
       const int64_t base = row * args.ld + t.n0 + c_begin * 32;
       float w = 0.f;
       uint4 qg[2], qu[2];
-      uint32_t sg4[NC / 2] = {}, su4[NC / 2] = {};
+      uint2 sg4[NC / 4] = {}, su4[NC / 4] = {};  // four bf16 scales each
       auto load_chunk = [&](int c, uint4 (&a)[2], uint4 (&b)[2]) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -464,12 +464,8 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
         w = __ldg(args.row_scale + row);
 #pragma unroll
         for (int i = 0; i < NC / 4; ++i) {
-          const uint2 a = __ldg(reinterpret_cast<const uint2*>(args.codes.sg + base / 32) + i);
-          const uint2 b = __ldg(reinterpret_cast<const uint2*>(args.codes.su + base / 32) + i);
-          sg4[2 * i] = a.x;
-          sg4[2 * i + 1] = a.y;
-          su4[2 * i] = b.x;
-          su4[2 * i + 1] = b.y;
+          sg4[i] = __ldg(reinterpret_cast<const uint2*>(args.codes.sg + base / 32) + i);
+          su4[i] = __ldg(reinterpret_cast<const uint2*>(args.codes.su + base / 32) + i);
         }
         load_chunk(0, qg, qu);
       }
@@ -506,7 +502,9 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
             bulk_commit_group();
           }
         };
-#pragma unroll
+        // (one chunk's code: unrolled over the chunks, the warps waited for
+        // instructions a quarter of the time)
+#pragma unroll 1
         for (int c = 0; c < NC; ++c) {
           uint32_t v[32];
           tmem_ld32(tmine + c * 32, v);
@@ -516,9 +514,10 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
           tmem_wait_ld();
           uint4 kg[4], ku[4], kh[4];
           if (valid) {
-            const uint32_t pg = sg4[c >> 1], pu = su4[c >> 1];
-            const float sg = __uint_as_float((c & 1) ? pg & 0xffff0000u : pg << 16);
-            const float su = __uint_as_float((c & 1) ? pu & 0xffff0000u : pu << 16);
+            const uint2 pg = NC == 8 && c >= 4 ? sg4[NC / 4 - 1] : sg4[0], pu = NC == 8 && c >= 4 ? su4[NC / 4 - 1] : su4[0];
+            const uint32_t wg = (c & 2) ? pg.y : pg.x, wu = (c & 2) ? pu.y : pu.x;
+            const float sg = __uint_as_float((c & 1) ? wg & 0xffff0000u : wg << 16);
+            const float su = __uint_as_float((c & 1) ? wu & 0xffff0000u : wu << 16);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
               uint32_t og[4], ou[4], oh[4];

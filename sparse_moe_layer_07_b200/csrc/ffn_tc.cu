@@ -830,7 +830,7 @@ int tile_columns(const moe_config_t& c, int64_t n, std::initializer_list<int> wi
   int64_t best_cost = 0;
   for (const int w : widths) {
     if (n % w != 0) continue;
-    const int64_t waves = (n / w * row_tiles + num_sms - 1) / num_sms, cost = waves * (w + 32);
+    const int64_t waves = (n / w * row_tiles + num_sms - 1) / num_sms, cost = waves * (w + 240);
     if (best_cost == 0 || cost < best_cost) {
       best = w;
       best_cost = cost;
