@@ -164,18 +164,9 @@ __device__ __forceinline__ int source_token(const TcArgs& args, int row, int n_r
 // from TMEM column `tacc` on (gate/up: the matching up columns u_off further
 // on).  Rows with valid == false are read (the TMEM loads are warp-wide) but
 // not stored.  n_rows = kept rows.
-// kCodes (gate/up, tiles of 128 columns): the pre-activations are also kept as
-// 8-bit codes.  A thread holds 32 columns of one row at a time, which is a
-// block's worth, so amax needs no exchange between threads.  A warp whose 32 rows
-// are all valid (`whole`) puts H and the codes into `stage` and stores them by
-// TMA: the threads' own stores, each 16 bytes of its row, touch 32 lines an
-// instruction, and with three matrices to write they held the kernel back (187
-// against 175 us at T 2048, d 1536, f 8192; 10.1 against 9.3 ms at Grok size).
-template <int MODE, bool kScatter, bool kCodes = false>
+template <int MODE, bool kScatter>
 __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, int row0, int r, bool valid, int n0,
-                                              int n_cols, int u_off, uint32_t tacc, bool whole = false,
-                                              uint8_t* stage = nullptr, const CUtensorMap* tmH = nullptr,
-                                              const CUtensorMap* tmG = nullptr, const CUtensorMap* tmU = nullptr) {
+                                              int n_cols, int u_off, uint32_t tacc) {
   if (MODE == kGateUp) {
     __nv_bfloat16* H = static_cast<__nv_bfloat16*>(args.out);
     __nv_bfloat16* dst_row = H + (int64_t)(row0 + r) * args.ld_out + n0;
@@ -183,7 +174,6 @@ __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, in
     // flight while chunk c is computed and stored (the loop is unrolled so the
     // two register sets stay in registers)
     const int nch = n_cols / 32;
-    uint32_t scales_g[2] = {0, 0}, scales_u[2] = {0, 0};
     uint32_t gb[2][32], ub[2][32];
     tmem_ld32(tacc, gb[0]);
     tmem_ld32(tacc + u_off, ub[0]);
@@ -204,62 +194,13 @@ __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, in
       for (int i = 0; i < 16; ++i)
         p[i] = pack_bf16x2(silu_mul_fast(__uint_as_float(g[2 * i]), __uint_as_float(u[2 * i])),
                            silu_mul_fast(__uint_as_float(g[2 * i + 1]), __uint_as_float(u[2 * i + 1])));
-      if (kCodes && whole) {
-        const int lane = threadIdx.x & 31;
-        uint8_t* st = stage + (c & 1) * 4096;
-        uint32_t cg[8], cu[8];
-        scales_g[c >> 1] |= (uint32_t)code32(g, cg) << (16 * (c & 1));
-        scales_u[c >> 1] |= (uint32_t)code32(u, cu) << (16 * (c & 1));
-        if (lane == 0) bulk_wait_group_read<1>();  // the stores that last read this buffer are done with it
-        __syncwarp();
-        uint4* hl = reinterpret_cast<uint4*>(st + lane * 64);  // 64-byte swizzle
-#pragma unroll
-        for (int i = 0; i < 4; ++i) hl[i ^ ((lane >> 1) & 3)] = make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
-        uint4* gl = reinterpret_cast<uint4*>(st + 2048 + lane * 32);
-        uint4* ul = reinterpret_cast<uint4*>(st + 3072 + lane * 32);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          gl[i] = make_uint4(cg[4 * i], cg[4 * i + 1], cg[4 * i + 2], cg[4 * i + 3]);
-          ul[i] = make_uint4(cu[4 * i], cu[4 * i + 1], cu[4 * i + 2], cu[4 * i + 3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          const int y = row0 + r;  // lane 0 holds the warp's first row
-          tma_store_2d(tmH, st, n0 + c * 32, y);
-          tma_store_2d(tmG, st + 2048, n0 + c * 32, y);
-          tma_store_2d(tmU, st + 3072, n0 + c * 32, y);
-          bulk_commit_group();
-        }
-        if (c == 3) {
-          const int64_t so = ((int64_t)(row0 + r) * args.ld_out + n0) / 32;
-          *reinterpret_cast<uint2*>(args.scale_g + so) = make_uint2(scales_g[0], scales_g[1]);
-          *reinterpret_cast<uint2*>(args.scale_u + so) = make_uint2(scales_u[0], scales_u[1]);
-        }
-      } else if (valid) {
+      if (valid) {
         // streaming stores: H is read back by the next launch, not by this one, so
         // its lines should not push the operand tiles out of L2 (1-2% faster)
         uint4* d4 = reinterpret_cast<uint4*>(dst_row + c * 32);
 #pragma unroll
         for (int i = 0; i < 4; ++i) __stcs(d4 + i, make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]));
-        if (kCodes) {
-          const int64_t o = (int64_t)(row0 + r) * args.ld_out + n0 + c * 32;
-          uint32_t cg[8], cu[8];
-          scales_g[c >> 1] |= (uint32_t)code32(g, cg) << (16 * (c & 1));
-          scales_u[c >> 1] |= (uint32_t)code32(u, cu) << (16 * (c & 1));
-          uint4* g4 = reinterpret_cast<uint4*>(args.code_g + o);
-          uint4* u4 = reinterpret_cast<uint4*>(args.code_u + o);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            __stcs(g4 + i, make_uint4(cg[4 * i], cg[4 * i + 1], cg[4 * i + 2], cg[4 * i + 3]));
-            __stcs(u4 + i, make_uint4(cu[4 * i], cu[4 * i + 1], cu[4 * i + 2], cu[4 * i + 3]));
-          }
-          if (c == 3) {
-            const int64_t so = ((int64_t)(row0 + r) * args.ld_out + n0) / 32;
-            *reinterpret_cast<uint2*>(args.scale_g + so) = make_uint2(scales_g[0], scales_g[1]);
-            *reinterpret_cast<uint2*>(args.scale_u + so) = make_uint2(scales_u[0], scales_u[1]);
-          }
-        } else if (args.save_g) {
+        if (args.save_g) {
           // training: keep the pre-activations for the backward pass
           const int64_t o = (int64_t)(row0 + r) * args.ld_out + n0 + c * 32;
           uint4* g4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.save_g) + o);
@@ -324,12 +265,108 @@ __device__ __forceinline__ void epilogue_rows(const TcArgs& args, int n_rows, in
   }
 }
 
+// Epilogue of a gate/up tile of 128 columns that also keeps the pre-activations
+// as 8-bit codes.  A thread holds 32 columns of one row at a time, which is a
+// block's worth, so amax needs no exchange between threads.  A warp whose 32 rows
+// are all valid (`whole`) puts H and the codes into `stage` (two buffers of 4 KB)
+// and stores them by TMA: the threads' own stores, each 16 bytes of its row, touch
+// 32 lines an instruction, and with three matrices to write they held the kernel
+// back (187 against 175 us at T 2048, d 1536, f 8192; 10.1 against 9.3 ms at Grok
+// size).  r, row0, n0, tacc as in epilogue_rows.
+__device__ __forceinline__ void epilogue_codes(const TcArgs& args, int row0, int r, bool valid, int n0, uint32_t tacc,
+                                               bool whole, uint8_t* stage, const CUtensorMap* tmH,
+                                               const CUtensorMap* tmG, const CUtensorMap* tmU) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = row0 + r;
+  uint32_t gb[2][32], ub[2][32];
+  tmem_ld32(tacc, gb[0]);
+  tmem_ld32(tacc + 128, ub[0]);
+  uint32_t scales_g = 0, scales_u = 0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < 4; c0 += 2) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = c0 + k;
+      tmem_wait_ld();
+      tmem_regs_ready(gb[k]);
+      tmem_regs_ready(ub[k]);
+      if (c < 3) {  // the next chunk's loads fly during this one
+        tmem_ld32(tacc + (c + 1) * 32, gb[k ^ 1]);
+        tmem_ld32(tacc + 128 + (c + 1) * 32, ub[k ^ 1]);
+      }
+      const uint32_t(&g)[32] = gb[k];
+      const uint32_t(&u)[32] = ub[k];
+      uint4 h[4], cg[2], cu[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = 8 * i + 2 * j;
+          w[j] = pack_bf16x2(silu_mul_fast(__uint_as_float(g[e]), __uint_as_float(u[e])),
+                             silu_mul_fast(__uint_as_float(g[e + 1]), __uint_as_float(u[e + 1])));
+        }
+        h[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      uint32_t qg[8], qu[8];
+      const uint32_t sg = code32(g, qg), su = code32(u, qu);
+      scales_g = k == 0 ? sg : scales_g | sg << 16;
+      scales_u = k == 0 ? su : scales_u | su << 16;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        cg[i] = make_uint4(qg[4 * i], qg[4 * i + 1], qg[4 * i + 2], qg[4 * i + 3]);
+        cu[i] = make_uint4(qu[4 * i], qu[4 * i + 1], qu[4 * i + 2], qu[4 * i + 3]);
+      }
+      if (whole) {
+        uint8_t* st = stage + k * 4096;
+        if (lane == 0) bulk_wait_group_read<1>();  // the stores that last read this buffer are done with it
+        __syncwarp();
+        uint4* hl = reinterpret_cast<uint4*>(st + lane * 64);  // 64-byte swizzle
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hl[i ^ ((lane >> 1) & 3)] = h[i];
+        uint4* gl = reinterpret_cast<uint4*>(st + 2048 + lane * 32);
+        uint4* ul = reinterpret_cast<uint4*>(st + 3072 + lane * 32);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          gl[i] = cg[i];
+          ul[i] = cu[i];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {  // which holds the warp's first row
+          tma_store_2d(tmH, st, n0 + c * 32, (int)row);
+          tma_store_2d(tmG, st + 2048, n0 + c * 32, (int)row);
+          tma_store_2d(tmU, st + 3072, n0 + c * 32, (int)row);
+          bulk_commit_group();
+        }
+      } else if (valid) {
+        const int64_t o = row * args.ld_out + n0 + c * 32;
+        uint4* h4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(args.out) + o);
+        uint4* g4 = reinterpret_cast<uint4*>(args.code_g + o);
+        uint4* u4 = reinterpret_cast<uint4*>(args.code_u + o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __stcs(h4 + i, h[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          __stcs(g4 + i, cg[i]);
+          __stcs(u4 + i, cu[i]);
+        }
+      }
+    }
+    if (valid) {  // two blocks' scales
+      const int64_t so = (row * args.ld_out + n0) / 32 + c0;
+      *reinterpret_cast<uint32_t*>(args.scale_g + so) = scales_g;
+      *reinterpret_cast<uint32_t*>(args.scale_u + so) = scales_u;
+    }
+  }
+}
+
 // FUSED = true (down only): instead of writing Y by grouped row, the epilogue
 // adds row_scale * (H W_down) into a zeroed fp32 out[token] with vector
 // atomics.  With top-2 a token receives at most two terms and 0 + a + b rounds
 // the same in either order, so the result is the combine's fp32 sum bit for
 // bit, without the Y buffer.  FUSED = true with gate/up keeps the
-// pre-activations as 8-bit codes (epilogue_rows).
+// pre-activations as 8-bit codes (epilogue_codes).
 template <int MODE, int MMA_N, bool FUSED>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
@@ -493,9 +530,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = t.rows <= 64 ? (lane < 16 ? q * 16 + lane : BM) : q * 32 + lane;
       const bool valid = r < t.rows;
       const uint32_t tacc = tmem_base + buf * kAccStride + ((uint32_t)(q * 32) << 16);
-      epilogue_rows<MODE, kScatter, kCodes>(args, sched.offs[kE], t.m0, r, valid, t.n0, C::BN_OUT, C::BN_OUT, tacc,
-                                            t.rows > 64 && (q + 1) * 32 <= t.rows, sOut + (warp - 2) * 8192, &tmH,
-                                            &tmG, &tmU);
+      if (kCodes)
+        epilogue_codes(args, t.m0, r, valid, t.n0, tacc, t.rows > 64 && (q + 1) * 32 <= t.rows, sOut + (warp - 2) * 8192,
+                       &tmH, &tmG, &tmU);
+      else
+        epilogue_rows<MODE, kScatter>(args, sched.offs[kE], t.m0, r, valid, t.n0, C::BN_OUT, C::BN_OUT, tacc);
       tc_fence_before();
       mbar_arrive(&tempty[buf]);
     }
