@@ -47,10 +47,10 @@ constexpr int BK = 64;
 // per quarter each taking half of the tile's columns; for kDH that measured 14%
 // slower than 4 relative to the forward GEMMs in the same capture.)
 // C8 is 0, or with 8-bit checkpoints the number of kDH's epilogue warps: its
-// epilogue decodes as well, and 4 warps take about 36K clocks a tile, more than
-// the tile's products (8 clocks per unit of d) below d of about 4500: 8 warps
-// are 12% faster at d = 1536 (223 against 255 us, T 2048, f 8192), 4 warps 12%
-// at d = 6144 (6.11 against 6.94 ms, T 8192, f 32768).
+// epilogue decodes as well, and where the tile's products are few (8 clocks per
+// unit of d) it is what the tile waits for.  8 warps against 4 (f 8192): d 1536,
+// T 2048 154 against 172 us; d 2560, T 4096 348 against 362; d 4096 490 against
+// 492; d 6144 737-768 against 700-748, where the products hide it.
 template <int MODE, int C8 = 0>
 struct Warps {
   static constexpr int kEpi = MODE == 0 && C8 ? C8 : 4;
