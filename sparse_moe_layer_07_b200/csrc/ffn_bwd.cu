@@ -49,8 +49,8 @@ constexpr int BK = 64;
 // C8 is 0, or with 8-bit checkpoints the number of kDH's epilogue warps: its
 // epilogue decodes as well, and where the tile's products are few (8 clocks per
 // unit of d) it is what the tile waits for.  8 warps against 4 (f 8192): d 1536,
-// T 2048 154 against 172 us; d 2560, T 4096 348 against 362; d 4096 490 against
-// 492; d 6144 737-768 against 700-748, where the products hide it.
+// T 2048 122 against 139 us; d 2560, T 4096 326 against 321; d 4096 480 against
+// 475, where the products hide it.
 template <int MODE, int C8 = 0>
 struct Warps {
   static constexpr int kEpi = MODE == 0 && C8 ? C8 : 4;
@@ -453,11 +453,20 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
       float w = 0.f;
       uint4 qg[2], qu[2];
       uint2 sg4[NC / 4] = {}, su4[NC / 4] = {};  // four bf16 scales each
+      // a checkpoint is 16-byte aligned, and its parts lie multiples of 256 bytes apart
+      const bool sectors = (reinterpret_cast<uintptr_t>(args.codes.g) & 31u) == 0;
       auto load_chunk = [&](int c, uint4 (&a)[2], uint4 (&b)[2]) {
+        const uint4* g = reinterpret_cast<const uint4*>(args.codes.g + base + c * 32);
+        const uint4* u = reinterpret_cast<const uint4*>(args.codes.u + base + c * 32);
+        if (sectors) {
+          load32_once(g, a);
+          load32_once(u, b);
+        } else {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          a[p] = __ldcs(reinterpret_cast<const uint4*>(args.codes.g + base + c * 32) + p);
-          b[p] = __ldcs(reinterpret_cast<const uint4*>(args.codes.u + base + c * 32) + p);
+          for (int p = 0; p < 2; ++p) {
+            a[p] = __ldg(g + p);
+            b[p] = __ldg(u + p);
+          }
         }
       };
       if (MODE == kDH && C8 && valid) {
@@ -478,7 +487,8 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
       const uint32_t tacc = tmem_base + buf * kAccStride + ((uint32_t)(q * 32) << 16);
       if (MODE == kDH && C8) {
         const uint32_t tmine = tacc + c_begin * 32;
-        float dot = 0.f;
+        const f32x2 w2 = pack2(w, w), one = pack2(1.f, 1.f), minus1 = pack2(-1.f, -1.f);
+        f32x2 dot = pack2(0.f, 0.f);
         // The three results go out 32 rows x 32 columns at a time by TMA from shared
         // memory (rows of 64 bytes, 64-byte swizzle), two buffers a warp: stored by
         // the threads, each 16 bytes of its own row, they kept the load/store unit at
@@ -518,36 +528,29 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
             const uint32_t wg = (c & 2) ? pg.y : pg.x, wu = (c & 2) ? pu.y : pu.x;
             const float sg = __uint_as_float((c & 1) ? wg & 0xffff0000u : wg << 16);
             const float su = __uint_as_float((c & 1) ? wu & 0xffff0000u : wu << 16);
+            const f32x2 sg2 = pack2(sg, sg), su2 = pack2(su, su);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
               uint32_t og[4], ou[4], oh[4];
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int word = 2 * p + i;
-                float g4[4], u4[4], dg[4], du[4], hw[4];
-                codes4((&qg[word >> 2].x)[word & 3], g4);
-                codes4((&qu[word >> 2].x)[word & 3], u4);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float g = sg * g4[k], u = su * u4[k];
-                  const float dhu = __uint_as_float(v[p * 8 + 4 * i + k]);
-                  // the approximate quotient (2 ulp; 0 where e^-g passes 2^126, its
-                  // limit): the IEEE one held this epilogue at 65 us a tile
-                  const float sig = __fdividef(1.0f, 1.0f + __expf(-g));
-                  const float sl = g * sig;
-                  const float h = sl * u;
-                  dot = fmaf(dhu, h, dot);
-                  const float dh = w * dhu;
-                  dg[k] = dh * u * (sig * (1.0f + g * (1.0f - sig)));
-                  du[k] = dh * sl;
-                  hw[k] = w * h;
-                }
-                og[2 * i] = pack_bf16x2(dg[0], dg[1]);
-                og[2 * i + 1] = pack_bf16x2(dg[2], dg[3]);
-                ou[2 * i] = pack_bf16x2(du[0], du[1]);
-                ou[2 * i + 1] = pack_bf16x2(du[2], du[3]);
-                oh[2 * i] = pack_bf16x2(hw[0], hw[1]);
-                oh[2 * i + 1] = pack_bf16x2(hw[2], hw[3]);
+              for (int i = 0; i < 4; ++i) {  // two values at a time
+                const int word = 2 * p + (i >> 1);
+                const f32x2 g = mul2(sg2, codes2((&qg[word >> 2].x)[word & 3], i & 1));
+                const f32x2 u = mul2(su2, codes2((&qu[word >> 2].x)[word & 3], i & 1));
+                const f32x2 dhu = pack2(__uint_as_float(v[p * 8 + 2 * i]), __uint_as_float(v[p * 8 + 2 * i + 1]));
+                // the approximate quotient (2 ulp; 0 where e^-g passes 2^126, its
+                // limit): the IEEE one held this epilogue at 65 us a tile
+                float g0, g1;
+                unpack2(g, g0, g1);
+                const f32x2 sig = pack2(__fdividef(1.0f, 1.0f + __expf(-g0)), __fdividef(1.0f, 1.0f + __expf(-g1)));
+                const f32x2 sl = mul2(g, sig);
+                const f32x2 h = mul2(sl, u);
+                dot = fma2(dhu, h, dot);
+                const f32x2 dh = mul2(w2, dhu);
+                // silu'(g) = sig + sl (1 - sig)
+                og[i] = pack_bf16x2(mul2(mul2(dh, u), fma2(sl, fma2(sig, minus1, one), sig)));
+                ou[i] = pack_bf16x2(mul2(dh, sl));
+                oh[i] = pack_bf16x2(mul2(w2, h));
               }
               kg[p] = make_uint4(og[0], og[1], og[2], og[3]);
               ku[p] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
@@ -576,7 +579,11 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
             }
           }
         }
-        if (valid) args.dw_part[(row * (int64_t)args.n_tiles + t.nb) * kSplit + half] = dot;
+        if (valid) {
+          float d0, d1;
+          unpack2(dot, d0, d1);
+          args.dw_part[(row * (int64_t)args.n_tiles + t.nb) * kSplit + half] = d0 + d1;
+        }
       } else if (MODE == kDH) {
         const bool valid = r < t.rows;
         const int64_t row = t.m0 + r;
@@ -788,7 +795,7 @@ bool map_weights(CUtensorMap* m, const void* base, int E, int64_t R, int64_t C) 
 }  // namespace
 
 int bwd_dh_parts_per_tile() { return Warps<kDH>::kEpi / 4; }
-int bwd_dh_c8_parts_per_tile(const moe_config_t& c) { return c.d < 4096 ? 2 : 1; }
+int bwd_dh_c8_parts_per_tile(const moe_config_t& c) { return c.d < 2048 ? 2 : 1; }
 
 cudaError_t launch_bwd_dh(const moe_config_t& c, const void* dout_perm, const int32_t* offsets, const void* wd,
                           const void* G, const void* U, const void* H, const float* row_scale, void* dG, void* dU,

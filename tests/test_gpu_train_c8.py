@@ -242,6 +242,19 @@ def test_shared_scratch_of_two_layers_and_a_replayed_graph():
     assert moe.get_device_error() == 0
 
 
+def test_checkpoint_at_a_16_byte_address():
+    """The alignment that every buffer of the library may have gives the same bits."""
+    s = Step("ragged")
+    out, grads = s.forward(), s.backward()
+    s.ck = torch.empty(s.ck.numel() + 16, dtype=torch.uint8, device="cuda")[16:]
+    assert s.ck.data_ptr() % 32 == 16
+    assert torch.equal(out, s.forward())
+    again = s.backward()
+    for q in KEYS:
+        assert torch.equal(grads[q], again[q]), q
+    assert moe.get_device_error() == 0
+
+
 def test_blocks_with_overflow_and_zero_rows():
     s = Step("few_rows")
     x = s.L.dev["x"]
