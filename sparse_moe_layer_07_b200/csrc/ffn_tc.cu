@@ -325,7 +325,7 @@ __device__ __forceinline__ void epilogue_codes(const TcArgs& args, int row0, int
 #pragma unroll
         for (int i = 0; i < 4; ++i) hl[i ^ ((lane >> 1) & 3)] = h[i];
         uint4* gl = reinterpret_cast<uint4*>(st + 2048 + lane * 32);
-        uint4* ul = reinterpret_cast<uint4*>(st + 3072 + lane * 32);
+        uint4* ul = reinterpret_cast<uint4*>(st + 2048 + 1024 + lane * 32);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           gl[i] = cg[i];
@@ -336,7 +336,7 @@ __device__ __forceinline__ void epilogue_codes(const TcArgs& args, int row0, int
         if (lane == 0) {  // which holds the warp's first row
           tma_store_2d(tmH, st, n0 + c * 32, (int)row);
           tma_store_2d(tmG, st + 2048, n0 + c * 32, (int)row);
-          tma_store_2d(tmU, st + 3072, n0 + c * 32, (int)row);
+          tma_store_2d(tmU, st + 2048 + 1024, n0 + c * 32, (int)row);
           bulk_commit_group();
         }
       } else if (valid) {
