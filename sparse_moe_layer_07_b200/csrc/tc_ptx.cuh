@@ -321,23 +321,11 @@ __device__ __forceinline__ void umma_s8(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
-// D[tmem] (+)= (A scale_A) (B scale_B), 8/6/4-bit floating point in blocks of 32
-// along K with e8m0 scales in TMEM -> fp32, one CTA.  The types and the byte of
-// each scale word are in the instruction descriptor.
-__device__ __forceinline__ void umma_mxf8f6f4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
-}
-
-// Guarded forms for a warp that runs its issue loop as a whole: the lane with
-// `lead` set issues, without a branch (reconverging after one cost 250 clocks
-// a K block here).
+// Block-scaled product D[tmem] (+)= (A scale_A) (B scale_B), 8/6/4-bit floating
+// point in blocks of 32 along K with e8m0 scales in TMEM -> fp32, one CTA; the
+// types and the byte of each scale word are in the instruction descriptor.  For a
+// warp that runs its issue loop as a whole: the lane with `lead` set issues,
+// without a branch (reconverging after one cost 250 clocks a K block here).
 __device__ __forceinline__ void umma_mxf8f6f4_if(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                                  uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
                                                  uint32_t accumulate) {
@@ -350,16 +338,6 @@ __device__ __forceinline__ void umma_mxf8f6f4_if(uint32_t lead, uint32_t d_tmem,
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void umma_bf16_if(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
 __device__ __forceinline__ void umma_commit_if(uint32_t lead, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -367,13 +345,6 @@ __device__ __forceinline__ void umma_commit_if(uint32_t lead, uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
       "r"(lead)
       : "memory");
-}
-
-// Copies 512 bytes of scales (32 rows of 16 bytes) from shared memory into four
-// TMEM columns, repeated in each of the four lane quarters: byte b of column j
-// of lane i is byte 4 j + b of row i.  Ordered before later MMAs of this thread.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
 // Arrives once on `bar` when every tcgen05 op issued so far by this thread is done.
@@ -410,7 +381,7 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-// The other way: thread i writes 4 columns of its lane.
+// Thread i writes 4 (or 8) columns of its TMEM lane.
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w)
@@ -445,12 +416,6 @@ __device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[32]) {
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo_bytes >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo_bytes >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// The same without a swizzle: 8-row x 16-byte core matrices of 128 contiguous
-// bytes, one after the other along the rows.
-__device__ __forceinline__ uint64_t plain_desc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
 }
 
 // Instruction descriptor, kind::mxf8f6f4, K-major e4m3 A and e2m1 B with e8m0
