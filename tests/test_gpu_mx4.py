@@ -273,6 +273,26 @@ def test_replays_from_a_graph(T, cf):
     assert moe.get_device_error() == 0
 
 
+def test_batches_on_several_streams_at_once():
+    """One set of weights, a batch and a scratch for each stream: one token, decode, and both sizes of row tiles."""
+    L = LayerInputs(configs.scaled(W["mid_bf16"], name="mx_streams", T=700, d=256, f=384, capacity_factor=4.0))
+    D = L.dev
+    qw = moe.MxExperts(L.cfg, D["wg"], D["wu"], D["wd"])
+    jobs = []
+    for T in (1, 32, 130, 700):
+        c = moe.Config(T, 256, 384, capacity_factor=4.0)
+        jobs.append((c, D["x"][:T].contiguous(), torch.empty(moe.workspace_size_mx4(c), dtype=torch.uint8, device="cuda")))
+    want = [moe.layer_forward_mx4(c, x, D["wr"], qw, ws=ws) for c, x, ws in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [moe.layer_forward_mx4(c, x, D["wr"], qw, ws=ws, stream=st)
+           for _ in range(5) for (c, x, ws), st in zip(jobs, streams)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert torch.equal(out, want[i % len(jobs)]), i
+    assert moe.get_device_error() == 0
+
+
 def test_trained_then_served():
     """The set in use: a training step with 8-bit checkpoints and the balance loss, an update, the result served in 4 bits."""
     w = configs.scaled(W["mid_bf16"], name="mx_serve", T=400, d=256, f=512, capacity_factor=1.25)

@@ -43,6 +43,8 @@ CASES = {
     # experts 2..7 have no rows
     "two_experts": dict(T=272, d=256, f=256, capacity_factor=4.0, logit_bias=(60.0, 50.0, 0, 0, 0, 0, 0, 0)),
     "wide": dict(T=130, d=1536, f=512, capacity_factor=4.0),
+    # d of 2048 and more: the dH kernel's other split of its epilogue
+    "wider": dict(T=300, d=2304, f=512, capacity_factor=1.25),
 }
 
 
@@ -252,6 +254,36 @@ def test_checkpoint_at_a_16_byte_address():
     again = s.backward()
     for q in KEYS:
         assert torch.equal(grads[q], again[q]), q
+    assert moe.get_device_error() == 0
+
+
+def test_tile_mode_does_not_change_the_bits():
+    s = Step("ragged")
+    out, grads = s.forward(), s.backward()
+    with moe.gemm_tiles("pair"):
+        assert torch.equal(out, s.forward())
+        again = s.backward()
+    for q in KEYS:
+        assert torch.equal(grads[q], again[q]), q
+    assert moe.get_device_error() == 0
+
+
+def test_two_steps_on_two_streams_at_once():
+    steps = [Step("ragged"), Step("drop"), Step("two_experts")]
+    want = [(s.forward(), s.backward()) for s in steps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    got = [[] for _ in steps]
+    for _ in range(3):
+        for s, st, g in zip(steps, streams, got):
+            with torch.cuda.stream(st):
+                g.append((s.forward(), s.backward()))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for out, grads in g:
+            assert torch.equal(w[0], out)
+            for q in KEYS:
+                assert torch.equal(w[1][q], grads[q]), q
     assert moe.get_device_error() == 0
 
 
