@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(256) router_bwd_token_kernel(
     const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w, const __nv_bfloat16* __restrict__ wr,
     const float* __restrict__ dx32, int64_t T, int64_t d, int64_t max_slot, float* __restrict__ dlogits,
     float* __restrict__ dweight, __nv_bfloat16* __restrict__ dx, int* err) {
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int nq = (int)(d / 4);  // 4-column groups of a row (d is a multiple of 128)
@@ -155,6 +156,7 @@ __global__ void __launch_bounds__(256) router_bwd_token_aux_kernel(
     const int32_t* __restrict__ topk_idx, const float* __restrict__ topk_w, const __nv_bfloat16* __restrict__ wr,
     const float* __restrict__ dx32, int64_t T, int64_t d, int64_t max_slot, float* __restrict__ dlogits,
     float* __restrict__ dweight, __nv_bfloat16* __restrict__ dx, const float* __restrict__ dl_aux, int* err) {
+  pdl_wait();
   const int lane = threadIdx.x & 31, group = lane >> 3, part = lane & 7;
   const int64_t warps = (int64_t)gridDim.x * (blockDim.x >> 5);
   const int nq = (int)(d / 4);
@@ -239,6 +241,7 @@ __global__ void __launch_bounds__(256) router_bwd_token_aux_kernel(
 __global__ void __launch_bounds__(256) router_bwd_weight_kernel(const float* __restrict__ dlogits,
                                                                const __nv_bfloat16* __restrict__ x, int64_t T,
                                                                int64_t d, int chunks, float* __restrict__ part) {
+  pdl_wait();
   const int64_t v = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;  // 8-column group
   const int c = blockIdx.y;
   const int64_t per = (T + chunks - 1) / chunks;
@@ -295,6 +298,7 @@ __global__ void __launch_bounds__(256) router_bwd_reduce_kernel(const float* __r
                                                                const float* __restrict__ dlogits, int64_t T,
                                                                int64_t d, Tout* __restrict__ dw_router,
                                                                Tout* __restrict__ dbias) {
+  pdl_wait();
   const int64_t n = (int64_t)kE * d;
   for (int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; k < n; k += (int64_t)gridDim.x * blockDim.x) {
     // sixteen chunks' loads in flight, added in chunk order (one load at a time
@@ -354,30 +358,32 @@ cudaError_t launch_router_bwd(const moe_config_t& c, const float* dw_part, int n
                               void* dbias, float* wr_part, cudaStream_t s, const Ctx& ctx, const float* dl_aux,
                               bool bf16_out) {
   if (c.T == 0) return cudaSuccess;
+  const dim3 threads(256);
+  const auto* wr = static_cast<const __nv_bfloat16*>(w_router);
+  auto* dx16 = static_cast<__nv_bfloat16*>(dx);
+  cudaError_t e;
   if (dl_aux)
-    router_bwd_token_aux_kernel<<<capped((c.T + 15) / 16, ctx), 256, 0, s>>>(
-        dw_part, n_parts, slot_of, topk_idx, topk_w, static_cast<const __nv_bfloat16*>(w_router), dx32, c.T, c.d,
-        slot_rows(c), dlogits, dweight, static_cast<__nv_bfloat16*>(dx), dl_aux, ctx.err);
+    e = launch_pdl(router_bwd_token_aux_kernel, dim3(capped((c.T + 15) / 16, ctx)), threads, 0, s, no_extra_attr(),
+                   dw_part, n_parts, slot_of, topk_idx, topk_w, wr, dx32, c.T, c.d, slot_rows(c), dlogits, dweight, dx16,
+                   dl_aux, ctx.err);
   else
-    router_bwd_token_kernel<<<capped((c.T + 7) / 8, ctx), 256, 0, s>>>(
-        dw_part, n_parts, slot_of, topk_idx, topk_w, static_cast<const __nv_bfloat16*>(w_router), dx32, c.T, c.d,
-        slot_rows(c), dlogits, dweight, static_cast<__nv_bfloat16*>(dx), ctx.err);
-  cudaError_t e = cudaGetLastError();
+    e = launch_pdl(router_bwd_token_kernel, dim3(capped((c.T + 7) / 8, ctx)), threads, 0, s, no_extra_attr(), dw_part,
+                   n_parts, slot_of, topk_idx, topk_w, wr, dx32, c.T, c.d, slot_rows(c), dlogits, dweight, dx16, ctx.err);
   if (e != cudaSuccess) return e;
-  dim3 grid((unsigned)((c.d / 8 + 255) / 256), (unsigned)kRouterBwdChunks);
-  router_bwd_weight_kernel<<<grid, 256, 0, s>>>(dlogits, static_cast<const __nv_bfloat16*>(x), c.T, c.d,
-                                                kRouterBwdChunks, wr_part);
-  e = cudaGetLastError();
+  const dim3 grid((unsigned)((c.d / 8 + 255) / 256), (unsigned)kRouterBwdChunks);
+  e = launch_pdl(router_bwd_weight_kernel, grid, threads, 0, s, no_extra_attr(), static_cast<const float*>(dlogits),
+                 static_cast<const __nv_bfloat16*>(x), c.T, c.d, kRouterBwdChunks, wr_part);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = capped((kE * c.d + 255) / 256, ctx);
+  const dim3 blocks(capped((kE * c.d + 255) / 256, ctx));
+  const float *part = wr_part, *dl = dlogits;
   if (bf16_out)
-    router_bwd_reduce_kernel<<<blocks, 256, 0, s>>>(wr_part, kRouterBwdChunks, dlogits, c.T, c.d,
-                                                    static_cast<__nv_bfloat16*>(dw_router),
-                                                    static_cast<__nv_bfloat16*>(dbias));
+    e = launch_pdl(router_bwd_reduce_kernel<__nv_bfloat16>, blocks, threads, 0, s, no_extra_attr(), part,
+                   kRouterBwdChunks, dl, c.T, c.d, static_cast<__nv_bfloat16*>(dw_router),
+                   static_cast<__nv_bfloat16*>(dbias));
   else
-    router_bwd_reduce_kernel<<<blocks, 256, 0, s>>>(wr_part, kRouterBwdChunks, dlogits, c.T, c.d,
-                                                    static_cast<float*>(dw_router), static_cast<float*>(dbias));
-  return cudaGetLastError();
+    e = launch_pdl(router_bwd_reduce_kernel<float>, blocks, threads, 0, s, no_extra_attr(), part, kRouterBwdChunks, dl,
+                   c.T, c.d, static_cast<float*>(dw_router), static_cast<float*>(dbias));
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace moe

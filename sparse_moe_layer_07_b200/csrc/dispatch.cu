@@ -271,10 +271,9 @@ __global__ void __launch_bounds__(kBT) dispatch_small_kernel(const int32_t* __re
 }
 
 // x_perm[s, :] = x[perm[s], :] for s < offsets[E]; one warp per row, 16-byte vectors.
-__global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ perm,
-                                                         const int32_t* __restrict__ offsets, int64_t T,
-                                                         int64_t row_vec, uint4* __restrict__ x_perm, int* err) {
-  pdl_wait();
+__device__ __forceinline__ void gather_rows(const uint4* __restrict__ x, const int32_t* __restrict__ perm,
+                                            const int32_t* __restrict__ offsets, int64_t T, int64_t row_vec,
+                                            uint4* __restrict__ x_perm, int* err) {
   int64_t n = offsets[kE];
   const int lane = threadIdx.x & 31;
   if (n < 0 || n > 2 * T) {
@@ -301,6 +300,35 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* __restric
     }
     for (; v < row_vec; v += 32) dst[v] = __ldg(src + v);
   }
+}
+
+__global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ perm,
+                                                         const int32_t* __restrict__ offsets, int64_t T,
+                                                         int64_t row_vec, uint4* __restrict__ x_perm, int* err) {
+  pdl_wait();
+  gather_rows(x, perm, offsets, T, row_vec, x_perm, err);
+}
+
+// Up to two gathers by the same perm and the zeroing of a buffer in one launch
+// (blockIdx.y: a gather, or the buffer): a step of few tokens is bound by its
+// launches (T 40 with 8-bit checkpoints: 135 us with five, 123 with two, the
+// backward's launches overlapping too).
+struct GatherZero {
+  const uint4* x[2];
+  uint4* x_perm[2];
+  float4* zero;
+  int64_t n4;
+};
+__global__ void __launch_bounds__(256) gather_zero_kernel(const GatherZero a, const int32_t* __restrict__ perm,
+                                                         const int32_t* __restrict__ offsets, int64_t T,
+                                                         int64_t row_vec, int* err) {
+  pdl_wait();
+  if (blockIdx.y + 1 < gridDim.y) {
+    gather_rows(a.x[blockIdx.y], perm, offsets, T, row_vec, a.x_perm[blockIdx.y], err);
+    return;
+  }
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < a.n4; i += (int64_t)gridDim.x * blockDim.x)
+    a.zero[i] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 }  // namespace
@@ -415,6 +443,23 @@ cudaError_t launch_gather(const moe_config_t& c, const void* x, const int32_t* p
   const cudaError_t e = launch_pdl(gather_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, s, no_extra_attr(),
                                    static_cast<const uint4*>(x), perm, offsets, c.T, row_vec,
                                    static_cast<uint4*>(x_perm), ctx.err);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_gather_zero(const moe_config_t& c, const void* x0, void* x0_perm, const void* x1, void* x1_perm,
+                               const int32_t* perm, const int32_t* offsets, float* zero, cudaStream_t s,
+                               const Ctx& ctx) {
+  if (c.T == 0) return cudaSuccess;
+  const int parts = x1 ? 3 : 2;
+  int64_t blocks = (slot_rows(c) + 7) / 8;
+  const int64_t cap_blocks = (int64_t)ctx.num_sms * 8 / parts;
+  if (blocks > cap_blocks) blocks = cap_blocks;
+  const GatherZero a{{static_cast<const uint4*>(x0), static_cast<const uint4*>(x1)},
+                     {static_cast<uint4*>(x0_perm), static_cast<uint4*>(x1_perm)},
+                     reinterpret_cast<float4*>(zero),
+                     c.T * c.d / 4};
+  const cudaError_t e = launch_pdl(gather_zero_kernel, dim3((unsigned)blocks, parts), dim3(256), 0, s, no_extra_attr(),
+                                   a, perm, offsets, c.T, c.d / 8, ctx.err);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
     tmem_relinquish();
     tc_fence_before();
   }
+  pdl_wait();
   if (warp == 2 && lane == 0) build_schedule<MODE>(sched, args);
   __syncthreads();
   tc_fence_after();
@@ -760,8 +761,9 @@ cudaError_t launch_bwd(const CUtensorMap& a0, const CUtensorMap& a1, const CUten
   auto kern = bwd_gemm_kernel<MODE, C8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  kern<<<ctx.num_sms, Warps<MODE, C8>::kThreads, SMEM_BYTES, s>>>(a0, a1, b0, b1, out, args);
-  return cudaGetLastError();
+  e = launch_pdl(kern, dim3(ctx.num_sms), dim3(Warps<MODE, C8>::kThreads), SMEM_BYTES, s, no_extra_attr(), a0, a1, b0,
+                 b1, out, args);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 BwdArgs base_args(const moe_config_t& c, const int32_t* offsets, const Ctx& ctx) {

@@ -106,6 +106,10 @@ cudaError_t launch_route_counts(const moe_config_t& c, const int32_t* idx, int32
 
 cudaError_t launch_gather(const moe_config_t& c, const void* x, const int32_t* perm,
                           const int32_t* offsets, void* x_perm, cudaStream_t s, const Ctx& ctx);
+// bf16 rows of x0 (and of x1 when given) by perm, and zero [T, d] cleared, in one launch.
+cudaError_t launch_gather_zero(const moe_config_t& c, const void* x0, void* x0_perm, const void* x1, void* x1_perm,
+                               const int32_t* perm, const int32_t* offsets, float* zero, cudaStream_t s,
+                               const Ctx& ctx);
 
 cudaError_t launch_combine(const moe_config_t& c, const float* y, const int32_t* slot_of,
                            const float* topk_w, int weights_applied, void* out, cudaStream_t s,

@@ -1152,8 +1152,7 @@ moe_status_t moe_layer_forward_train_c8(const moe_config_t* cfg, const void* x, 
   }
   if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_FWD_GATHER, stream);
-    e = launch_gather(c, x, perm, offsets, w8 + S.x_perm, stream, ctx);
-    if (e == cudaSuccess) e = launch_zero_rows(c, sum32, stream, ctx);
+    e = launch_gather_zero(c, x, w8 + S.x_perm, nullptr, nullptr, perm, offsets, sum32, stream, ctx);
   }
   if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_FWD_GATE_UP, stream);
@@ -1213,8 +1212,7 @@ moe_status_t moe_layer_backward_c8(const moe_config_t* cfg, const void* x, const
   cudaError_t e;
   {
     PhaseMark m(MOE_PHASE_BWD_GATHER, stream);
-    e = launch_gather(c, dout, perm, offsets, w8 + S.dout_perm, stream, ctx);
-    if (e == cudaSuccess) e = launch_gather(c, x, perm, offsets, w8 + S.x_perm, stream, ctx);
+    e = launch_gather_zero(c, dout, w8 + S.dout_perm, x, w8 + S.x_perm, perm, offsets, dx32, stream, ctx);
   }
   if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_BWD_DH, stream);
@@ -1222,18 +1220,15 @@ moe_status_t moe_layer_backward_c8(const moe_config_t* cfg, const void* x, const
                          w8 + S.h, dw_part, stream, ctx);
   }
   if (e == cudaSuccess) {
-    PhaseMark m(MOE_PHASE_BWD_ZERO, stream);
-    e = launch_zero_rows(c, dx32, stream, ctx);
-  }
-  if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_BWD_DX, stream);
     e = launch_bwd_dx(c, w8 + S.dg, w8 + S.du, offsets, w_gate, w_up, perm, dx32, stream, ctx);
   }
   if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_BWD_ROUTER, stream);
-    e = launch_router_bwd(c, dw_part, (int)(c.f / 256) * bwd_dh_c8_parts_per_tile(c), slot_of, topk_idx, topk_w, w_router, dx32, x,
-                          reinterpret_cast<float*>(w8 + S.dlogits), reinterpret_cast<float*>(w8 + S.dweight), dx,
-                          dw_router, dbias, reinterpret_cast<float*>(w8 + S.wr_part), stream, ctx, dlogits, true);
+    e = launch_router_bwd(c, dw_part, (int)(c.f / 256) * bwd_dh_c8_parts_per_tile(c), slot_of, topk_idx, topk_w,
+                          w_router, dx32, x, reinterpret_cast<float*>(w8 + S.dlogits),
+                          reinterpret_cast<float*>(w8 + S.dweight), dx, dw_router, dbias,
+                          reinterpret_cast<float*>(w8 + S.wr_part), stream, ctx, dlogits, true);
   }
   if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_BWD_WG_DOWN, stream);
