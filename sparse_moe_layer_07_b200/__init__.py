@@ -729,17 +729,18 @@ def balance_loss(cfg: Config, logits, topk_idx, token_mask=None, seq_offsets=Non
         if seq_offsets.dtype != torch.int32 or n_seq < 1:
             raise ValueError("seq_offsets must be int32 with at least two entries")
     o = dict(out) if out else {}
-    if "loss" not in o:
-        o["loss"] = _empty((3,), torch.float32, logits)
-    if "counts" not in o:
-        o["counts"] = _empty((n_seq, cfg.E), torch.int32, logits)
     if not want_grad:
         o["dlogits"] = None
-    elif "dlogits" not in o:
-        o["dlogits"] = _empty((cfg.T, cfg.E), torch.float32, logits)
-    _expect("loss", o["loss"], 3, torch.float32)
-    _expect("counts", o["counts"], n_seq * cfg.E, torch.int32)
-    _expect("dlogits", o["dlogits"], cfg.T * cfg.E, torch.float32)
+    for k, n, dt in (("loss", 3, torch.float32), ("counts", n_seq * cfg.E, torch.int32),
+                     ("dlogits", cfg.T * cfg.E, torch.float32)) if out else ():
+        _expect(k, o.get(k), n, dt)
+    if "loss" not in o:
+        o["loss"] = logits.new_empty((3,))
+    if "counts" not in o:
+        o["counts"] = topk_idx.new_empty((n_seq, cfg.E))
+    if "dlogits" not in o:
+        shape = (cfg.T, cfg.E)
+        o["dlogits"] = torch.empty_like(logits) if logits.shape == shape else logits.new_empty(shape)
     if ws is None:
         need = balance_loss_workspace_size(cfg, n_seq)
         ws = _empty((need,), torch.uint8, logits) if need else None
