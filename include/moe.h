@@ -559,6 +559,9 @@ MOE_API moe_status_t moe_balance_loss(const moe_config_t* cfg, const float* logi
  * moe_layer_forward_train and moe_layer_backward record a pair of CUDA events
  * on the call's stream around each of their kernels (events are created on
  * first use and reused; nothing is recorded while disabled, the default).
+ * moe_layer_forward_train_c8 and moe_layer_backward_c8 do the same, with the
+ * clearing of the sums in the GATHER phases and all three weight gradients, one
+ * launch, in WG_DOWN.
  * moe_profile_read waits for every recorded event, writes for each phase p < n
  * the summed milliseconds ms[p] and the number of calls calls[p] since the
  * previous read, and then forgets them.  ms and calls hold n entries (either

@@ -34,6 +34,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tc_ptx.cuh"
@@ -82,15 +84,18 @@ static_assert((3 * kStages + 5) * 8 + 12 <= 256, "barrier area");
 
 enum Mode { kDH = 0, kDX = 1, kWG = 2 };
 
+struct WgShape {           // dW [E, M, N]
+  int M, m_tiles, n_tiles; // M / BM, N / BN
+  int m_outer;             // tiles of one expert ordered M-block major
+};
+
 struct BwdArgs {
   const int32_t* offsets;  // [E + 1]
   int64_t rows_alloc;      // rows of the grouped buffers
   int n_tiles;             // N / BN (kDX: d / bn)
   int bn;                  // kDX: columns of a tile, 256 or 192
-  int m_tiles;             // kWG: M / BM
   int num_kb;              // kDH: d / BK;  kDX: 2 f / BK
   int half_kb;             // kDX: f / BK (first half dG x W_gate, second dU x W_up)
-  int m_outer;             // kWG: tiles of one expert ordered M-block major
   const int32_t* perm;     // kDX: token of each row
   int64_t n_tok;
   const float* row_scale;  // kDH
@@ -103,10 +108,19 @@ struct BwdArgs {
   __nv_bfloat16* dU;
   float* dw_part;          // kDH: [rows, n_tiles * parts per tile]
   float* out;              // kDX: dx32 [T, d];  kWG: dW [E, M, N]
-  int64_t ld;              // kDH: f;  kDX: d;  kWG: N
-  int64_t M;               // kWG
+  int64_t ld;              // kDH: f;  kDX: d
+  WgShape wg[3];           // kWG: C8 all three products, else the first
   int* err;
 };
+
+// kWG, C8: operands and outputs of the second and third product beside tmA0 x
+// tmB0 -> tmOut and tmA1 x tmB1.
+struct WgMaps {
+  CUtensorMap b2, out1, out2;
+};
+struct NoMaps {};
+template <int MODE, int C8>
+using MoreMaps = std::conditional_t<MODE == kWG && C8 != 0, WgMaps, NoMaps>;
 
 struct Sched {
   int offs[kE + 1];
@@ -116,12 +130,18 @@ struct Sched {
 
 struct Tile {
   int e, m0, rows, n0, nb;
+  int part;                // kWG, C8: which of the three products
   int row0, nrows, nkb;    // kWG: the expert's grouped rows and K blocks
 };
 
-template <int MODE>
+template <int MODE, int C8>
 __device__ __forceinline__ Tile decode_tile(const Sched& s, const BwdArgs& a, int L) {
   Tile t;
+  t.part = 0;
+  if (MODE == kWG && C8) {  // the products have the same number of tiles
+    t.part = (L >= s.prefix[kE]) + (L >= 2 * s.prefix[kE]);
+    L -= t.part * s.prefix[kE];
+  }
   int e = 0;
 #pragma unroll
   for (int k = 1; k < kE; ++k)
@@ -131,13 +151,14 @@ __device__ __forceinline__ Tile decode_tile(const Sched& s, const BwdArgs& a, in
   t.row0 = s.offs[e];
   t.nrows = s.offs[e + 1] - s.offs[e];
   if (MODE == kWG) {
+    const WgShape& w = a.wg[t.part];
     int mb, nb;
-    if (a.m_outer) {
-      mb = local / a.n_tiles;
-      nb = local - mb * a.n_tiles;
+    if (w.m_outer) {
+      mb = local / w.n_tiles;
+      nb = local - mb * w.n_tiles;
     } else {
-      nb = local / a.m_tiles;
-      mb = local - nb * a.m_tiles;
+      nb = local / w.m_tiles;
+      mb = local - nb * w.m_tiles;
     }
     t.m0 = mb * BM;
     t.rows = BM;
@@ -176,7 +197,7 @@ __device__ __forceinline__ void build_schedule(Sched& sched, const BwdArgs& args
     sched.mt[k] = (n + BM - 1) / BM;
     sched.prefix[k] = acc;
     // weight gradients: every expert owns its M x N tiles (zero when it has no rows)
-    acc += MODE == kWG ? (ok ? args.m_tiles * args.n_tiles : 0) : sched.mt[k] * args.n_tiles;
+    acc += MODE == kWG ? (ok ? args.wg[0].m_tiles * args.wg[0].n_tiles : 0) : sched.mt[k] * args.n_tiles;
   }
   sched.prefix[kE] = acc;
   if (!ok) flag_error(args.err, MOE_DEVERR_OFFSETS);
@@ -196,7 +217,8 @@ template <int MODE, int C8>
 __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
     bwd_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
-                    const __grid_constant__ CUtensorMap tmOut, const BwdArgs args) {
+                    const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ MoreMaps<MODE, C8> more,
+                    const BwdArgs args) {
   constexpr int S = kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -254,7 +276,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int total = sched.prefix[kE];
+  const int total = sched.prefix[kE] * (MODE == kWG && C8 ? 3 : 1);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -263,7 +285,14 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
       bool ok = true;
       const uint64_t keep = policy_evict_last();
       for (int L = blockIdx.x; L < total && ok; L += gridDim.x) {
-        const Tile t = decode_tile<MODE>(sched, args, L);
+        const Tile t = decode_tile<MODE, C8>(sched, args, L);
+        const CUtensorMap *mA = &tmA0, *mB = &tmB0;  // kWG
+        if constexpr (MODE == kWG && C8 != 0) {
+          if (t.part) {
+            mA = &tmA1;
+            mB = t.part == 1 ? &tmB1 : &more.b2;
+          }
+        }
         for (int kb = 0; kb < t.nkb; ++kb, ++it) {
           const int s = it % S;
           const uint32_t ph = (it / S) & 1u;
@@ -288,8 +317,8 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
                 tma_load_3d_hint(b + c * CHUNK, first ? &tmB0 : &tmB1, &full[s], k0, t.n0 + 64 * c, t.e, keep);
           } else {
             const int r0 = t.row0 + kb * BK;
-            tma_load_3d_hint(a, &tmA0, &full[s], 0, r0, t.m0 / 64, keep);
-            tma_load_3d_hint(b, &tmB0, &full[s], 0, r0, t.n0 / 64, keep);
+            tma_load_3d_hint(a, mA, &full[s], 0, r0, t.m0 / 64, keep);
+            tma_load_3d_hint(b, mB, &full[s], 0, r0, t.n0 / 64, keep);
             *issued_kb = it + 1;
           }
         }
@@ -314,7 +343,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
       uint32_t it = 0, tc = 0, zphase = 0;  // zphase: parity bit per stage of `zeroed`
       bool ok = true, issued = false;
       for (int L = blockIdx.x; L < total && ok; L += gridDim.x, ++tc) {
-        const Tile t = decode_tile<MODE>(sched, args, L);
+        const Tile t = decode_tile<MODE, C8>(sched, args, L);
         // a row block of at most 64 rows (an expert's last) runs M = 64 MMAs
         const uint32_t idesc = (MODE != kWG && t.rows <= 64) ? IDESC_M64 : IDESC;
         const uint32_t buf = tc & 1u;
@@ -398,7 +427,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
     // lane waits for the stage itself, so its stores follow the TMA's.
     uint32_t it = 0;
     for (int L = blockIdx.x; L < total; L += gridDim.x) {
-      const Tile t = decode_tile<MODE>(sched, args, L);
+      const Tile t = decode_tile<MODE, C8>(sched, args, L);
       const uint32_t it_last = it + (uint32_t)t.nkb - 1u;
       it += (uint32_t)t.nkb;
       if (t.nkb == 0) continue;
@@ -443,7 +472,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
     const int c_begin = half * (BN / 32) / kSplit, c_end = c_begin + (BN / 32) / kSplit;
     uint32_t tc = 0;
     for (int L = blockIdx.x; L < total; L += gridDim.x, ++tc) {
-      const Tile t = decode_tile<MODE>(sched, args, L);
+      const Tile t = decode_tile<MODE, C8>(sched, args, L);
       const uint32_t buf = tc & 1u;
       const uint32_t tph = (tc >> 1) & 1u;
       // tile row of this thread; M = 64 accumulators hold row 16 q + i in lane i (< 16) of quarter q
@@ -682,11 +711,12 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
                                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
           }
         }
-      } else if (C8) {
+      } else if constexpr (C8 != 0 && MODE == kWG) {
         // as below with 32 rows x 64 bf16 columns (128 bytes) per store
+        const CUtensorMap* mOut = t.part == 0 ? &tmOut : (t.part == 1 ? &more.out1 : &more.out2);
         const bool zero = t.nkb == 0;
         uint8_t* stage0 = sOut + (q * 2) * OUT_STAGE;
-        const int y = t.e * (int)args.M + t.m0 + q * 32;
+        const int y = t.e * args.wg[t.part].M + t.m0 + q * 32;
 #pragma unroll 1
         for (int c = 0; c < BN / 64; ++c) {
           uint32_t v[32], v2[32];
@@ -709,7 +739,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&tmOut, st, t.n0 + c * 64, y);
+            tma_store_2d(mOut, st, t.n0 + c * 64, y);
             bulk_commit_group();
           }
         }
@@ -718,7 +748,7 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
         // placed with the 128-byte swizzle (piece j of row r at j ^ (r % 8))
         const bool zero = t.nkb == 0;
         uint8_t* stage0 = sOut + (q * 2) * OUT_STAGE;
-        const int y = t.e * (int)args.M + t.m0 + q * 32;
+        const int y = t.e * args.wg[t.part].M + t.m0 + q * 32;
 #pragma unroll 1
         for (int c = 0; c < BN / 32; ++c) {
           uint32_t v[32];
@@ -757,12 +787,13 @@ __global__ void __launch_bounds__(Warps<MODE, C8>::kThreads, 1)
 
 template <int MODE, int C8 = 0>
 cudaError_t launch_bwd(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0, const CUtensorMap& b1,
-                       const CUtensorMap& out, const BwdArgs& args, cudaStream_t s, const Ctx& ctx) {
+                       const CUtensorMap& out, const BwdArgs& args, cudaStream_t s, const Ctx& ctx,
+                       const MoreMaps<MODE, C8>& more = {}) {
   auto kern = bwd_gemm_kernel<MODE, C8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(ctx.num_sms), dim3(Warps<MODE, C8>::kThreads), SMEM_BYTES, s, no_extra_attr(), a0, a1, b0,
-                 b1, out, args);
+                 b1, out, more, args);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -870,41 +901,61 @@ cudaError_t launch_bwd_dx(const moe_config_t& c, const void* dG, const void* dU,
   return launch_bwd<kDX>(ta0, ta1, tb0, tb1, ta0, a, s, ctx);
 }
 
+namespace {
+
+// Rows [rows, C] viewed as [C / 64 chunks][rows][64]: one box = `chunks` chunks of 64 x 64.
+bool map_chunks(CUtensorMap* m, const void* base, int64_t rows, int64_t C, uint32_t chunks) {
+  const uint64_t dims[3] = {64, (uint64_t)rows, (uint64_t)(C / 64)};
+  const uint64_t str[2] = {(uint64_t)C * 2, 128};
+  const uint32_t box[3] = {64, 64, chunks};
+  return encode_tmap(m, base, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// dW [E * M, N] stored 32 rows x 128 bytes at a time from the swizzled staging tiles
+bool map_dw(CUtensorMap* m, const void* dW, int64_t rows, int64_t N, bool bf16) {
+  const uint32_t esz = bf16 ? 2 : 4;
+  const uint64_t dims[2] = {(uint64_t)N, (uint64_t)rows};
+  const uint64_t str[1] = {(uint64_t)N * esz};
+  const uint32_t box[2] = {128 / esz, 32};
+  return encode_tmap_dtype(m, dW, 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                           bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
+}
+
+WgShape wg_shape(int64_t M, int64_t N, bool m_outer) {
+  return {(int)M, (int)(M / BM), (int)(N / BN), m_outer ? 1 : 0};
+}
+
+}  // namespace
+
 cudaError_t launch_bwd_wgrad(const moe_config_t& c, const void* a_rows, int64_t M, const void* b_rows, int64_t N,
-                             const int32_t* offsets, void* dW, bool m_outer, cudaStream_t s, const Ctx& ctx,
-                             bool bf16_out) {
+                             const int32_t* offsets, float* dW, bool m_outer, cudaStream_t s, const Ctx& ctx) {
   const int64_t rows = slot_rows(c);
   if (rows == 0 || M % BM != 0 || N % BN != 0) return rows == 0 ? cudaSuccess : cudaErrorInvalidValue;
   CUtensorMap ta, tb, to;
-  {
-    // [rows, C] viewed as [C / 64 chunks][rows][64]: one box = nch chunks of 64 x 64
-    const uint64_t a_dims[3] = {64, (uint64_t)rows, (uint64_t)(M / 64)};
-    const uint64_t a_str[2] = {(uint64_t)M * 2, 128};
-    const uint32_t a_box[3] = {64, 64, 2};
-    const uint64_t b_dims[3] = {64, (uint64_t)rows, (uint64_t)(N / 64)};
-    const uint64_t b_str[2] = {(uint64_t)N * 2, 128};
-    const uint32_t b_box[3] = {64, 64, 4};
-    if (!encode_tmap(&ta, a_rows, 3, a_dims, a_str, a_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_tmap(&tb, b_rows, 3, b_dims, b_str, b_box, CU_TENSOR_MAP_SWIZZLE_128B))
-      return cudaErrorInvalidValue;
-  }
-  // dW [E * M, N] stored 32 rows x 128 bytes at a time from the swizzled staging tiles
-  const uint32_t esz = bf16_out ? 2 : 4;
-  const uint64_t o_dims[2] = {(uint64_t)N, (uint64_t)c.E * M};
-  const uint64_t o_str[1] = {(uint64_t)N * esz};
-  const uint32_t o_box[2] = {128 / esz, 32};
-  if (!encode_tmap_dtype(&to, dW, 2, o_dims, o_str, o_box, CU_TENSOR_MAP_SWIZZLE_128B,
-                         bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
+  if (!map_chunks(&ta, a_rows, rows, M, 2) || !map_chunks(&tb, b_rows, rows, N, 4) || !map_dw(&to, dW, c.E * M, N, false))
     return cudaErrorInvalidValue;
   BwdArgs a = base_args(c, offsets, ctx);
-  a.m_tiles = (int)(M / BM);
-  a.n_tiles = (int)(N / BN);
-  a.m_outer = m_outer ? 1 : 0;
-  a.ld = N;
-  a.M = M;
-  if (bf16_out) return launch_bwd<kWG, 4>(ta, ta, tb, tb, to, a, s, ctx);
-  a.out = static_cast<float*>(dW);
+  a.wg[0] = wg_shape(M, N, m_outer);
+  a.out = dW;
   return launch_bwd<kWG>(ta, ta, tb, tb, to, a, s, ctx);
+}
+
+cudaError_t launch_bwd_wgrads_c8(const moe_config_t& c, const void* hw, const void* dout_perm, const void* x_perm,
+                                 const void* dG, const void* dU, const int32_t* offsets, void* dw_down, void* dw_gate,
+                                 void* dw_up, cudaStream_t s, const Ctx& ctx) {
+  const int64_t rows = slot_rows(c);
+  if (rows == 0 || c.d % BN != 0 || c.f % BN != 0) return rows == 0 ? cudaSuccess : cudaErrorInvalidValue;
+  CUtensorMap ta0, ta1, tb0, tb1, to;
+  WgMaps more;
+  if (!map_chunks(&ta0, hw, rows, c.f, 2) || !map_chunks(&tb0, dout_perm, rows, c.d, 4) ||
+      !map_dw(&to, dw_down, c.E * c.f, c.d, true) || !map_chunks(&ta1, x_perm, rows, c.d, 2) ||
+      !map_chunks(&tb1, dG, rows, c.f, 4) || !map_chunks(&more.b2, dU, rows, c.f, 4) ||
+      !map_dw(&more.out1, dw_gate, c.E * c.d, c.f, true) || !map_dw(&more.out2, dw_up, c.E * c.d, c.f, true))
+    return cudaErrorInvalidValue;
+  BwdArgs a = base_args(c, offsets, ctx);
+  a.wg[0] = wg_shape(c.f, c.d, c.f >= c.d);
+  a.wg[1] = a.wg[2] = wg_shape(c.d, c.f, c.d >= c.f);
+  return launch_bwd<kWG, 4>(ta0, ta1, tb0, tb1, to, a, s, ctx, more);
 }
 
 }  // namespace moe

@@ -183,8 +183,12 @@ cudaError_t launch_bwd_dx(const moe_config_t& c, const void* dG, const void* dU,
                           const void* wg, const void* wu, const int32_t* perm, float* dx32, cudaStream_t s,
                           const Ctx& ctx);
 cudaError_t launch_bwd_wgrad(const moe_config_t& c, const void* a_rows, int64_t M, const void* b_rows, int64_t N,
-                             const int32_t* offsets, void* dW, bool m_outer, cudaStream_t s, const Ctx& ctx,
-                             bool bf16_out = false);
+                             const int32_t* offsets, float* dW, bool m_outer, cudaStream_t s, const Ctx& ctx);
+// dW_down = hw^T dout, dW_gate = x^T dG, dW_up = x^T dU over each expert's rows, bf16, in
+// one launch (T 40 step 123 -> 117 us; at Grok size 52.2 -> 52.4 ms, the spread of runs).
+cudaError_t launch_bwd_wgrads_c8(const moe_config_t& c, const void* hw, const void* dout_perm, const void* x_perm,
+                                 const void* dG, const void* dU, const int32_t* offsets, void* dw_down, void* dw_gate,
+                                 void* dw_up, cudaStream_t s, const Ctx& ctx);
 // dout_perm[r] = dout[perm[r]],  dy_perm[r] = bf16(row_scale[r] * dout[perm[r]])  (r < offsets[E])
 cudaError_t launch_bwd_gather(const moe_config_t& c, const void* dout, const int32_t* perm, const int32_t* offsets,
                               const float* row_scale, void* dout_perm, void* dy_perm, cudaStream_t s, const Ctx& ctx);

@@ -1232,15 +1232,8 @@ moe_status_t moe_layer_backward_c8(const moe_config_t* cfg, const void* x, const
   }
   if (e == cudaSuccess) {
     PhaseMark m(MOE_PHASE_BWD_WG_DOWN, stream);
-    e = launch_bwd_wgrad(c, w8 + S.h, c.f, w8 + S.dout_perm, c.d, offsets, dw_down, c.f >= c.d, stream, ctx, true);
-  }
-  if (e == cudaSuccess) {
-    PhaseMark m(MOE_PHASE_BWD_WG_GATE, stream);
-    e = launch_bwd_wgrad(c, w8 + S.x_perm, c.d, w8 + S.dg, c.f, offsets, dw_gate, c.d >= c.f, stream, ctx, true);
-  }
-  if (e == cudaSuccess) {
-    PhaseMark m(MOE_PHASE_BWD_WG_UP, stream);
-    e = launch_bwd_wgrad(c, w8 + S.x_perm, c.d, w8 + S.du, c.f, offsets, dw_up, c.d >= c.f, stream, ctx, true);
+    e = launch_bwd_wgrads_c8(c, w8 + S.h, w8 + S.dout_perm, w8 + S.x_perm, w8 + S.dg, w8 + S.du, offsets, dw_down,
+                             dw_gate, dw_up, stream, ctx);
   }
   return cuda_status(e);
 }
