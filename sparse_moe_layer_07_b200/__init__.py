@@ -14,6 +14,7 @@ from __future__ import annotations
 import collections.abc
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -234,6 +235,11 @@ def _expect_layer(cfg, x=None, w_router=None, w_gate=None, w_up=None, w_down=Non
 
 def _empty(shape, dtype, like):
     return like.new_empty(shape, dtype=dtype)
+
+
+def _empty_like(like, shape):
+    """Uninitialised tensor of the type of `like` (empty_like is the cheaper call)."""
+    return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
 
 
 _HERE = contextlib.nullcontext()
@@ -599,24 +605,33 @@ def layer_backward(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ws, gra
     return g
 
 
-class _Views(collections.abc.Mapping):
-    """Named views of consecutive 256-byte aligned parts (name, dtype, shape) of a buffer, made when asked for."""
+def _parts(spec):
+    """Byte offset, type, shape and strides of the consecutive 256-byte aligned parts (name, dtype, shape) of a
+    buffer, the last dimension in bytes, and the bytes that they take."""
+    at, o = {}, 0
+    for name, dt, shape in spec:
+        size = (*shape[:-1], shape[-1] * dt.itemsize)
+        at[name] = (o, dt, size, tuple(math.prod(size[i + 1:]) for i in range(len(size))))
+        o += _round256(math.prod(size))
+    return at, o
 
-    def __init__(self, buf, spec):
+
+class _Views(collections.abc.Mapping):
+    """Named views of the parts (``_parts``) of a buffer, made when asked for."""
+
+    def __init__(self, buf, parts):
         self._flat = buf.view(torch.uint8).view(-1)
-        self._at, self._made, o = {}, {}, 0
-        for name, dt, shape in spec:
-            nbytes = math.prod(shape) * dt.itemsize
-            self._at[name] = (o, nbytes, dt, shape)
-            o += _round256(nbytes)
-        if o > self._flat.numel():
-            raise ValueError(f"the buffer holds {self._flat.numel()} bytes, its parts take {o}")
+        self._at, need = parts
+        self._made = {}
+        if need > self._flat.numel():
+            raise ValueError(f"the buffer holds {self._flat.numel()} bytes, its parts take {need}")
 
     def __getitem__(self, name):
         v = self._made.get(name)
         if v is None:
-            o, nbytes, dt, shape = self._at[name]
-            v = self._made[name] = self._flat[o:o + nbytes].view(dt).view(shape)
+            o, dt, size, strides = self._at[name]
+            v = self._flat.as_strided(size, strides, self._flat.storage_offset() + o).view(dt)
+            self._made[name] = v
         return v
 
     def __iter__(self):
@@ -634,17 +649,21 @@ def workspace_size_train_c8(cfg: Config) -> int:
     return lib.moe_workspace_size_train_c8(cfg.ref)
 
 
+@functools.lru_cache(maxsize=64)
+def _checkpoint_parts(T, E, f):
+    rows, i32, f32 = 2 * T, torch.int32, torch.float32
+    return _parts([("topk_idx", i32, (T, 2)), ("topk_w", f32, (T, 2)), ("logits", f32, (T, E)),
+                   ("route", i32, (3 * E + 1,)), ("perm", i32, (rows,)), ("slot_of", i32, (T, 2)),
+                   ("row_scale", f32, (rows,)), ("g_codes", torch.int8, (rows, f)),
+                   ("u_codes", torch.int8, (rows, f)), ("g_scale", torch.bfloat16, (rows, f // 32)),
+                   ("u_scale", torch.bfloat16, (rows, f // 32))])
+
+
 def checkpoint_views_c8(cfg: Config, ckpt):
     """Named views into a checkpoint of layer_forward_train_c8 (layout stated in include/moe.h): the routing
     (topk_idx and logits are what balance_loss takes; route holds counts_raw [E], counts_kept [E] and offsets
     [E + 1]) and the 8-bit codes with their scales."""
-    T, E, f, rows = cfg.T, cfg.E, cfg.f, cfg.T * cfg.top_k
-    i32, f32 = torch.int32, torch.float32
-    return _Views(ckpt, [("topk_idx", i32, (T, 2)), ("topk_w", f32, (T, 2)), ("logits", f32, (T, E)),
-                         ("route", i32, (3 * E + 1,)), ("perm", i32, (rows,)), ("slot_of", i32, (T, 2)),
-                         ("row_scale", f32, (rows,)), ("g_codes", torch.int8, (rows, f)),
-                         ("u_codes", torch.int8, (rows, f)), ("g_scale", torch.bfloat16, (rows, f // 32)),
-                         ("u_scale", torch.bfloat16, (rows, f // 32))])
+    return _Views(ckpt, _checkpoint_parts(cfg.T, cfg.E, cfg.f))
 
 
 def _nbytes(t):
@@ -657,7 +676,7 @@ def layer_forward_train_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, ckpt,
     (workspace_size_train_c8 bytes) is scratch that every layer of a model can share."""
     _expect_layer(cfg, x, w_router, w_gate, w_up, w_down, logit_bias, out)
     if out is None:
-        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x)
+        out = _empty_like(x, (cfg.T, cfg.d))
     with _same_device(x, w_router, w_gate, w_up, w_down, ckpt, ws, logit_bias, out):
         _check(lib.moe_layer_forward_train_c8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias),
                                               _dev_ptr(w_gate), _dev_ptr(w_up), _dev_ptr(w_down), _dev_ptr(out),
@@ -680,10 +699,12 @@ def layer_backward_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ckpt
     g = dict(grads or {})
     if not want_dbias:
         g["dbias"] = None
+    like = {"dx": x, "dw_router": w_router, "dbias": w_router, "dw_gate": w_gate, "dw_up": w_up, "dw_down": w_down}
     for k, shape in shapes.items():
-        if k not in g:
-            g[k] = _empty(shape, dt, x)
-        _expect(k, g[k], math.prod(shape), dt)
+        if k in g:
+            _expect(k, g[k], math.prod(shape), dt)
+        else:
+            g[k] = _empty_like(like[k], shape)
     with _same_device(x, w_router, w_gate, w_up, w_down, dout, ckpt, ws, dlogits, *g.values()):
         _check(lib.moe_layer_backward_c8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(w_gate), _dev_ptr(w_up),
                                          _dev_ptr(w_down), _dev_ptr(dout), _dev_ptr(dlogits), _dev_ptr(g["dx"]),
@@ -739,8 +760,7 @@ def balance_loss(cfg: Config, logits, topk_idx, token_mask=None, seq_offsets=Non
     if "counts" not in o:
         o["counts"] = topk_idx.new_empty((n_seq, cfg.E))
     if "dlogits" not in o:
-        shape = (cfg.T, cfg.E)
-        o["dlogits"] = torch.empty_like(logits) if logits.shape == shape else logits.new_empty(shape)
+        o["dlogits"] = _empty_like(logits, (cfg.T, cfg.E))
     if ws is None:
         need = balance_loss_workspace_size(cfg, n_seq)
         ws = _empty((need,), torch.uint8, logits) if need else None
@@ -894,7 +914,7 @@ def mx4_workspace_views(cfg: Config, ws):
     R = rows // 128 + cfg.E
     spec = [("x_codes", (rows, d)), ("x_scales", (R, d // 128, 512)), ("h_codes", (rows, f)),
             ("h_scales", (R, f // 128, 512))]
-    return _Views(ws, [(name, torch.uint8, shape) for name, shape in spec])
+    return _Views(ws, _parts([(name, torch.uint8, shape) for name, shape in spec]))
 
 
 def expert_ffn_mx4(cfg: Config, x_perm, offsets, qw: MxExperts, row_scale=None, y=None, ws=None, stream=None):
@@ -926,7 +946,7 @@ def layer_forward_mx4(cfg: Config, x, w_router, qw: MxExperts, logit_bias=None, 
     _expect_layer(cfg, x=x, w_router=w_router, logit_bias=logit_bias, out=out)
     qw.check(cfg)
     if out is None:
-        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x)
+        out = _empty_like(x, (cfg.T, cfg.d))
     if ws is None:
         ws = _empty((max(workspace_size_mx4(cfg), 1),), torch.uint8, x)
     _expect("stats", stats, 3 * cfg.E + 2, torch.int32)
