@@ -249,6 +249,8 @@ def _same_device(first, *others):
     """Tensors of one call live on one CUDA device (None is allowed among the others): the context in which that
     device is current."""
     i = first.get_device()
+    if i < 0:
+        raise ValueError("expected a CUDA tensor")
     for t in others:
         if t is not None and t.get_device() != i:
             raise ValueError(f"tensors on {first.device} and {t.device} in one call")
@@ -678,9 +680,9 @@ def layer_forward_train_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, ckpt,
     if out is None:
         out = _empty_like(x, (cfg.T, cfg.d))
     with _same_device(x, w_router, w_gate, w_up, w_down, ckpt, ws, logit_bias, out):
-        _check(lib.moe_layer_forward_train_c8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias),
-                                              _dev_ptr(w_gate), _dev_ptr(w_up), _dev_ptr(w_down), _dev_ptr(out),
-                                              _dev_ptr(ckpt), _nbytes(ckpt), _dev_ptr(ws), _nbytes(ws),
+        _check(lib.moe_layer_forward_train_c8(cfg.ref, _ptr(x), _ptr(w_router), _ptr(logit_bias),
+                                              _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out),
+                                              _ptr(ckpt), _nbytes(ckpt), _ptr(ws), _nbytes(ws),
                                               _stream(stream, x.device)), "moe_layer_forward_train_c8")
     return out
 
@@ -706,11 +708,11 @@ def layer_backward_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ckpt
         else:
             g[k] = _empty_like(like[k], shape)
     with _same_device(x, w_router, w_gate, w_up, w_down, dout, ckpt, ws, dlogits, *g.values()):
-        _check(lib.moe_layer_backward_c8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(w_gate), _dev_ptr(w_up),
-                                         _dev_ptr(w_down), _dev_ptr(dout), _dev_ptr(dlogits), _dev_ptr(g["dx"]),
-                                         _dev_ptr(g["dw_router"]), _dev_ptr(g["dbias"]), _dev_ptr(g["dw_gate"]),
-                                         _dev_ptr(g["dw_up"]), _dev_ptr(g["dw_down"]), _dev_ptr(ckpt), _nbytes(ckpt),
-                                         _dev_ptr(ws), _nbytes(ws), _stream(stream, x.device)),
+        _check(lib.moe_layer_backward_c8(cfg.ref, _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up),
+                                         _ptr(w_down), _ptr(dout), _ptr(dlogits), _ptr(g["dx"]),
+                                         _ptr(g["dw_router"]), _ptr(g["dbias"]), _ptr(g["dw_gate"]),
+                                         _ptr(g["dw_up"]), _ptr(g["dw_down"]), _ptr(ckpt), _nbytes(ckpt),
+                                         _ptr(ws), _nbytes(ws), _stream(stream, x.device)),
                "moe_layer_backward_c8")
     return g
 
@@ -765,9 +767,9 @@ def balance_loss(cfg: Config, logits, topk_idx, token_mask=None, seq_offsets=Non
         need = balance_loss_workspace_size(cfg, n_seq)
         ws = _empty((need,), torch.uint8, logits) if need else None
     with _same_device(logits, topk_idx, token_mask, seq_offsets, ws, *o.values()):
-        _check(lib.moe_balance_loss(cfg.ref, _dev_ptr(logits), _dev_ptr(topk_idx), _dev_ptr(token_mask),
-                                    _dev_ptr(seq_offsets), n_seq, float(balance_coef), float(z_coef),
-                                    _dev_ptr(o["counts"]), _dev_ptr(o["loss"]), _dev_ptr(o["dlogits"]), _dev_ptr(ws),
+        _check(lib.moe_balance_loss(cfg.ref, _ptr(logits), _ptr(topk_idx), _ptr(token_mask),
+                                    _ptr(seq_offsets), n_seq, float(balance_coef), float(z_coef),
+                                    _ptr(o["counts"]), _ptr(o["loss"]), _ptr(o["dlogits"]), _ptr(ws),
                                     0 if ws is None else _nbytes(ws), _stream(stream, logits.device)),
                "moe_balance_loss")
     return o
@@ -849,7 +851,7 @@ def quantize_mx4(cfg: Config, w, codes=None, scales=None, stream=None):
     _expect("codes", codes, E * N * (K // 2), torch.uint8)
     _expect("scales", scales, E * (N // 128) * (K // 128) * 512, torch.uint8)
     with _same_device(w, codes, scales):
-        _check(lib.moe_quantize_mx4(cfg.ref, _dev_ptr(w), K, N, _dev_ptr(codes), _dev_ptr(scales),
+        _check(lib.moe_quantize_mx4(cfg.ref, _ptr(w), K, N, _ptr(codes), _ptr(scales),
                                     _stream(stream, w.device)), "moe_quantize_mx4")
     return codes, scales
 
@@ -870,7 +872,7 @@ def dequantize_mx4(cfg: Config, codes, scales, out=None, stream=None):
         out = _empty((cfg.E, K, N), torch.bfloat16, codes)
     _expect("out", out, cfg.E * K * N, torch.bfloat16)
     with _same_device(codes, scales, out):
-        _check(lib.moe_dequantize_mx4(cfg.ref, _dev_ptr(codes), _dev_ptr(scales), K, N, _dev_ptr(out),
+        _check(lib.moe_dequantize_mx4(cfg.ref, _ptr(codes), _ptr(scales), K, N, _ptr(out),
                                       _stream(stream, codes.device)), "moe_dequantize_mx4")
     return out
 
@@ -900,7 +902,7 @@ class MxExperts:
                 raise ValueError(f"{name} weights are [K, N] = {list(_mx4_shape(cfg, c, s))}, the layer needs {list(kn)}")
 
     def ptrs(self):
-        return [_dev_ptr(t) for t in self.tensors()]
+        return [_ptr(t) for t in self.tensors()]
 
 
 def expert_ffn_mx4_workspace_size(cfg: Config) -> int:
@@ -930,8 +932,8 @@ def expert_ffn_mx4(cfg: Config, x_perm, offsets, qw: MxExperts, row_scale=None, 
     _expect("row_scale", row_scale, rows, torch.float32)
     _expect("y", y, rows * cfg.d, torch.float32)
     with _same_device(x_perm, offsets, row_scale, y, ws, *qw.tensors()):
-        _check(lib.moe_expert_ffn_mx4(cfg.ref, _dev_ptr(x_perm), _dev_ptr(offsets), *qw.ptrs(), _dev_ptr(row_scale),
-                                      _dev_ptr(y), _dev_ptr(ws), _nbytes(ws), _stream(stream, x_perm.device)),
+        _check(lib.moe_expert_ffn_mx4(cfg.ref, _ptr(x_perm), _ptr(offsets), *qw.ptrs(), _ptr(row_scale),
+                                      _ptr(y), _ptr(ws), _nbytes(ws), _stream(stream, x_perm.device)),
                "moe_expert_ffn_mx4")
     return y
 
@@ -951,8 +953,8 @@ def layer_forward_mx4(cfg: Config, x, w_router, qw: MxExperts, logit_bias=None, 
         ws = _empty((max(workspace_size_mx4(cfg), 1),), torch.uint8, x)
     _expect("stats", stats, 3 * cfg.E + 2, torch.int32)
     with _same_device(x, w_router, logit_bias, out, stats, ws, *qw.tensors()):
-        _check(lib.moe_layer_forward_mx4(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias), *qw.ptrs(),
-                                         _dev_ptr(out), _dev_ptr(stats), _dev_ptr(ws), _nbytes(ws),
+        _check(lib.moe_layer_forward_mx4(cfg.ref, _ptr(x), _ptr(w_router), _ptr(logit_bias), *qw.ptrs(),
+                                         _ptr(out), _ptr(stats), _ptr(ws), _nbytes(ws),
                                          _stream(stream, x.device)), "moe_layer_forward_mx4")
     return out
 
