@@ -743,9 +743,7 @@ def balance_loss(cfg: Config, logits, topk_idx, token_mask=None, seq_offsets=Non
     _expect("logits", logits, cfg.T * cfg.E, torch.float32)
     _expect("topk_idx", topk_idx, cfg.T * cfg.top_k, torch.int32)
     if token_mask is not None:
-        if token_mask.dtype == torch.bool:
-            token_mask = token_mask.view(torch.uint8)
-        _expect("token_mask", token_mask, cfg.T, torch.uint8)
+        _expect("token_mask", token_mask, cfg.T, torch.bool if token_mask.dtype == torch.bool else torch.uint8)
     n_seq = 1
     if seq_offsets is not None:
         n_seq = seq_offsets.numel() - 1
