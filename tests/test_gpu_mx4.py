@@ -273,6 +273,23 @@ def test_replays_from_a_graph(T, cf):
     assert moe.get_device_error() == 0
 
 
+def test_offsets_past_32_bits():
+    """140000 rows of 32768 columns of H, more than 2^32 codes: the last tokens' outputs are those of a batch of them."""
+    T, n, d, f = 70000, 600, 256, 32768
+    gen = torch.Generator(device="cuda").manual_seed(12)
+
+    def normal_(*shape, std=1.0):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(std=std, generator=gen)
+
+    x, wr = normal_(T, d), normal_(8, d, std=d ** -0.5)
+    c = moe.Config(T, d, f, capacity_factor=4.0)
+    qw = moe.MxExperts(c, normal_(8, d, f, std=d ** -0.5), normal_(8, d, f, std=d ** -0.5), normal_(8, f, d, std=f ** -0.5))
+    out = moe.layer_forward_mx4(c, x, wr, qw)
+    last = moe.layer_forward_mx4(moe.Config(n, d, f, capacity_factor=4.0), x[T - n:], wr, qw)
+    assert torch.equal(out[T - n:], last)
+    assert moe.get_device_error() == 0
+
+
 def test_batches_on_several_streams_at_once():
     """One set of weights, a batch and a scratch for each stream: one token, decode, and both sizes of row tiles."""
     L = LayerInputs(configs.scaled(W["mid_bf16"], name="mx_streams", T=700, d=256, f=384, capacity_factor=4.0))

@@ -287,6 +287,39 @@ def test_two_steps_on_two_streams_at_once():
     assert moe.get_device_error() == 0
 
 
+def test_offsets_past_32_bits():
+    """140000 rows of 32768 columns: more than 2^32 codes and values.  A token's output and dx depend on its own row
+    alone, so the last tokens' equal those of a batch of them, and the rest's weight gradients add up."""
+    T, n, d, f = 70000, 600, 256, 32768
+    gen = torch.Generator(device="cuda").manual_seed(11)
+
+    def normal_(*shape, std=1.0):
+        return torch.empty(shape, dtype=torch.bfloat16, device="cuda").normal_(std=std, generator=gen)
+
+    x, dout = normal_(T, d), normal_(T, d)
+    weights = (normal_(8, d, std=d ** -0.5), normal_(8, d, f, std=d ** -0.5), normal_(8, d, f, std=d ** -0.5),
+               normal_(8, f, d, std=f ** -0.5))
+
+    def step(lo, hi):
+        c = moe.Config(hi - lo, d, f, capacity_factor=4.0)
+        ck, ws = _buffers(c)
+        out = moe.layer_forward_train_c8(c, x[lo:hi], *weights, ck, ws)
+        return out, moe.layer_backward_c8(c, x[lo:hi], *weights, dout[lo:hi], ck, ws)
+
+    out, g = step(0, T)
+    last, gl = step(T - n, T)
+    assert torch.equal(out[T - n:], last) and torch.equal(g["dx"][T - n:], gl["dx"])
+    first, gf = step(0, T - n)
+    assert torch.equal(out[:T - n], first)
+    for q in KEYS[3:]:
+        # three bf16 roundings; and on both sides fp32 sums of the same n = 17500 terms an expert, off by at most
+        # (n + 2) 2^-23 sum |term|, where sum |term| is about 0.8^2 sqrt(n) = 84 times the sum's rms (130 taken)
+        got, want = g[q].float(), gf[q].float() + gl[q].float()
+        tol = 3 * 2.0 ** -9 * (gf[q].float().abs() + gl[q].float().abs() + got.abs()) + 0.54 * got.pow(2).mean().sqrt()
+        assert ((got - want).abs() <= tol).all(), q
+    assert moe.get_device_error() == 0
+
+
 def test_blocks_with_overflow_and_zero_rows():
     s = Step("few_rows")
     x = s.L.dev["x"]
