@@ -577,18 +577,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float sc = (store && args.row_scale) ? __ldg(args.row_scale + row) : 1.0f;
         float* dst = args.out + (store ? drow : 0) * args.ld + t.nt * bn;
+        // Sums: the 4-column pieces of eight rows change places among eight lanes
+        // first, so that an instruction adds whole 128-byte lines of four rows and
+        // not 16 bytes of 32 (T 4096, d 6144, f 8192: 349 against 381 us; whole
+        // sectors in lane pairs 447, 64 bytes in fours 372).
+        constexpr int kTurns = MODE == kDownSum ? 3 : 0, kRows = 1 << kTurns;
+        float* dst_of[kRows];  // rows of this lane's group; NULL: not stored
+#pragma unroll
+        for (int j = 0; j < kRows; ++j)
+          dst_of[j] = reinterpret_cast<float*>(__shfl_sync(
+              0xffffffffu, store ? reinterpret_cast<unsigned long long>(dst) : 0ull, (lane & ~(kRows - 1)) | j));
         auto finish = [&](int c, const uint32_t (&v)[32]) {
-          if (store) {
-            float4* d4 = reinterpret_cast<float4*>(dst + c * 32);
+          float4 p[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            p[k] = make_float4(sc * __uint_as_float(v[4 * k]), sc * __uint_as_float(v[4 * k + 1]),
+                               sc * __uint_as_float(v[4 * k + 2]), sc * __uint_as_float(v[4 * k + 3]));
+          // piece k of lane l goes to piece (k, low bits of l) of lane (l, low bits of k)
+#pragma unroll
+          for (int s = 0; s < kTurns; ++s) {
+            const bool odd = (lane >> s) & 1;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float4 o = make_float4(sc * __uint_as_float(v[4 * k]), sc * __uint_as_float(v[4 * k + 1]),
-                                           sc * __uint_as_float(v[4 * k + 2]), sc * __uint_as_float(v[4 * k + 3]));
-              if (MODE == kDownSum)
-                atomicAdd(d4 + k, o);
+              if (k >> s & 1) continue;
+              const int o = k | 1 << s;
+              float4 x = odd ? p[k] : p[o];
+              x.x = __shfl_xor_sync(0xffffffffu, x.x, 1 << s);
+              x.y = __shfl_xor_sync(0xffffffffu, x.y, 1 << s);
+              x.z = __shfl_xor_sync(0xffffffffu, x.z, 1 << s);
+              x.w = __shfl_xor_sync(0xffffffffu, x.w, 1 << s);
+              if (odd)
+                p[k] = x;
               else
-                d4[k] = o;
+                p[o] = x;
             }
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float* row_dst = dst_of[k & (kRows - 1)];
+            if (!row_dst) continue;
+            float4* d4 = reinterpret_cast<float4*>(row_dst + c * 32 + 4 * ((k & ~(kRows - 1)) | (lane & (kRows - 1))));
+            if (MODE == kDownSum)
+              atomicAdd(d4, p[k]);
+            else
+              *d4 = p[k];
           }
         };
 #pragma unroll
