@@ -152,9 +152,9 @@ bool use_pair_tiles(const moe_config_t& c);
 // Columns of an N tile, of `widths` (those that divide n), by the time that the
 // waves of tiles take: a wave costs its columns and 240 more, for the rows' tile,
 // which it loads whatever its width.  Measured at d 1536, T 2048, cf 1.25, where 6 x
-// 36 tiles of 256 and 8 x 36 of 192 are both two waves: 192 takes 0.85 (4-bit
+// 36 tiles of 256 and 8 x 36 of 192 are both two waves: 192 takes 0.92 (4-bit
 // down), 0.88 (bf16 down) and 0.93 (dx) of the time of 256; at d 6144, T 4096, f
-// 8192, 15 waves of 192 take 409 us and 12 of 256 371 us (4-bit down).
+// 8192, 15 waves of 192 take 397 us and 12 of 256 356 us (4-bit down).
 int tile_columns(const moe_config_t& c, int64_t n, std::initializer_list<int> widths, int num_sms);
 
 // Down with the combine fused: adds row_scale * (H W_down) into a zeroed fp32
