@@ -321,7 +321,8 @@ __device__ __forceinline__ void window_tokens(const BalanceArgs& a, const Chunk&
   }
 }
 
-// The block's sum, in thread 0.
+// The block's sum, in thread 0, which reads sh.fred behind the barrier: a barrier
+// between two calls keeps the second one's writes behind these reads.
 __device__ __forceinline__ float2 block_sum(float2 s, Shared& sh) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -540,9 +541,10 @@ __global__ void __launch_bounds__(kNT, 3) balance_gradient_kernel(const BalanceA
       window_tokens(a, k, l, seq, inv_n, sum, sh);
       if (w0 + kWindow <= k.last) __syncthreads();
     }
+    // a chunk without a window (padding) has passed no barrier since the last chunk's sum was read
+    if (k.last < k.first) __syncthreads();
     sum = block_sum(sum, sh);  // its barrier ends the use of sh.hist
     if (threadIdx.x == 0) a.chunk_sum[c] = sum;
-    if (k.last < k.first) __syncthreads();  // no window's barriers before sh.fred is written again
   }
   // the block that finishes last adds up the chunks' sums
   if (threadIdx.x == 0) {
