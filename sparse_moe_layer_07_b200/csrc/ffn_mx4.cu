@@ -645,14 +645,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// y[r, :] = sum over p of parts[p][r, :] in order, rows below offsets[8].
+// y[r, :] = sum over p of parts[p][r, :] in order, rows from offsets[0] to offsets[8].
 __global__ void __launch_bounds__(256) mx4_sum_parts_kernel(const float4* __restrict__ parts, int n_parts,
                                                            const int32_t* __restrict__ offsets, int64_t max_rows,
                                                            int64_t row_vec, float4* __restrict__ y) {
   pdl_wait();
+  const int64_t first = offsets[0];
   int64_t n = offsets[kE];
-  if (n < 0 || n > max_rows) n = 0;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n * row_vec;
+  if (first < 0 || n > max_rows) n = 0;
+  for (int64_t i = first * row_vec + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n * row_vec;
        i += (int64_t)gridDim.x * blockDim.x) {
     float4 a = __ldg(parts + i);
     for (int p = 1; p < n_parts; ++p) {

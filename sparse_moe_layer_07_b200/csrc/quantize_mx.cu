@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(256) dequantize_mx4_kernel(const uint8_t* __re
   }
 }
 
-// Grouped rows to e4m3: row r < offsets[8] of the codes is src row r, or
-// src[perm[r]] when perm is given.  A thread takes 8 values (16 bytes), four
+// Grouped rows to e4m3: row r of the codes, from offsets[0] to offsets[8], is src
+// row r, or src[perm[r]] when perm is given.  A thread takes 8 values (16 bytes), four
 // neighbours one 32-block, a warp 256 columns of a row at a time with four such
 // pieces in flight; blockIdx.y shares the columns out, so that a few rows still
 // spread over the SMs.  The scale of row r goes to the 512-byte block of its
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(256) quantize_rows_mx8_kernel(const __nv_bfloa
       prev = v[k];
     }
     if (!ok) {
-      s_off[8] = 0;
+      s_off[0] = s_off[8] = 0;
       flag_error(err, MOE_DEVERR_OFFSETS);
     }
   }
@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(256) quantize_rows_mx8_kernel(const __nv_bfloa
   const int per = (pieces + (int)gridDim.y - 1) / (int)gridDim.y;
   const int c_begin = (int)blockIdx.y * per, c_end = min(c_begin + per, pieces);
   const int rows = s_off[8], warps = (int)gridDim.x * 8;
-  for (int r = (int)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
+  for (int r = s_off[0] + (int)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += warps) {
     int64_t sr = r;
     if (perm) {
       sr = __ldg(perm + r);
