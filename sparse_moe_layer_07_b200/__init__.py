@@ -3,8 +3,12 @@
 Thin ctypes binding over ``libmoe_b200.so`` (C ABI declared in
 ``include/moe.h``).  The functions below carry the same names as the C entry
 points without the ``moe_`` prefix; they only check and marshal arguments
-(tensor pointers, the current CUDA stream) and allocate output tensors with
-PyTorch when the caller does not pass them.  Every step of the layer runs in
+(tensor pointers, the current CUDA stream) and allocate output tensors and
+scratch with PyTorch when the caller does not pass them.  A call with `stream`
+runs there and returns at once: its inputs have to be ready on that stream,
+results are taken up behind it (``wait_stream``), and tensors that the caller
+made on another stream stay its own to keep until then; what the call itself
+allocates belongs to `stream`.  Every step of the layer runs in
 the library's CUDA kernels: there is no fallback of any kind, and importing
 this package fails if the library has not been built
 (``python sparse_moe_layer_07_b200/build.py``).
@@ -15,6 +19,7 @@ import collections.abc
 import contextlib
 import ctypes
 import functools
+import inspect
 import math
 import os
 
@@ -199,6 +204,8 @@ def _dev_ptr(t):
 
 def _stream(stream, device=None):
     if stream is not None:
+        if device is not None and stream.device != device:
+            raise ValueError(f"a stream of {stream.device} for tensors on {device}")
         return stream.cuda_stream
     if device is not None and device.index is not None:
         return torch._C._cuda_getCurrentRawStream(device.index)  # 2 us less than through a Stream object
@@ -233,13 +240,57 @@ def _expect_layer(cfg, x=None, w_router=None, w_gate=None, w_up=None, w_down=Non
     _expect("out", out, cfg.T * cfg.d, dt)
 
 
-def _empty(shape, dtype, like):
-    return like.new_empty(shape, dtype=dtype)
+def _empty(shape, dtype, like, stream):
+    """Uninitialised tensor for work on `stream` (None: the current one).  It comes from that stream's memory: a block
+    freed on the current stream may still be in use there, and scratch that a call drops when it returns must not go
+    back to the current stream while `stream` still writes it.  The current stream is recorded as a user, since the
+    caller takes the results up there."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    if t.is_cuda:
+        t.record_stream(here)
+    return t
 
 
-def _empty_like(like, shape):
+def _empty_like(like, shape, stream):
     """Uninitialised tensor of the type of `like` (empty_like is the cheaper call)."""
-    return torch.empty_like(like) if like.shape == shape else like.new_empty(shape)
+    if stream is not None or like.shape != shape:
+        return _empty(shape, like.dtype, like, stream)
+    return torch.empty_like(like)
+
+
+def _record(result, stream):
+    if isinstance(result, torch.Tensor):
+        if result.is_cuda:
+            result.record_stream(stream)
+    elif isinstance(result, dict):
+        _record(list(result.values()), stream)
+    elif isinstance(result, (list, tuple)):
+        for r in result:
+            _record(r, stream)
+
+
+def _on_stream(fn):
+    """Runs a function of several steps with its argument `stream` as the current stream, so that all it allocates,
+    copies and exchanges is ordered there; the caller's stream is recorded as a user of what it returns."""
+    sig = inspect.signature(fn)
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        bound = sig.bind(*args, **kw)
+        stream = bound.arguments.pop("stream", None)
+        if stream is None:
+            return fn(*args, **kw)
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            result = fn(*bound.args, **bound.kwargs)
+        _record(result, here)
+        return result
+
+    return call
 
 
 _HERE = contextlib.nullcontext()
@@ -278,11 +329,11 @@ def router_topk(cfg: Config, x, w_router, logit_bias=None, logits=None, topk_idx
     """Router logits, top-2 experts and their softmax weights.  Returns (idx, w, logits|None)."""
     _expect_layer(cfg, x=x, w_router=w_router, logit_bias=logit_bias)
     if topk_idx is None:
-        topk_idx = _empty((cfg.T, cfg.top_k), torch.int32, x)
+        topk_idx = _empty((cfg.T, cfg.top_k), torch.int32, x, stream)
     if topk_w is None:
-        topk_w = _empty((cfg.T, cfg.top_k), torch.float32, x)
+        topk_w = _empty((cfg.T, cfg.top_k), torch.float32, x, stream)
     if logits is None and want_logits:
-        logits = _empty((cfg.T, cfg.E), torch.float32, x)
+        logits = _empty((cfg.T, cfg.E), torch.float32, x, stream)
     _check(lib.moe_router_topk(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias), _dev_ptr(logits),
                                _dev_ptr(topk_idx), _dev_ptr(topk_w), _stream(stream, x.device)), "moe_router_topk")
     return topk_idx, topk_w, logits
@@ -294,19 +345,19 @@ def dispatch(cfg: Config, x, topk_idx, topk_w, gather: bool = True, out=None, ws
     dev = topk_idx
     rows = cfg.T * cfg.top_k
     o = dict(out or {})
-    o.setdefault("counts_raw", _empty((cfg.E,), torch.int32, dev))
-    o.setdefault("counts_kept", _empty((cfg.E,), torch.int32, dev))
-    o.setdefault("offsets", _empty((cfg.E + 1,), torch.int32, dev))
-    o.setdefault("perm", _empty((rows,), torch.int32, dev))
-    o.setdefault("slot_of", _empty((cfg.T, cfg.top_k), torch.int32, dev))
-    o.setdefault("row_scale", _empty((rows,), torch.float32, dev))
+    o.setdefault("counts_raw", _empty((cfg.E,), torch.int32, dev, stream))
+    o.setdefault("counts_kept", _empty((cfg.E,), torch.int32, dev, stream))
+    o.setdefault("offsets", _empty((cfg.E + 1,), torch.int32, dev, stream))
+    o.setdefault("perm", _empty((rows,), torch.int32, dev, stream))
+    o.setdefault("slot_of", _empty((cfg.T, cfg.top_k), torch.int32, dev, stream))
+    o.setdefault("row_scale", _empty((rows,), torch.float32, dev, stream))
     if gather:
-        o.setdefault("x_perm", _empty((rows, cfg.d), cfg.torch_dtype, dev))
+        o.setdefault("x_perm", _empty((rows, cfg.d), cfg.torch_dtype, dev, stream))
     else:
         o["x_perm"] = None
     nbytes = dispatch_workspace_size(cfg)
     if ws is None:
-        ws = _empty((max(nbytes, 1),), torch.uint8, dev)
+        ws = _empty((max(nbytes, 1),), torch.uint8, dev, stream)
     _check(lib.moe_dispatch(cfg.ref, _dev_ptr(x), _dev_ptr(topk_idx), _dev_ptr(topk_w), _dev_ptr(o["counts_raw"]),
                             _dev_ptr(o["counts_kept"]), _dev_ptr(o["offsets"]), _dev_ptr(o["perm"]),
                             _dev_ptr(o["slot_of"]), _dev_ptr(o["row_scale"]), _dev_ptr(o["x_perm"]),
@@ -319,7 +370,7 @@ def gather_rows(src, idx, out=None, stream=None):
     n = idx.numel()
     row_bytes = src[0].numel() * src.element_size() if src.shape[0] else src.stride(0) * src.element_size()
     if out is None:
-        out = torch.empty((n,) + tuple(src.shape[1:]), dtype=src.dtype, device=src.device)
+        out = _empty((n,) + tuple(src.shape[1:]), src.dtype, src, stream)
     if idx.dtype != torch.int32:
         raise ValueError("idx must be int32")
     _check(lib.moe_gather_rows(_dev_ptr(src), src.shape[0], _dev_ptr(idx), n, row_bytes, _dev_ptr(out),
@@ -330,7 +381,7 @@ def gather_rows(src, idx, out=None, stream=None):
 def route_counts(cfg: Config, topk_idx, counts=None, stream=None):
     """counts[e] = assignments routed to expert e (device int32 [E])."""
     if counts is None:
-        counts = _empty((cfg.E,), torch.int32, topk_idx)
+        counts = _empty((cfg.E,), torch.int32, topk_idx, stream)
     _check(lib.moe_route_counts(cfg.ref, _dev_ptr(topk_idx), _dev_ptr(counts), _stream(stream, topk_idx.device)),
            "moe_route_counts")
     return counts
@@ -344,18 +395,18 @@ def dispatch_shard(cfg: Config, capacity: int, shard_counts, shard: int, x, topk
     dev = topk_idx
     rows = cfg.T * cfg.top_k
     o = dict(out or {})
-    o.setdefault("counts_raw", _empty((cfg.E,), torch.int32, dev))
-    o.setdefault("counts_kept", _empty((cfg.E,), torch.int32, dev))
-    o.setdefault("offsets", _empty((cfg.E + 1,), torch.int32, dev))
-    o.setdefault("perm", _empty((rows,), torch.int32, dev))
-    o.setdefault("slot_of", _empty((cfg.T, cfg.top_k), torch.int32, dev))
-    o.setdefault("row_scale", _empty((rows,), torch.float32, dev))
+    o.setdefault("counts_raw", _empty((cfg.E,), torch.int32, dev, stream))
+    o.setdefault("counts_kept", _empty((cfg.E,), torch.int32, dev, stream))
+    o.setdefault("offsets", _empty((cfg.E + 1,), torch.int32, dev, stream))
+    o.setdefault("perm", _empty((rows,), torch.int32, dev, stream))
+    o.setdefault("slot_of", _empty((cfg.T, cfg.top_k), torch.int32, dev, stream))
+    o.setdefault("row_scale", _empty((rows,), torch.float32, dev, stream))
     if gather:
-        o.setdefault("x_perm", _empty((rows, cfg.d), cfg.torch_dtype, dev))
+        o.setdefault("x_perm", _empty((rows, cfg.d), cfg.torch_dtype, dev, stream))
     else:
         o["x_perm"] = None
     if ws is None:
-        ws = _empty((max(dispatch_workspace_size(cfg), 1),), torch.uint8, dev)
+        ws = _empty((max(dispatch_workspace_size(cfg), 1),), torch.uint8, dev, stream)
     if shard_counts.dtype != torch.int32 or shard_counts.dim() != 2 or shard_counts.shape[1] != cfg.E:
         raise ValueError("shard_counts must be int32 [n_shards, E]")
     _check(lib.moe_dispatch_shard(cfg.ref, int(capacity), _dev_ptr(shard_counts), shard_counts.shape[0], int(shard),
@@ -373,14 +424,14 @@ def dispatch_noalloc(cfg: Config, x, topk_idx, topk_w, gather: bool = True, out=
     dev = topk_idx
     rows = cfg.T * cfg.top_k
     o = dict(out or {})
-    o.setdefault("counts_raw", _empty((cfg.E,), torch.int32, dev))
-    o.setdefault("counts_kept", _empty((cfg.E,), torch.int32, dev))
-    o.setdefault("offsets", _empty((cfg.E + 1,), torch.int32, dev))
-    o.setdefault("perm", _empty((rows,), torch.int32, dev))
-    o.setdefault("slot_of", _empty((cfg.T, cfg.top_k), torch.int32, dev))
-    o.setdefault("row_scale", _empty((rows,), torch.float32, dev))
+    o.setdefault("counts_raw", _empty((cfg.E,), torch.int32, dev, stream))
+    o.setdefault("counts_kept", _empty((cfg.E,), torch.int32, dev, stream))
+    o.setdefault("offsets", _empty((cfg.E + 1,), torch.int32, dev, stream))
+    o.setdefault("perm", _empty((rows,), torch.int32, dev, stream))
+    o.setdefault("slot_of", _empty((cfg.T, cfg.top_k), torch.int32, dev, stream))
+    o.setdefault("row_scale", _empty((rows,), torch.float32, dev, stream))
     if gather:
-        o.setdefault("x_perm", _empty((rows, cfg.d), cfg.torch_dtype, dev))
+        o.setdefault("x_perm", _empty((rows, cfg.d), cfg.torch_dtype, dev, stream))
     else:
         o["x_perm"] = None
     _check(lib.moe_dispatch_noalloc(cfg.ref, _dev_ptr(x), _dev_ptr(topk_idx), _dev_ptr(topk_w),
@@ -392,7 +443,7 @@ def dispatch_noalloc(cfg: Config, x, topk_idx, topk_w, gather: bool = True, out=
 
 def expert_gate_up(cfg: Config, x_perm, offsets, w_gate, w_up, h=None, stream=None):
     if h is None:
-        h = _empty((cfg.T * cfg.top_k, cfg.f), cfg.torch_dtype, x_perm)
+        h = _empty((cfg.T * cfg.top_k, cfg.f), cfg.torch_dtype, x_perm, stream)
     _check(lib.moe_expert_gate_up(cfg.ref, _dev_ptr(x_perm), _dev_ptr(offsets), _dev_ptr(w_gate), _dev_ptr(w_up),
                                   _dev_ptr(h), _stream(stream, x_perm.device)), "moe_expert_gate_up")
     return h
@@ -400,7 +451,7 @@ def expert_gate_up(cfg: Config, x_perm, offsets, w_gate, w_up, h=None, stream=No
 
 def expert_down(cfg: Config, h, offsets, w_down, row_scale=None, y=None, ws=None, stream=None):
     if y is None:
-        y = _empty((cfg.T * cfg.top_k, cfg.d), torch.float32, h)
+        y = _empty((cfg.T * cfg.top_k, cfg.d), torch.float32, h, stream)
     _check(lib.moe_expert_down(cfg.ref, _dev_ptr(h), _dev_ptr(offsets), _dev_ptr(w_down), _dev_ptr(row_scale),
                                _dev_ptr(y), _dev_ptr(ws), 0 if ws is None else ws.numel(),
                                _stream(stream, h.device)), "moe_expert_down")
@@ -411,9 +462,9 @@ def expert_ffn(cfg: Config, x_perm, offsets, w_gate, w_up, w_down, row_scale=Non
                stream=None):
     """SwiGLU experts over the grouped rows.  Returns (h, y)."""
     if h is None:
-        h = _empty((cfg.T * cfg.top_k, cfg.f), cfg.torch_dtype, x_perm)
+        h = _empty((cfg.T * cfg.top_k, cfg.f), cfg.torch_dtype, x_perm, stream)
     if y is None:
-        y = _empty((cfg.T * cfg.top_k, cfg.d), torch.float32, x_perm)
+        y = _empty((cfg.T * cfg.top_k, cfg.d), torch.float32, x_perm, stream)
     _check(lib.moe_expert_ffn(cfg.ref, _dev_ptr(x_perm), _dev_ptr(offsets), _dev_ptr(w_gate), _dev_ptr(w_up),
                               _dev_ptr(w_down), _dev_ptr(row_scale), _dev_ptr(h), _dev_ptr(y), _dev_ptr(ws),
                               0 if ws is None else ws.numel(), _stream(stream, x_perm.device)), "moe_expert_ffn")
@@ -423,9 +474,9 @@ def expert_ffn(cfg: Config, x_perm, offsets, w_gate, w_up, w_down, row_scale=Non
 def expert_down_combine(cfg: Config, h, offsets, w_down, row_scale, perm, out=None, ws=None, stream=None):
     """down x routing weight summed straight into token order (down + combine, no y)."""
     if out is None:
-        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, h)
+        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, h, stream)
     if ws is None:
-        ws = _empty((max(lib.moe_expert_down_combine_workspace_size(cfg.ref), 1),), torch.uint8, h)
+        ws = _empty((max(lib.moe_expert_down_combine_workspace_size(cfg.ref), 1),), torch.uint8, h, stream)
     _check(lib.moe_expert_down_combine(cfg.ref, _dev_ptr(h), _dev_ptr(offsets), _dev_ptr(w_down), _dev_ptr(row_scale),
                                        _dev_ptr(perm), _dev_ptr(out), _dev_ptr(ws), ws.numel(),
                                        _stream(stream, h.device)), "moe_expert_down_combine")
@@ -457,7 +508,7 @@ def ep_dispatch_peers(cfg: Config, peers: EpPeers, table, x, disp, grp_offsets=N
     grouped buffers (moe_ep_dispatch_peers).  table [world, E] int32 on the
     device; disp: this rank's dispatch() result.  Returns grp_offsets [E + 1]."""
     if grp_offsets is None:
-        grp_offsets = _empty((cfg.E + 1,), torch.int32, table)
+        grp_offsets = _empty((cfg.E + 1,), torch.int32, table, stream)
     _expect("table", table, peers.world * cfg.E, torch.int32)
     _check(lib.moe_ep_dispatch_peers(cfg.ref, peers.ref, _dev_ptr(table), _dev_ptr(x), _dev_ptr(disp["offsets"]),
                                      _dev_ptr(disp["perm"]), _dev_ptr(disp["row_scale"]), _dev_ptr(grp_offsets),
@@ -505,7 +556,7 @@ def peer_release(addr: int, handle: bytes):
 
 def combine(cfg: Config, y, slot_of, topk_w=None, weights_applied: bool = True, out=None, stream=None):
     if out is None:
-        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, y)
+        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, y, stream)
     _check(lib.moe_combine(cfg.ref, _dev_ptr(y), _dev_ptr(slot_of), _dev_ptr(topk_w), int(bool(weights_applied)),
                            _dev_ptr(out), _stream(stream, y.device)), "moe_combine")
     return out
@@ -516,9 +567,9 @@ def layer_forward(cfg: Config, x, w_router, w_gate, w_up, w_down, logit_bias=Non
     """The whole layer; returns out [T, d] (stats, if given, is filled on the device)."""
     _expect_layer(cfg, x, w_router, w_gate, w_up, w_down, logit_bias, out)
     if out is None:
-        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x)
+        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x, stream)
     if ws is None:
-        ws = _empty((max(workspace_size(cfg), 1),), torch.uint8, x)
+        ws = _empty((max(workspace_size(cfg), 1),), torch.uint8, x, stream)
     _check(lib.moe_layer_forward(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias), _dev_ptr(w_gate),
                                  _dev_ptr(w_up), _dev_ptr(w_down), _dev_ptr(out), _dev_ptr(stats), _dev_ptr(ws),
                                  ws.numel(), _stream(stream, x.device)), "moe_layer_forward")
@@ -573,7 +624,7 @@ def layer_forward_train(cfg: Config, x, w_router, w_gate, w_up, w_down, ws, logi
     """The layer forward that keeps the backward's inputs in ws (moe_workspace_size_train bytes)."""
     _expect_layer(cfg, x, w_router, w_gate, w_up, w_down, logit_bias, out)
     if out is None:
-        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x)
+        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x, stream)
     _check(lib.moe_layer_forward_train(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias),
                                        _dev_ptr(w_gate), _dev_ptr(w_up), _dev_ptr(w_down), _dev_ptr(out),
                                        _dev_ptr(ws), ws.numel(), _stream(stream, x.device)), "moe_layer_forward_train")
@@ -590,15 +641,15 @@ def layer_backward(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ws, gra
     _expect("dout", dout, cfg.T * cfg.d if cfg.T else dout.numel(), cfg.torch_dtype)
     E, d, f = cfg.E, cfg.d, cfg.f
     g = dict(grads or {})
-    g.setdefault("dx", _empty((cfg.T, d), cfg.torch_dtype, x))
-    g.setdefault("dw_router", _empty((E, d), torch.float32, x))
+    g.setdefault("dx", _empty((cfg.T, d), cfg.torch_dtype, x, stream))
+    g.setdefault("dw_router", _empty((E, d), torch.float32, x, stream))
     if want_dbias:
-        g.setdefault("dbias", _empty((E,), torch.float32, x))
+        g.setdefault("dbias", _empty((E,), torch.float32, x, stream))
     else:
         g["dbias"] = None
-    g.setdefault("dw_gate", _empty((E, d, f), torch.float32, x))
-    g.setdefault("dw_up", _empty((E, d, f), torch.float32, x))
-    g.setdefault("dw_down", _empty((E, f, d), torch.float32, x))
+    g.setdefault("dw_gate", _empty((E, d, f), torch.float32, x, stream))
+    g.setdefault("dw_up", _empty((E, d, f), torch.float32, x, stream))
+    g.setdefault("dw_down", _empty((E, f, d), torch.float32, x, stream))
     _check(lib.moe_layer_backward_aux(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(w_gate), _dev_ptr(w_up),
                                       _dev_ptr(w_down), _dev_ptr(dout), _dev_ptr(dlogits), _dev_ptr(g["dx"]),
                                       _dev_ptr(g["dw_router"]), _dev_ptr(g["dbias"]), _dev_ptr(g["dw_gate"]),
@@ -678,7 +729,7 @@ def layer_forward_train_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, ckpt,
     (workspace_size_train_c8 bytes) is scratch that every layer of a model can share."""
     _expect_layer(cfg, x, w_router, w_gate, w_up, w_down, logit_bias, out)
     if out is None:
-        out = _empty_like(x, (cfg.T, cfg.d))
+        out = _empty_like(x, (cfg.T, cfg.d), stream)
     with _same_device(x, w_router, w_gate, w_up, w_down, ckpt, ws, logit_bias, out):
         _check(lib.moe_layer_forward_train_c8(cfg.ref, _ptr(x), _ptr(w_router), _ptr(logit_bias),
                                               _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out),
@@ -706,7 +757,7 @@ def layer_backward_c8(cfg: Config, x, w_router, w_gate, w_up, w_down, dout, ckpt
         if k in g:
             _expect(k, g[k], math.prod(shape), dt)
         else:
-            g[k] = _empty_like(like[k], shape)
+            g[k] = _empty_like(like[k], shape, stream)
     with _same_device(x, w_router, w_gate, w_up, w_down, dout, ckpt, ws, dlogits, *g.values()):
         _check(lib.moe_layer_backward_c8(cfg.ref, _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up),
                                          _ptr(w_down), _ptr(dout), _ptr(dlogits), _ptr(g["dx"]),
@@ -721,9 +772,9 @@ def quantize_int8(cfg: Config, w, q=None, scale=None, stream=None):
     """Per-output-channel int8 codes and fp32 scales of expert weights w [E, K, N] (bf16)."""
     E, K, N = w.shape
     if q is None:
-        q = torch.empty((E, K, N), dtype=torch.int8, device=w.device)
+        q = _empty((E, K, N), torch.int8, w, stream)
     if scale is None:
-        scale = torch.empty((E, N), dtype=torch.float32, device=w.device)
+        scale = _empty((E, N), torch.float32, w, stream)
     _check(lib.moe_quantize_int8(cfg.ref, _dev_ptr(w), K, N, _dev_ptr(q), _dev_ptr(scale), _stream(stream, w.device)),
            "moe_quantize_int8")
     return q, scale
@@ -756,14 +807,14 @@ def balance_loss(cfg: Config, logits, topk_idx, token_mask=None, seq_offsets=Non
                      ("dlogits", cfg.T * cfg.E, torch.float32)) if out else ():
         _expect(k, o.get(k), n, dt)
     if "loss" not in o:
-        o["loss"] = logits.new_empty((3,))
+        o["loss"] = _empty((3,), torch.float32, logits, stream)
     if "counts" not in o:
-        o["counts"] = topk_idx.new_empty((n_seq, cfg.E))
+        o["counts"] = _empty((n_seq, cfg.E), torch.int32, topk_idx, stream)
     if "dlogits" not in o:
-        o["dlogits"] = _empty_like(logits, (cfg.T, cfg.E))
+        o["dlogits"] = _empty_like(logits, (cfg.T, cfg.E), stream)
     if ws is None:
         need = balance_loss_workspace_size(cfg, n_seq)
-        ws = _empty((need,), torch.uint8, logits) if need else None
+        ws = _empty((need,), torch.uint8, logits, stream) if need else None
     with _same_device(logits, topk_idx, token_mask, seq_offsets, ws, *o.values()):
         _check(lib.moe_balance_loss(cfg.ref, _ptr(logits), _ptr(topk_idx), _ptr(token_mask),
                                     _ptr(seq_offsets), n_seq, float(balance_coef), float(z_coef),
@@ -813,9 +864,9 @@ def expert_ffn_w8(cfg: Config, x_perm, offsets, qw: QuantizedExperts, row_scale=
                   stream=None):
     """SwiGLU experts with int8 weights over the grouped rows.  Returns (y, ws)."""
     if y is None:
-        y = _empty((cfg.T * cfg.top_k, cfg.d), torch.float32, x_perm)
+        y = _empty((cfg.T * cfg.top_k, cfg.d), torch.float32, x_perm, stream)
     if ws is None:
-        ws = _empty((max(lib.moe_expert_ffn_w8_workspace_size(cfg.ref), 1),), torch.uint8, x_perm)
+        ws = _empty((max(lib.moe_expert_ffn_w8_workspace_size(cfg.ref), 1),), torch.uint8, x_perm, stream)
     _check(lib.moe_expert_ffn_w8(cfg.ref, _dev_ptr(x_perm), _dev_ptr(offsets), *qw.ptrs(), _dev_ptr(row_scale),
                                  _dev_ptr(y), _dev_ptr(ws), ws.numel(), _stream(stream, x_perm.device)),
            "moe_expert_ffn_w8")
@@ -827,9 +878,9 @@ def layer_forward_w8(cfg: Config, x, w_router, qw: QuantizedExperts, logit_bias=
     """The whole layer with int8 expert weights; returns out [T, d]."""
     _expect_layer(cfg, x=x, w_router=w_router, logit_bias=logit_bias, out=out)
     if out is None:
-        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x)
+        out = _empty((cfg.T, cfg.d), cfg.torch_dtype, x, stream)
     if ws is None:
-        ws = _empty((max(lib.moe_workspace_size_w8(cfg.ref), 1),), torch.uint8, x)
+        ws = _empty((max(lib.moe_workspace_size_w8(cfg.ref), 1),), torch.uint8, x, stream)
     _check(lib.moe_layer_forward_w8(cfg.ref, _dev_ptr(x), _dev_ptr(w_router), _dev_ptr(logit_bias), *qw.ptrs(),
                                     _dev_ptr(out), _dev_ptr(stats), _dev_ptr(ws), ws.numel(),
                                     _stream(stream, x.device)), "moe_layer_forward_w8")
@@ -843,9 +894,9 @@ def quantize_mx4(cfg: Config, w, codes=None, scales=None, stream=None):
         raise ValueError(f"w must be bf16 [{cfg.E}, K, N]")
     E, K, N = w.shape
     if codes is None:
-        codes = _empty((E, N, K // 2), torch.uint8, w)
+        codes = _empty((E, N, K // 2), torch.uint8, w, stream)
     if scales is None:
-        scales = _empty((E, N // 128, K // 128, 512), torch.uint8, w)
+        scales = _empty((E, N // 128, K // 128, 512), torch.uint8, w, stream)
     _expect("codes", codes, E * N * (K // 2), torch.uint8)
     _expect("scales", scales, E * (N // 128) * (K // 128) * 512, torch.uint8)
     with _same_device(w, codes, scales):
@@ -867,7 +918,7 @@ def dequantize_mx4(cfg: Config, codes, scales, out=None, stream=None):
     """The weights [E, K, N] in bf16 that quantize_mx4's codes and scales stand for (exact)."""
     K, N = _mx4_shape(cfg, codes, scales)
     if out is None:
-        out = _empty((cfg.E, K, N), torch.bfloat16, codes)
+        out = _empty((cfg.E, K, N), torch.bfloat16, codes, stream)
     _expect("out", out, cfg.E * K * N, torch.bfloat16)
     with _same_device(codes, scales, out):
         _check(lib.moe_dequantize_mx4(cfg.ref, _ptr(codes), _ptr(scales), K, N, _ptr(out),
@@ -922,9 +973,9 @@ def expert_ffn_mx4(cfg: Config, x_perm, offsets, qw: MxExperts, row_scale=None, 
     qw.check(cfg)
     rows = cfg.T * cfg.top_k
     if y is None:
-        y = _empty((rows, cfg.d), torch.float32, x_perm)
+        y = _empty((rows, cfg.d), torch.float32, x_perm, stream)
     if ws is None:
-        ws = _empty((max(expert_ffn_mx4_workspace_size(cfg), 1),), torch.uint8, x_perm)
+        ws = _empty((max(expert_ffn_mx4_workspace_size(cfg), 1),), torch.uint8, x_perm, stream)
     _expect("x_perm", x_perm, rows * cfg.d, cfg.torch_dtype)
     _expect("offsets", offsets, cfg.E + 1, torch.int32)
     _expect("row_scale", row_scale, rows, torch.float32)
@@ -946,9 +997,9 @@ def layer_forward_mx4(cfg: Config, x, w_router, qw: MxExperts, logit_bias=None, 
     _expect_layer(cfg, x=x, w_router=w_router, logit_bias=logit_bias, out=out)
     qw.check(cfg)
     if out is None:
-        out = _empty_like(x, (cfg.T, cfg.d))
+        out = _empty_like(x, (cfg.T, cfg.d), stream)
     if ws is None:
-        ws = _empty((max(workspace_size_mx4(cfg), 1),), torch.uint8, x)
+        ws = _empty((max(workspace_size_mx4(cfg), 1),), torch.uint8, x, stream)
     _expect("stats", stats, 3 * cfg.E + 2, torch.int32)
     with _same_device(x, w_router, logit_bias, out, stats, ws, *qw.tensors()):
         _check(lib.moe_layer_forward_mx4(cfg.ref, _ptr(x), _ptr(w_router), _ptr(logit_bias), *qw.ptrs(),

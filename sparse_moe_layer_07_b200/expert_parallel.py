@@ -28,14 +28,12 @@ ranks' buffers (CUDA IPC); ep_forward_peers_local runs the same kernels for
 """
 from __future__ import annotations
 
-import contextlib
-
 import numpy as np
 import torch
 import torch.distributed as dist
 
-from . import (Config, EpPeers, combine, dispatch, ep_combine_peers, ep_dispatch_peers, ep_expert_ffn_peers,
-               expert_ffn, gather_rows, peer_export, peer_import, peer_release, router_topk)
+from . import (Config, EpPeers, _on_stream, combine, dispatch, ep_combine_peers, ep_dispatch_peers,
+               ep_expert_ffn_peers, expert_ffn, gather_rows, peer_export, peer_import, peer_release, router_topk)
 
 
 def owned_experts(rank: int, world: int, E: int = 8):
@@ -84,6 +82,7 @@ def ep_plan(table, rank: int, world: int):
     return {"send_splits": send, "recv_splits": recv, "fwd": fwd, "inv": inv, "offsets": offsets, "mine": mine}
 
 
+@_on_stream
 def ep_prepare(cfg: Config, x, w_router, logit_bias=None, stream=None):
     """Route and group this rank's tokens; counts_kept [E] is what the table gathers."""
     idx, w, _ = router_topk(cfg, x, w_router, logit_bias, stream=stream)
@@ -91,6 +90,7 @@ def ep_prepare(cfg: Config, x, w_router, logit_bias=None, stream=None):
     return {"idx": idx, "w": w, "disp": disp, "counts": disp["counts_kept"]}
 
 
+@_on_stream
 def ep_experts(cfg: Config, x_recv, plan, w_gate, w_up, w_down, stream=None):
     """Run this rank's experts on the received rows; returns their (unweighted)
     outputs in received order, fp32 [n_recv, d]."""
@@ -108,6 +108,7 @@ def ep_experts(cfg: Config, x_recv, plan, w_gate, w_up, w_down, stream=None):
     return gather_rows(y_grp, torch.from_numpy(plan["inv"]).to(dev), stream=stream)
 
 
+@_on_stream
 def ep_finish(cfg: Config, y_back, state, stream=None):
     """Weighted combine of the returned expert outputs, one row per kept slot in
     this rank's x_perm order (the combine reads only those slots)."""
@@ -142,6 +143,7 @@ def gather_table(counts, group=None):
     return torch.stack(parts).cpu().numpy()
 
 
+@_on_stream
 def layer_forward_ep(cfg: Config, x, w_router, w_gate, w_up, w_down, logit_bias=None, group=None, stream=None):
     """The layer with expert parallelism over the ranks of `group`: this rank's
     tokens in, this rank's output rows out.  w_gate/w_up/w_down hold all E
@@ -189,6 +191,7 @@ class EpPeerBuffers:
         return tuple(b + o for o in self.part_offsets)
 
 
+@_on_stream
 def ep_route(cfg: Config, x, w_router, logit_bias=None, stream=None):
     """Route and dispatch this rank's tokens without gathering x (the peer
     dispatch reads x itself)."""
@@ -196,6 +199,7 @@ def ep_route(cfg: Config, x, w_router, logit_bias=None, stream=None):
     return dispatch(cfg, x, idx, w, gather=False, stream=stream)
 
 
+@_on_stream
 def ep_forward_peers_local(cfg: Config, xs, w_router, w_gate, w_up, w_down, logit_bias=None, bufs=None,
                            stream=None):
     """The peer-memory path for len(xs) ranks held by this process on one
@@ -283,6 +287,7 @@ class EpPeerGroup:
         dist.barrier(group=self.group)
 
 
+@_on_stream
 def layer_forward_ep_peers(cfg: Config, x, w_router, w_gate, w_up, w_down, logit_bias=None, group=None,
                            peer_group: EpPeerGroup | None = None, stream=None):
     """The layer with expert parallelism over peer memory: this rank's tokens
@@ -292,16 +297,14 @@ def layer_forward_ep_peers(cfg: Config, x, w_router, w_gate, w_up, w_down, logit
     own = peer_group is None
     pg = EpPeerGroup(cfg, group, x.device) if own else peer_group
     try:
-        # the barriers order the current stream: run every phase on it
-        with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
-            disp = ep_route(cfg, x, w_router, logit_bias)
-            table = gather_table_device(disp["counts_kept"], group)
-            ep_dispatch_peers(cfg, pg.peers, table, x, disp, pg.bufs.grp_offsets)
-            ep_barrier(group, x.device)
-            ep_expert_ffn_peers(cfg, pg.peers, pg.bufs.grp_offsets, w_gate, w_up, w_down, pg.bufs.h)
-            ep_barrier(group, x.device)
-            return ep_combine_peers(cfg, pg.peers,
-                                    torch.empty((cfg.T, cfg.d), dtype=cfg.torch_dtype, device=x.device))
+        # the barriers order the current stream, which every phase runs on
+        disp = ep_route(cfg, x, w_router, logit_bias)
+        table = gather_table_device(disp["counts_kept"], group)
+        ep_dispatch_peers(cfg, pg.peers, table, x, disp, pg.bufs.grp_offsets)
+        ep_barrier(group, x.device)
+        ep_expert_ffn_peers(cfg, pg.peers, pg.bufs.grp_offsets, w_gate, w_up, w_down, pg.bufs.h)
+        ep_barrier(group, x.device)
+        return ep_combine_peers(cfg, pg.peers, torch.empty((cfg.T, cfg.d), dtype=cfg.torch_dtype, device=x.device))
     finally:
         if own:
             pg.close()

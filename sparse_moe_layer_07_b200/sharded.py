@@ -15,7 +15,7 @@ from __future__ import annotations
 import torch
 import torch.distributed as dist
 
-from . import Config, capacity, combine, dispatch_shard, expert_ffn, route_counts, router_topk
+from . import Config, _on_stream, capacity, combine, dispatch_shard, expert_ffn, route_counts, router_topk
 
 
 def gather_shard_counts(counts: torch.Tensor, group=None) -> torch.Tensor:
@@ -33,6 +33,7 @@ def global_capacity(cfg_shard: Config, tokens_global: int) -> int:
     return capacity(g)
 
 
+@_on_stream
 def layer_forward_shard(cfg: Config, tokens_global: int, shard_counts_fn, shard: int, x, w_router, w_gate, w_up,
                         w_down, logit_bias=None, stream=None):
     """This rank's tokens through the layer with the global capacity.  shard_counts_fn
