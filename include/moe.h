@@ -425,8 +425,10 @@ MOE_API moe_status_t moe_dequantize_mx4(const moe_config_t* cfg, const uint8_t* 
  * each product in microscaled 8-bit floating point: blocks of 32 along K of a
  * row of x_perm, then of H (formed in fp32), share a power of two as above with
  * x = floor(log2 m) - 8 and e4m3 elements (the largest element is at most 448,
- * so none is cut off; relative error of an element at most 2^-4, of a row in
- * the root mean square about 2.6%, where the 4-bit weights have about 11%):
+ * so none is cut off; an element v is off by at most 2^-4 |v|, or by 2^-10 2^x
+ * where that is more: below 2^-6 2^x the steps stay 2^-9 2^x; a row of normally
+ * distributed values in the root mean square by about 2.6%, where the 4-bit
+ * weights have about 11%):
  *   h = silu(x^ W^_gate) * (x^ W^_up),  y = row_scale * (h^ W^_down)
  * with fp32 accumulation.  A row block with a NaN or an infinity makes its row
  * NaN.  c_*, s_*: codes and scales of moe_quantize_mx4; y [T*2, d] fp32.  bf16
