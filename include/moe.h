@@ -316,8 +316,10 @@ MOE_API moe_status_t moe_layer_backward_aux(const moe_config_t* cfg, const void*
  * U = X W_up as 8-bit codes (the bf16 pair keeps X, G, U and H); everything
  * else is scratch that all layers of a model can share, one call after the
  * other.  Blocks of 32 columns of a row share a scale:
- *   s = bf16(max |v| / 127) (0 when below 2^-126),  c = rint(v / s),  v^ = c s
- * from the fp32 accumulators; a block that holds a NaN or an infinity gets
+ *   s = bf16(max |v| / 127) (0 when below 2^-126),  c = rint(v * (1 / s)),  v^ = c s
+ * from the fp32 accumulators, 1 / s rounded to fp32 (so c is the integer nearest
+ * to v / s, or either of two where the quotient is within 2^-17 of their middle;
+ * |v^ - v| <= s / 2 (1 + 2^-16)); a block that holds a NaN or an infinity gets
  * s = NaN, codes 0, and decodes to NaN.  out is moe_layer_forward's bit for
  * bit (it does not go through the codes).  The backward is the derivative of
  * the layer at G^, U^: with H^ = silu(G^) U^, dHu = dout W_down^T, routing

@@ -66,15 +66,17 @@ __device__ __forceinline__ float silu_mul_fast(float g, float u) { return __fdiv
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // 8-bit code of a block of 32 values (activation checkpoints): s = bf16(amax /
-// 127) and c = rint(v / s), so an element is off by at most s / 2 = amax / 254
-// (an e4m3 code of the same 8 bits would be off by up to 1/16 of the element:
-// for normally distributed rows a root mean square error of 2.6% against 0.5%).
-// A scale below 2^-126 counts as 0 (all codes 0); a block that holds a NaN or
-// an infinity gets the scale NaN and decodes to NaN.  amax is found on the bit
-// patterns (as unsigned integers NaN and inf are the largest).  |v / s| stays
-// under 127.25, since rounding s to bf16 moves it by at most 2^-9, so no clamp
-// is needed; adding 1.5 * 2^23 rounds to an integer (ties to even) whose low
-// byte is the code.
+// 127) and c = rint(v * (1 / s)) with 1 / s in fp32, which moves a quotient by up
+// to 2^-17: next to a tie c may be the other neighbour, and an element is off by
+// at most s / 2 (1 + 2^-16) (a divide instead would cost a call per element).
+// s / 2 is about amax / 254 (an e4m3 code of the same 8 bits would be off by up to
+// 1/16 of the element: for normally distributed rows a root mean square error of
+// 2.6% against 0.5%).  A scale below 2^-126 counts as 0 (all codes 0); a block
+// that holds a NaN or an infinity gets the scale NaN and decodes to NaN.  amax is
+// found on the bit patterns (as unsigned integers NaN and inf are the largest).
+// Rounding s to bf16 moves it down by less than 2^-8 of itself, so |v / s| stays
+// under 127 (1 + 2^-8) < 127.5 and no clamp is needed; adding 1.5 * 2^23 rounds to
+// an integer (ties to even) whose low byte is the code.
 __device__ __forceinline__ uint16_t code32(const uint32_t (&v)[32], uint32_t (&codes)[8]) {
   uint32_t m = 0;
 #pragma unroll
