@@ -297,7 +297,9 @@ __device__ __forceinline__ void window_tokens(const BalanceArgs& a, const Chunk&
     float p[kE], f[kE], total = 0.f, dot = 0.f;
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
-      p[e] = __expf(l[j][e] - top);  // a few ulp, as the logarithm and quotient below
+      // within 2 + 1.2 |l - top| ulp, the logarithm and quotient below within 3 (expf and
+      // logf, within 2 and 1, spill here: 47 against 39 us a call at 2^20 tokens)
+      p[e] = __expf(l[j][e] - top);
       total += p[e];
       f[e] = __int_as_float(sh.hist[seq[j]][e]);
     }
