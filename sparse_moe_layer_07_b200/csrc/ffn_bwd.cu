@@ -23,7 +23,10 @@
 // C8 variants (8-bit checkpoints): kDH decodes G and U from codes and bf16
 // scales (2.1 bytes a value pair where bf16 G, U and H are 6), forms H again
 // and writes hw = bf16(w * H), so that dW_down = hw^T dout takes dout as it is
-// and the product w * dout is rounded nowhere; kWG writes bf16.  Measured
+// and the product w * dout is rounded nowhere; kWG writes bf16.  dG, dU and hw are
+// rounded to bf16 in both pairs: the widest operands at this MMA rate (tf32 has
+// half of it and twice the bytes).  A gradient is off by 0.0024 in the mean square
+// for it, where its own rounding to bf16 alone makes 0.0017.  Measured
 // (kDH / kDX / one kWG): T 2048, d 1536, f 8192 119 / 202 / 108 us, where the
 // products alone at the measured matrix rate are 63 / 126 / 63 and the operand
 // tiles arrive from L2 at 11 to 12 TB/s; T 8192, d 6144, f 32768 5.3 / 10.9 / 5.5
