@@ -20,8 +20,8 @@
 //     names a slot of its own for the pair's counts;
 //   more: cleared totals per sequence, a kernel that adds the chunks' counts to
 //     them, a kernel for the rest.
-// Measured: 3.4 us for 32 tokens, 10.2 us for 16384 (64 sequences), 1.5 + 11.8 +
-// 24.1 us for 2^20 (1000 sequences), of which 11.7 us are its 76 MB at the copy
+// Measured: 3.7 us for 32 tokens, 10.3 us for 16384 (64 sequences), 1.6 + 11.8 +
+// 25.0 us for 2^20 (1000 sequences), of which 11.7 us are its 76 MB at the copy
 // rate: there a chunk's chain, three blocks an SM and three rounds, bounds it.
 // Counts are integers, so no order matters; the float sums run in a fixed order
 // (thread, warp, chunk), so results do not depend on scheduling.

@@ -27,7 +27,7 @@
 // rounded to bf16 in both pairs: the widest operands at this MMA rate (tf32 has
 // half of it and twice the bytes).  A gradient is off by 0.0024 in the mean square
 // for it, where its own rounding to bf16 alone makes 0.0017.  Measured
-// (kDH / kDX / one kWG): T 2048, d 1536, f 8192 119 / 202 / 108 us, where the
+// (kDH / kDX / one of kWG's products): T 2048, d 1536, f 8192 119 / 202 / 105 us, where the
 // products alone at the measured matrix rate are 63 / 126 / 63 and the operand
 // tiles arrive from L2 at 11 to 12 TB/s; T 8192, d 6144, f 32768 5.3 / 10.9 / 5.5
 // ms against 4.8 / 9.6 / 4.8 at the rate under the power limit.

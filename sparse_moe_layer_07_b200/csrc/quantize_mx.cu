@@ -3,8 +3,9 @@
 // quantize: w [E, K, N] bf16 (N contiguous) -> codes [E, N, K / 2] (K
 // contiguous: the 4-bit operand of the block-scaled MMA has to be K-major) and
 // scales in blocks of 128 channels x 128 K.  Bound by memory (2 + 0.53 bytes a
-// weight): 6.35 TB/s for [8, 32768, 6144] (640 us), and 6.0 TB/s back (684 us;
-// blocks that run along K instead of N took 749 us).  A block of 256 threads
+// weight): 6.3 TB/s for [8, 32768, 6144] (640 to 646 us), and 5.8 to 6.0 TB/s back
+// (684 to 700 us; blocks that run along K instead of N took 749 us); on a box with
+// slower DRAM the two take 1373 us together.  A block of 256 threads
 // takes 128 K x 128 channels: a thread reads one 32-block of two channels (rows
 // of 256 bytes across the block), so the largest magnitude needs no exchange,
 // and the codes turn through shared memory into 64-byte runs.
