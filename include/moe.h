@@ -540,7 +540,8 @@ MOE_API moe_status_t moe_expert_utilization(const int32_t* stats, int32_t E, int
  * +inf makes loss and its own dlogits row NaN; -inf logits are experts of
  * probability 0.
  * All in fp32 but the sum of the losses over chunks of 1024 tokens, in double;
- * p[t, e] is within 2^-24 (13.4 R + 20) of itself for logits up to R in magnitude.
+ * p[t, e] is within 2^-24 (13.4 R + 20) of itself, or of 2^-126 where it is less,
+ * for logits up to R in magnitude.
  * logits [T, E] fp32, topk_idx [T, 2] as moe_router_topk writes them;
  * token_mask [T] bytes or NULL (all live); seq_offsets [n_seq + 1] int32,
  * non-decreasing within [0, T] (empty sequences allowed, tokens before the
